@@ -53,10 +53,10 @@ typedef enum {
     PA_ERR_SHAPE = 2,           /* shapes disagree with each other or with the plan       */
     PA_ERR_DTYPE = 3,           /* dtype not F32/F16/BF16                                 */
     PA_ERR_RANGE = 4,           /* index out of range: page id, position, u32 overflow    */
-    PA_ERR_WRITE_CONFLICT = 5,  /* two queries of one plan write the same cache slot      */
+    PA_ERR_WRITE_CONFLICT = 5,  /* two writers of one cache slot, page or total           */
     PA_ERR_WORKSPACE = 6,       /* workspace missing, too small or over the limit         */
     PA_ERR_SPLITS = 7,          /* split count outside 1..PA_MAX_SPLITS                   */
-    PA_ERR_LIMIT = 8,           /* head dim > 1024, position dim > 256, grid limits       */
+    PA_ERR_LIMIT = 8,           /* head dim > 1024, position dim > 256, grid limits, host memory */
     PA_ERR_CUDA = 9,            /* a CUDA runtime call or kernel launch failed            */
     PA_ERR_STATE = 10           /* plan not uploaded                                      */
 } pa_status;
@@ -343,6 +343,104 @@ pa_status paged_attn_forward_split_static(const pa_plan *plan, const void *q, co
                                           int32_t num_kv_heads, int32_t head_dim, int32_t value_dim,
                                           float scale, int32_t causal, int32_t window, pa_dtype dtype,
                                           int32_t splits, pa_stream_t stream);
+
+/*
+ * Per-head RMS norm of the step's queries and keys, the rotation by position,
+ * and the append of keys and values, in one pass.  For every query row of the
+ * plan and every head row x of q and new_k (fp32 arithmetic, one rounding):
+ *   y = x / sqrt(mean(x^2) + eps) * weight          (weight NULL: y = x)
+ * and, with a rope table, the pairs (a, b) of the first rope_dim elements of y,
+ * (y[i], y[i + rope_dim/2]) or, interleaved, (y[2i], y[2i+1]), become
+ * (a cos_i - b sin_i, b cos_i + a sin_i).  Queries go to q_out, keys and the
+ * unchanged values to the caches at the plan's slots (as paged_kv_store).
+ *
+ *   q       [queries, num_heads, head_dim]      rows `q_stride` elements apart
+ *   new_k   [queries, num_kv_heads, head_dim]   rows `k_stride` apart
+ *   new_v   [queries, num_kv_heads, value_dim]  rows `v_stride` apart (three views of
+ *                                               one projection output, say)
+ *   q_out   [queries, num_heads, head_dim]      dense; may be q itself when that is dense
+ *   rope_table [max_positions, rope_dim] fp32: rope_dim/2 cosines, then as many sines
+ *           (rope_dim even, 2..head_dim); NULL: no rotation
+ *   positions [queries] int32, or NULL: the plan's positions.  They differ once an
+ *           eviction has moved the keys: the rotation goes by the place in the text,
+ *           the slot by the place in the cache.
+ *   q_weight, k_weight [head_dim] in the operand dtype, each may be NULL
+ *   key_mass [pages, num_kv_heads, page_size] fp32 or NULL: the written keys' totals
+ *           are set to 0 (paged_attn_forward_mass)
+ *
+ * Except for q_out == q, the written tensors overlap no input.  A position the
+ * table has no row for sets PA_DEVICE_RANGE in the status word and leaves that
+ * query's rows (q_out and caches) as they were.  Zero queries: PA_OK, no launch.
+ */
+pa_status paged_qk_norm_rope_store(const pa_plan *plan, const void *q, int64_t q_stride, const void *new_k,
+                                   int64_t k_stride, const void *new_v, int64_t v_stride, void *q_out, void *k_cache,
+                                   void *v_cache, float *key_mass, const float *rope_table, int32_t max_positions,
+                                   int32_t rope_dim, int32_t interleaved, const int32_t *positions, const void *q_weight,
+                                   const void *k_weight, float eps, int32_t num_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t value_dim, pa_dtype dtype, pa_stream_t stream);
+
+/*
+ * Workspace bytes for paged_attn_forward_mass: the split partials and
+ * log-sum-exp values, the score rows of the decode items (fp32 [decode items,
+ * num_heads, keys]) and the work lists.  `keys` is the longest history of the
+ * plan's decode items, or max_keys when that is more, at most `window` when
+ * window > 0 (pass 0 for a call that is not causal).  A larger max_keys lets a
+ * captured decode loop (pa_plan_advance, staged plans) grow past the histories
+ * it was captured with.  0 for invalid arguments.
+ */
+size_t pa_mass_workspace_bytes(const pa_plan *plan, int32_t num_heads, int32_t num_kv_heads, int32_t value_dim,
+                               int32_t splits, int32_t window, int64_t max_keys);
+
+/*
+ * paged_attn_forward_split that also adds up what each cached key was used for:
+ *   key_mass[page, kv, row] += sum over the plan's queries of the page's sequence
+ *                              and the query heads of group kv of softmax_j
+ * for every key j that a query sees (fp32 [pages, num_kv_heads, page_size], the
+ * head before the row).  Each key's terms are added in a fixed order by one owner,
+ * so repeated runs give the same bits; for that no page may be held by two used
+ * block-table entries (PA_ERR_WRITE_CONFLICT).  Slots no query sees are left as
+ * they were.  The totals say which keys paged_kv_evict keeps.
+ *
+ * workspace: >= pa_mass_workspace_bytes(plan, ...), 16-byte aligned, not shared
+ * by calls that may overlap; what it has beyond the need makes the score rows
+ * longer.  A decode item that sees more keys than its score row holds (only on
+ * graph replays) still gets its output, but adds nothing to the totals and sets
+ * PA_DEVICE_RANGE.  A captured call stays valid for plan images with the same
+ * counts whose sequences have one decode item each (or several, when captured so)
+ * and share no pages.  splits in 1..PA_MAX_SPLITS; other arguments, shapes and
+ * checks as paged_attn_forward.
+ */
+pa_status paged_attn_forward_mass(const pa_plan *plan, const void *q, const void *k_cache, const void *v_cache, void *out,
+                                  float *key_mass, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                  int32_t value_dim, float scale, int32_t causal, int32_t window, pa_dtype dtype,
+                                  void *workspace, size_t workspace_bytes, int32_t splits, pa_stream_t stream);
+
+/*
+ * Eviction: every sequence of `plan` shrinks to the length it has in
+ * `kept_plan` (a plan over the same sequences, page size and pool; its queries,
+ * if any, do not matter here).  Per sequence and KV head the first `sink` and the
+ * last `recent` keys stay, and of the others those with the largest key_mass
+ * (equal totals: the lower index; NaN below every number).  The kept keys keep
+ * their order and move, with their values and totals, to rows 0, 1, ... of the
+ * kept schedule.
+ *
+ *   kept [sequences, num_kv_heads, kept_stride] int32: the kept keys' former
+ *        indices, ascending, then -1 (kept_stride >= the longest kept history)
+ *
+ * kept_plan's block table names, entry by entry, either the source's own page
+ * (in place) or a page that no used entry of the source schedule names.  A page
+ * that rows move into has one holder (PA_ERR_WRITE_CONFLICT); pages that lie
+ * within the sink and stay in place may be shared by several sequences.  A
+ * sequence with equal lengths keeps every key (and is copied where the pages
+ * differ); otherwise its budget is at least sink + recent (PA_ERR_SHAPE).  Rows past
+ * a kept length are left as they were.  Lengths are read from the plans' device
+ * copies: a source advanced by graph replays is evicted at its true length.  The
+ * next step's plan is built from the kept lengths; rotated positions no longer
+ * equal cache rows then (see `positions` above).
+ */
+pa_status paged_kv_evict(const pa_plan *plan, const pa_plan *kept_plan, float *key_mass, void *k_cache, void *v_cache,
+                         int32_t *kept, int32_t kept_stride, int32_t sink, int32_t recent, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t value_dim, pa_dtype dtype, pa_stream_t stream);
 
 /*
  * Profiling hook: the next attention call made on this thread records

@@ -32,7 +32,8 @@ EXPORTED = ["pa_last_error", "pa_status_string", "pa_abi_version", "paged_attn_p
             "pa_workspace_bytes", "paged_attn_split_heuristic", "paged_mla_split_heuristic",
             "paged_attn_decode_sms_beside_prefill", "paged_kv_store", "paged_attn_forward",
             "paged_attn_forward_split", "paged_mla_forward", "pa_plan_advance", "pa_time_next_kernel",
-            "pa_device_status"]
+            "pa_device_status", "paged_qk_norm_rope_store", "pa_mass_workspace_bytes", "paged_attn_forward_mass",
+            "paged_kv_evict"]
 
 
 class PagedAttentionError(RuntimeError):
@@ -95,6 +96,16 @@ def load() -> ctypes.CDLL:
     lib.paged_mla_forward.restype = ctypes.c_int
     lib.pa_plan_advance.argtypes = [vp, vp]
     lib.pa_plan_advance.restype = ctypes.c_int
+    lib.paged_qk_norm_rope_store.argtypes = [vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, i32, i32, i32, vp,
+                                             vp, vp, ctypes.c_float, i32, i32, i32, i32, ctypes.c_int, vp]
+    lib.paged_qk_norm_rope_store.restype = ctypes.c_int
+    lib.pa_mass_workspace_bytes.argtypes = [vp, i32, i32, i32, i32, i32, i64]
+    lib.pa_mass_workspace_bytes.restype = sz
+    lib.paged_attn_forward_mass.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, ctypes.c_float, i32, i32,
+                                            ctypes.c_int, vp, sz, i32, vp]
+    lib.paged_attn_forward_mass.restype = ctypes.c_int
+    lib.paged_kv_evict.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, ctypes.c_int, vp]
+    lib.paged_kv_evict.restype = ctypes.c_int
     lib.pa_time_next_kernel.argtypes = [vp, vp]
     lib.pa_time_next_kernel.restype = ctypes.c_int
     lib.pa_device_status.argtypes = [ctypes.POINTER(i32), i32]
@@ -125,6 +136,7 @@ class Plan:
         self._handle = ctypes.c_void_p(handle)
         self.queries, self.sequences, self.width, self.page_size, self.pages = (int(x) for x in counts[:5])
         self.n_decode, self.n_tiles, self.n_tile_queries = (int(x) for x in counts[5:8])
+        self.longest = 0    # keys of the longest sequence the plan was built with
         self.words = None
         self.device = None
 
@@ -193,6 +205,7 @@ def paged_attn_plan(seq_lens, block_table, query_seq, query_pos, page_size: int,
     counts = (ctypes.c_int64 * 8)()
     _check(lib.pa_plan_describe(handle, counts))
     plan = Plan(handle.value, np.array(counts[:], dtype=np.int64))
+    plan.longest = int(seq_lens.max()) if len(seq_lens) else 0
     if upload:
         plan.upload(device)
     return plan
@@ -213,7 +226,9 @@ def _tensor(t: torch.Tensor, name: str, dtype, device, rank: int) -> None:
 
 def _storage_span(t: torch.Tensor):
     start = t.data_ptr()
-    return start, start + t.numel() * t.element_size()
+    if t.is_contiguous():
+        return start, start + t.numel() * t.element_size()
+    return start, start + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
 
 
 def _check_disjoint(out: torch.Tensor, *inputs) -> None:
@@ -373,6 +388,167 @@ def paged_mla_forward(plan: Plan, q, qp, latent_cache, pos_cache, scale: float, 
                                     float(scale), 1 if causal else 0, int(window), _DTYPES[dt], ws_ptr, ws_bytes,
                                     int(splits), _stream(dev)))
     return out
+
+
+def _key_mass(t, plan: Plan, heads: int, device) -> None:
+    _tensor(t, "key_mass", torch.float32, device, 3)
+    if tuple(t.shape) != (plan.pages, heads, plan.page_size):
+        raise ValueError("key_mass must be [pages, kv_heads, page_size]")
+
+
+def _rows(t, name: str, dtype, device, queries: int, dim: int) -> int:
+    """A [queries, heads, dim] operand whose rows may lie apart; returns the row stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have rank 3")
+    if t.shape[0] != queries or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [queries, heads, {dim}] matching the plan and cache")
+    sq, sh, sd = t.stride()
+    if (dim > 1 and sd != 1) or (t.shape[1] > 1 and sh != dim):
+        raise ValueError(f"{name}: each row's heads must be contiguous")
+    return sq if queries > 1 else t.shape[1] * dim
+
+
+def paged_qk_norm_rope_store(plan: Plan, q, new_k, new_v, k_cache, v_cache, rope_table=None, q_weight=None,
+                             k_weight=None, eps: float = 1e-6, interleaved: bool = False, positions=None,
+                             key_mass=None, q_out=None):
+    """RMS-norm and rotate q [Q, Hq, d] and new_k [Q, Hkv, d] per head, append new_k and new_v [Q, Hkv, dv].
+
+    q, new_k and new_v may be views whose rows lie apart (slices of one projection output).  rope_table is
+    fp32 [max_positions, rope_dim], cosines then sines; `positions` (int32 [Q]) replaces the plan's positions for
+    the rotation; key_mass, when given, is zeroed at the written keys.  Returns the queries, dense (`q_out` may be
+    a dense q itself)."""
+    dev, dt = k_cache.device, k_cache.dtype
+    if dt not in _DTYPES:
+        raise TypeError("dtype must be float32, float16 or bfloat16")
+    _tensor(k_cache, "k_cache", dt, dev, 4)
+    _tensor(v_cache, "v_cache", dt, dev, 4)
+    _plan_ready(plan, dev)
+    pages, ps, hkv, d = k_cache.shape
+    dv, n = v_cache.shape[3], plan.queries
+    if tuple(v_cache.shape[:3]) != (pages, ps, hkv) or pages != plan.pages or ps != plan.page_size:
+        raise ValueError("cache shapes do not match the plan")
+    q_stride = _rows(q, "q", dt, dev, n, d)
+    k_stride = _rows(new_k, "new_k", dt, dev, n, d)
+    v_stride = _rows(new_v, "new_v", dt, dev, n, dv)
+    hq = q.shape[1]
+    if new_k.shape[1] != hkv or new_v.shape[1] != hkv:
+        raise ValueError("new rows must be [queries, kv_heads, d|dv]")
+    table_ptr = pos_ptr = mass_ptr = qw_ptr = kw_ptr = None
+    far = rot = 0
+    if rope_table is not None:
+        _tensor(rope_table, "rope_table", torch.float32, dev, 2)
+        far, rot = rope_table.shape
+        if far == 0 or rot == 0:        # an empty tensor's null pointer would read as "no table"
+            raise ValueError("the rope table is empty")
+        table_ptr = rope_table.data_ptr()
+    if positions is not None:
+        _tensor(positions, "positions", torch.int32, dev, 1)
+        if positions.shape[0] != n:
+            raise ValueError("positions must be [queries]")
+        pos_ptr = positions.data_ptr()
+    if q_weight is not None:
+        _tensor(q_weight, "q_weight", dt, dev, 1)
+        qw_ptr = q_weight.data_ptr()
+    if k_weight is not None:
+        _tensor(k_weight, "k_weight", dt, dev, 1)
+        kw_ptr = k_weight.data_ptr()
+    for w in (q_weight, k_weight):
+        if w is not None and w.shape[0] != d:
+            raise ValueError("norm weights must be [head_dim]")
+    if key_mass is not None:
+        _key_mass(key_mass, plan, hkv, dev)
+        mass_ptr = key_mass.data_ptr()
+    if q_out is None:
+        q_out = torch.empty((n, hq, d), dtype=dt, device=dev)
+    else:
+        _tensor(q_out, "q_out", dt, dev, 3)
+        if tuple(q_out.shape) != (n, hq, d):
+            raise ValueError(f"q_out must have shape {(n, hq, d)}")
+        if not (q_out.data_ptr() == q.data_ptr() and q.is_contiguous()):
+            _check_disjoint(q_out, q)
+        _check_disjoint(q_out, new_k, new_v, k_cache, v_cache, rope_table, positions, q_weight, k_weight, key_mass)
+    for t in (k_cache, v_cache):
+        _check_disjoint(t, q, new_k, new_v, rope_table, positions, q_weight, k_weight, key_mass)
+    _check_disjoint(k_cache, v_cache)
+    if key_mass is not None:
+        _check_disjoint(key_mass, q, new_k, new_v, rope_table, positions, q_weight, k_weight)
+    _check(load().paged_qk_norm_rope_store(
+        plan.handle, q.data_ptr(), q_stride, new_k.data_ptr(), k_stride, new_v.data_ptr(), v_stride, q_out.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), mass_ptr, table_ptr, far, rot, 1 if interleaved else 0, pos_ptr, qw_ptr,
+        kw_ptr, float(eps), hq, hkv, d, dv, _DTYPES[dt], _stream(dev)))
+    return q_out
+
+
+def mass_workspace_bytes(plan: Plan, heads: int, kv_heads: int, value_dim: int, splits: int, window: int = 0,
+                         max_keys: int = 0) -> int:
+    return int(load().pa_mass_workspace_bytes(plan.handle, int(heads), int(kv_heads), int(value_dim), int(splits),
+                                              int(window), int(max_keys)))
+
+
+def make_mass_workspace(plan: Plan, heads: int, kv_heads: int, value_dim: int, splits: int, window: int = 0,
+                        max_keys: int = 0, device=None) -> torch.Tensor:
+    """Caller-owned workspace of paged_attn_forward_mass (window: 0 for calls that are not causal; max_keys: room
+    for the histories a captured decode loop will reach)."""
+    n = mass_workspace_bytes(plan, heads, kv_heads, value_dim, splits, window, max_keys)
+    return torch.empty((n + 3) // 4, dtype=torch.float32, device=device or plan.device)
+
+
+def paged_attn_forward_mass(plan: Plan, q, k_cache, v_cache, key_mass, scale: float, splits: int | None = None,
+                            workspace=None, causal: bool = True, out=None, window: int = 0):
+    """Paged attention that adds each key's softmax weights, over the plan's queries and a KV head's query heads, to
+    key_mass [pages, kv_heads, page_size] (fp32).  splits defaults to the split heuristic; the workspace is allocated
+    here when not given (make_mass_workspace)."""
+    out = _attn_common(plan, q, k_cache, v_cache, out)
+    hq, hkv, dv = q.shape[1], k_cache.shape[2], v_cache.shape[3]
+    _key_mass(key_mass, plan, hkv, q.device)
+    if splits is None:
+        splits = paged_attn_split_heuristic(plan, hq, hkv, window=window)
+    if workspace is None:
+        workspace = make_mass_workspace(plan, hq, hkv, dv, splits, window if causal else 0, device=q.device)
+    _check_disjoint(out, workspace, key_mass)
+    _check_disjoint(key_mass, q, k_cache, v_cache, workspace)
+    _check_disjoint(workspace, q, k_cache, v_cache)
+    _check(load().paged_attn_forward_mass(
+        plan.handle, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), key_mass.data_ptr(), hq, hkv,
+        q.shape[2], dv, float(scale), 1 if causal else 0, int(window), _DTYPES[q.dtype], workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), int(splits), _stream(q.device)))
+    return out
+
+
+def paged_kv_evict(plan: Plan, kept_plan: Plan, key_mass, k_cache, v_cache, sink: int = 0, recent: int = 0, kept=None):
+    """Shrink every sequence of `plan` to its length in `kept_plan`: the first `sink`, the last `recent` and, between
+    them, the keys with the largest key_mass stay and move to the kept schedule's rows.  Returns the kept keys' former
+    indices, int32 [sequences, kv_heads, longest kept history], -1 past a sequence's kept length."""
+    dev, dt = k_cache.device, k_cache.dtype
+    if dt not in _DTYPES:
+        raise TypeError("dtype must be float32, float16 or bfloat16")
+    _tensor(k_cache, "k_cache", dt, dev, 4)
+    _tensor(v_cache, "v_cache", dt, dev, 4)
+    _plan_ready(plan, dev)
+    _plan_ready(kept_plan, dev)
+    pages, ps, hkv, d = k_cache.shape
+    if tuple(v_cache.shape[:3]) != (pages, ps, hkv) or pages != plan.pages or ps != plan.page_size:
+        raise ValueError("cache shapes do not match the plan")
+    _key_mass(key_mass, plan, hkv, dev)
+    if kept is None:
+        kept = torch.empty((plan.sequences, hkv, kept_plan.longest), dtype=torch.int32, device=dev)
+    else:
+        _tensor(kept, "kept", torch.int32, dev, 3)
+        if tuple(kept.shape[:2]) != (plan.sequences, hkv):
+            raise ValueError("kept must be [sequences, kv_heads, n]")
+    _check_disjoint(kept, key_mass, k_cache, v_cache)
+    _check_disjoint(k_cache, v_cache, key_mass)
+    _check_disjoint(v_cache, key_mass)
+    _check(load().paged_kv_evict(plan.handle, kept_plan.handle, key_mass.data_ptr(), k_cache.data_ptr(),
+                                 v_cache.data_ptr(), kept.data_ptr(), kept.shape[2], int(sink), int(recent), hkv, d,
+                                 v_cache.shape[3], _DTYPES[dt], _stream(dev)))
+    return kept
 
 
 def paged_attn_plan_advance(plan: Plan) -> None:

@@ -1,0 +1,266 @@
+// Entry points around the attention of a bounded cache: norm + rotation +
+// append, attention with per-key weight totals, and eviction.  Argument checks
+// on the host first, then launches only, as for every call of the library.
+
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+#include <new>
+#include <vector>
+
+#include "plan_host.h"
+
+namespace pa {
+
+namespace {
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Longest history (in keys) any query of the plan's host copy may see.
+int64_t longest_tile_seq(const pa_plan *plan) {
+    const int32_t *w = plan->words.data();
+    int32_t longest = 0;
+    for (int32_t t = 0; t < plan->n_tiles; ++t)
+        longest = std::max(longest, w[plan->off_seqlen + w[plan->off_tiles + 4 * (size_t)t]]);
+    return longest;
+}
+
+}  // namespace
+
+MassLayout mass_layout(const pa_plan *plan, int32_t hq, int32_t dv, int32_t splits, int32_t window, int64_t max_keys) {
+    MassLayout l{};
+    const size_t rows = (size_t)plan->queries * hq;
+    const size_t part = splits > 1 ? align256((size_t)splits * rows * dv * sizeof(float)) : 0;
+    l.lse = part;
+    l.lse_final = l.lse + align256((size_t)splits * rows * sizeof(float));
+    l.groups = l.lse_final + (splits > 1 && plan->n_tiles > 0 ? align256(rows * sizeof(float)) : 0);
+    l.scores = l.groups + align256(((size_t)plan->sequences + 1 + plan->queries) * sizeof(int32_t));
+    int64_t keys = std::max<int64_t>(max_keys, plan->max_seq_len);
+    if (window > 0) keys = std::min<int64_t>(keys, window);
+    l.cap = plan->n_decode > 0 ? (keys + 31) / 32 * 32 : 0;
+    l.bytes = l.scores + align256((size_t)plan->n_decode * hq * (size_t)l.cap * sizeof(float));
+    return l;
+}
+
+cudaError_t add_mass(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass,
+                     cudaStream_t st) {
+    MassArgs m{};
+    m.plan = a.plan;
+    m.q = a.q; m.k = a.k;
+    m.key_mass = key_mass;
+    m.lse = a.ws_lse;
+    m.lse_final = a.splits > 1 ? reinterpret_cast<float *>(ws + lay.lse_final) : a.ws_lse;
+    m.scores = a.scores;
+    m.cap = a.score_cap;
+    m.group_start = reinterpret_cast<int32_t *>(ws + lay.groups);
+    m.group_list = m.group_start + plan->sequences + 1;
+    m.hq = a.hq; m.hkv = a.hkv; m.d = a.d;
+    m.splits = a.splits; m.causal = a.causal; m.window = a.window;
+    m.scale = a.scale;
+    m.dtype = a.dtype;
+    m.status = a.status;
+    cudaError_t e = cudaSuccess;
+    if (a.scores) {
+        const bool repeated = (plan_facts(plan) & kFactRepeatedItems) != 0;
+        m.longest = (int32_t)plan->max_seq_len;
+        if (repeated) e = launch_mass_index(m, kMassItems, st);
+        if (e == cudaSuccess) e = launch_mass_items(m, repeated, st);
+    }
+    if (e == cudaSuccess && plan->n_tiles > 0) {
+        // prefill tiles on the tensor-core kernel; otherwise every query of the plan
+        const MassRecords kind = prefill_supported(a) ? kMassTiles : kMassQueries;
+        m.longest = (int32_t)std::max<int64_t>(longest_tile_seq(plan), kind == kMassQueries ? plan->max_seq_len : 0);
+        e = launch_mass_index(m, kind, st);
+        if (e == cudaSuccess && a.splits > 1) e = launch_lse_final(m, reinterpret_cast<float *>(ws + lay.lse_final), st);
+        if (e == cudaSuccess) e = launch_mass_recompute(m, kind, st);
+    }
+    return e;
+}
+
+}  // namespace pa
+
+using pa::fail;
+
+extern "C" {
+
+size_t pa_mass_workspace_bytes(const pa_plan *plan, int32_t num_heads, int32_t num_kv_heads, int32_t value_dim,
+                               int32_t splits, int32_t window, int64_t max_keys) {
+    if (!plan || num_heads < 1 || num_heads > 65535 || num_kv_heads < 1 || num_heads % num_kv_heads || value_dim < 1 ||
+        value_dim > PA_MAX_HEAD_DIM || splits < 1 || splits > PA_MAX_SPLITS || window < 0 || max_keys < 0 ||
+        max_keys > INT32_MAX)
+        return 0;
+    return pa::mass_layout(plan, num_heads, value_dim, splits, window, max_keys).bytes;
+}
+
+pa_status paged_attn_forward_mass(const pa_plan *plan, const void *q, const void *k_cache, const void *v_cache, void *out,
+                                  float *key_mass, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                  int32_t value_dim, float scale, int32_t causal, int32_t window, pa_dtype dtype,
+                                  void *workspace, size_t workspace_bytes, int32_t splits, pa_stream_t stream) {
+    static const char kName[] = "paged_attn_forward_mass";
+    pa_status st = pa::check_attention_args(plan, num_heads, num_kv_heads, head_dim, value_dim, 0, scale, causal, window,
+                                            dtype, false, kName);
+    if (st != PA_OK) return st;
+    if (!key_mass) return fail(PA_ERR_ARG, "paged_attn_forward_mass: key_mass is null");
+    if (reinterpret_cast<uintptr_t>(key_mass) % sizeof(float))
+        return fail(PA_ERR_ARG, "paged_attn_forward_mass: key_mass not 4-byte aligned");
+    try {
+        if (pa::plan_facts(plan) & pa::kFactSharedPages)
+            return fail(PA_ERR_WRITE_CONFLICT, "paged_attn_forward_mass: two sequences hold one page, its totals would have two owners");
+        return pa::attention_with_mass(plan, q, k_cache, v_cache, out, key_mass, num_heads, num_kv_heads, head_dim,
+                                       value_dim, scale, causal, window, dtype, workspace, workspace_bytes, splits,
+                                       (cudaStream_t)stream, kName);
+    } catch (const std::bad_alloc &) {
+        return fail(PA_ERR_LIMIT, "paged_attn_forward_mass: out of host memory");
+    }
+}
+
+pa_status paged_qk_norm_rope_store(const pa_plan *plan, const void *q, int64_t q_stride, const void *new_k,
+                                   int64_t k_stride, const void *new_v, int64_t v_stride, void *q_out, void *k_cache,
+                                   void *v_cache, float *key_mass, const float *rope_table, int32_t max_positions,
+                                   int32_t rope_dim, int32_t interleaved, const int32_t *positions, const void *q_weight,
+                                   const void *k_weight, float eps, int32_t num_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t value_dim, pa_dtype dtype, pa_stream_t stream) {
+#define BAD(status, what) return fail(status, "paged_qk_norm_rope_store: " what)
+    if (!plan) BAD(PA_ERR_ARG, "plan is null");
+    if (!pa::valid_dtype(dtype)) BAD(PA_ERR_DTYPE, "dtype must be F32, F16 or BF16");
+    if (num_heads < 1 || num_kv_heads < 1 || head_dim < 1 || value_dim < 1)
+        BAD(PA_ERR_SHAPE, "heads, head_dim and value_dim must be >= 1");
+    if (head_dim > PA_MAX_HEAD_DIM || value_dim > PA_MAX_HEAD_DIM) BAD(PA_ERR_LIMIT, "head dim above 1024");
+    if (num_heads > 65535 || num_kv_heads > 65535) BAD(PA_ERR_LIMIT, "num_heads above the launch grid limit");
+    if (interleaved != 0 && interleaved != 1) BAD(PA_ERR_ARG, "interleaved must be 0 or 1");
+    if (rope_table) {
+        if (rope_dim < 2 || rope_dim % 2 || rope_dim > head_dim) BAD(PA_ERR_SHAPE, "rope_dim must be even and in 2..head_dim");
+        if (max_positions < 1) BAD(PA_ERR_SHAPE, "the rope table has no rows");
+    } else if (positions) {
+        BAD(PA_ERR_ARG, "positions without a rope table");
+    }
+    if ((q_weight || k_weight) && (!std::isfinite(eps) || eps < 0.f)) BAD(PA_ERR_SHAPE, "eps must be finite and >= 0");
+    if (q_stride < 0 || k_stride < 0 || v_stride < 0) BAD(PA_ERR_SHAPE, "negative stride");
+    const int64_t most = (int64_t)1 << 40;
+    if ((int64_t)plan->pages * plan->page_size * num_kv_heads * std::max(head_dim, value_dim) > most ||
+        (int64_t)plan->queries * num_heads * head_dim > most ||
+        std::max(q_stride, std::max(k_stride, v_stride)) > most / std::max(plan->queries, 1))
+        BAD(PA_ERR_RANGE, "tensor too large");
+    if (plan->queries == 0) return PA_OK;
+    if (!plan->dev) BAD(PA_ERR_STATE, "plan not uploaded");
+    if (!q || !new_k || !new_v || !q_out || !k_cache || !v_cache) BAD(PA_ERR_ARG, "null tensor");
+    const void *ptrs[] = {q, new_k, new_v, q_out, k_cache, v_cache, key_mass, rope_table, positions, q_weight, k_weight};
+    const char *names[] = {"q", "new_k", "new_v", "q_out", "k_cache", "v_cache", "key_mass", "the rope table",
+                           "positions", "q_weight", "k_weight"};
+    pa_status on_dev = pa::operands_on_device(ptrs, names, 11, "paged_qk_norm_rope_store");
+    if (on_dev != PA_OK) return on_dev;
+    for (const void *p : {(const void *)key_mass, (const void *)rope_table, (const void *)positions})
+        if (reinterpret_cast<uintptr_t>(p) % 4) BAD(PA_ERR_ARG, "32-bit operand not 4-byte aligned");
+    for (const void *p : {q, new_k, new_v, (const void *)q_out, (const void *)k_cache, (const void *)v_cache, q_weight, k_weight})
+        if (reinterpret_cast<uintptr_t>(p) % pa::elem_bytes(dtype)) BAD(PA_ERR_ARG, "operand not aligned to its element");
+    pa::NormRopeArgs a{};
+    a.plan = pa::view_of(plan);
+    a.q = q; a.k = new_k; a.v = new_v;
+    a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+    a.q_out = q_out; a.k_cache = k_cache; a.v_cache = v_cache;
+    a.key_mass = key_mass;
+    a.table = rope_table;
+    a.positions = positions;
+    a.q_weight = q_weight; a.k_weight = k_weight;
+    a.eps = eps;
+    a.max_positions = max_positions;
+    a.rot = rope_table ? rope_dim : 0;
+    a.interleaved = interleaved;
+    a.hq = num_heads; a.hkv = num_kv_heads; a.d = head_dim; a.dv = value_dim;
+    a.dtype = dtype;
+    a.status = pa::device_status_ptr();
+    if (!a.status) BAD(PA_ERR_CUDA, "device status word unavailable");
+    cudaError_t e = pa::launch_norm_rope_store(a, (cudaStream_t)stream);
+    if (e != cudaSuccess) return pa::fail_cuda(e, "paged_qk_norm_rope_store launch");
+    return PA_OK;
+#undef BAD
+}
+
+pa_status paged_kv_evict(const pa_plan *plan, const pa_plan *kept_plan, float *key_mass, void *k_cache, void *v_cache,
+                         int32_t *kept, int32_t kept_stride, int32_t sink, int32_t recent, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t value_dim, pa_dtype dtype, pa_stream_t stream) {
+#define BAD(status, what) return fail(status, "paged_kv_evict: " what)
+    if (!plan || !kept_plan) BAD(PA_ERR_ARG, "plan is null");
+    if (!pa::valid_dtype(dtype)) BAD(PA_ERR_DTYPE, "dtype must be F32, F16 or BF16");
+    if (num_kv_heads < 1 || head_dim < 1 || value_dim < 1) BAD(PA_ERR_SHAPE, "heads, head_dim and value_dim must be >= 1");
+    if (head_dim > PA_MAX_HEAD_DIM || value_dim > PA_MAX_HEAD_DIM) BAD(PA_ERR_LIMIT, "head dim above 1024");
+    if (num_kv_heads > 65535) BAD(PA_ERR_LIMIT, "num_kv_heads above the launch grid limit");
+    if (sink < 0 || recent < 0) BAD(PA_ERR_ARG, "sink and recent must be >= 0");
+    if ((int64_t)sink + recent > INT32_MAX) BAD(PA_ERR_RANGE, "sink + recent too large");
+    if (plan->sequences != kept_plan->sequences || plan->page_size != kept_plan->page_size || plan->pages != kept_plan->pages)
+        BAD(PA_ERR_SHAPE, "the plans differ in sequences, page size or pool");
+    if ((int64_t)plan->pages * plan->page_size * num_kv_heads * std::max(head_dim, value_dim) > (int64_t)1 << 40)
+        BAD(PA_ERR_RANGE, "cache too large");
+    try {
+        const int32_t *w = plan->words.data(), *d = kept_plan->words.data();
+        const int32_t ps = plan->page_size;
+        int32_t longest = 0;
+        // Rows are written into a page that nothing else reads or writes: a page no
+        // used entry of the source schedule names, named once, or the sequence's own
+        // page of the same index, held by nobody else.  Pages inside the sink keep
+        // every row where it is and may be shared.
+        const bool src_shared = (pa::plan_facts(plan) & pa::kFactSharedPages) != 0;
+        const bool dst_shared = (pa::plan_facts(kept_plan) & pa::kFactSharedPages) != 0;
+        std::vector<int32_t> written, all;      // filled only when some page is shared
+        for (int32_t s = 0; s < plan->sequences; ++s) {
+            const int32_t n = w[plan->off_seqlen + s], m = d[kept_plan->off_seqlen + s];
+            if (m > n) BAD(PA_ERR_SHAPE, "a sequence would keep more keys than it has");
+            if (m < n && m < (int64_t)sink + recent) BAD(PA_ERR_SHAPE, "a sequence's budget is below sink + recent");
+            longest = std::max(longest, m);
+            const int32_t *from = w + plan->off_table + (size_t)s * plan->width;
+            const int32_t *to = d + kept_plan->off_table + (size_t)s * kept_plan->width;
+            const int64_t used = ((int64_t)n + ps - 1) / ps, kept_pages = ((int64_t)m + ps - 1) / ps;
+            for (int64_t g = 0; g < kept_pages; ++g) {
+                const bool fresh = to[g] != from[g];
+                if (fresh && (plan->held[(size_t)to[g] / 64] >> (to[g] % 64) & 1))
+                    BAD(PA_ERR_WRITE_CONFLICT, "the kept schedule writes a page that the source schedule reads");
+                if ((src_shared || dst_shared) && (fresh || (m < n && (g + 1) * ps > sink))) written.push_back(to[g]);
+            }
+            if (src_shared) all.insert(all.end(), from, from + used);
+        }
+        if (src_shared || dst_shared) {
+            std::sort(written.begin(), written.end());
+            if (std::adjacent_find(written.begin(), written.end()) != written.end())
+                BAD(PA_ERR_WRITE_CONFLICT, "two sequences of the kept schedule write one page");
+            std::sort(all.begin(), all.end());
+            for (int32_t pg : written) {
+                auto range = std::equal_range(all.begin(), all.end(), pg);
+                if (range.second - range.first > 1)
+                    BAD(PA_ERR_WRITE_CONFLICT, "the kept schedule writes a page that two sequences hold");
+            }
+        }
+        if (kept_stride < longest) BAD(PA_ERR_SHAPE, "kept has fewer columns than the longest kept history");
+    } catch (const std::bad_alloc &) {
+        BAD(PA_ERR_LIMIT, "out of host memory");
+    }
+    if (plan->sequences == 0 || kept_stride == 0) return PA_OK;
+    if (!plan->dev || !kept_plan->dev) BAD(PA_ERR_STATE, "plan not uploaded");
+    if (!key_mass || !k_cache || !v_cache || !kept) BAD(PA_ERR_ARG, "null tensor");
+    const void *ptrs[] = {key_mass, k_cache, v_cache, kept};
+    const char *names[] = {"key_mass", "k_cache", "v_cache", "kept"};
+    pa_status on_dev = pa::operands_on_device(ptrs, names, 4, "paged_kv_evict");
+    if (on_dev != PA_OK) return on_dev;
+    for (const void *p : {(const void *)key_mass, (const void *)kept})
+        if (reinterpret_cast<uintptr_t>(p) % 4) BAD(PA_ERR_ARG, "32-bit operand not 4-byte aligned");
+    for (const void *p : {(const void *)k_cache, (const void *)v_cache})
+        if (reinterpret_cast<uintptr_t>(p) % pa::elem_bytes(dtype)) BAD(PA_ERR_ARG, "operand not aligned to its element");
+    pa::EvictArgs a{};
+    a.src = pa::view_of(plan);
+    a.dst = pa::view_of(kept_plan);
+    a.key_mass = key_mass;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.kept = kept;
+    a.kept_stride = kept_stride;
+    a.sink = sink; a.recent = recent;
+    a.hkv = num_kv_heads; a.d = head_dim; a.dv = value_dim;
+    a.elem = pa::elem_bytes(dtype);
+    a.status = pa::device_status_ptr();
+    if (!a.status) BAD(PA_ERR_CUDA, "device status word unavailable");
+    cudaError_t e = pa::launch_evict(a, (cudaStream_t)stream);
+    if (e != cudaSuccess) return pa::fail_cuda(e, "paged_kv_evict launch");
+    return PA_OK;
+#undef BAD
+}
+
+}  // extern "C"

@@ -259,6 +259,8 @@ __global__ void __launch_bounds__(128) decode_fast_kernel(AttnArgs a, int use_li
         // Online softmax update, one warp per head.
         for (int g = warp; g < GH; g += 4) {
             const float s = lane < C::TK ? sp[lane * GH + g] : -INFINITY;
+            if (a.scores && lane < C::TK && tb + lane < j1 && tb + lane - lo < a.score_cap)
+                a.scores[((int64_t)item * a.hq + h0 + g) * a.score_cap + (tb + lane - lo)] = s;
             float mt = s;
 #pragma unroll
             for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
@@ -335,7 +337,7 @@ __global__ void __launch_bounds__(128) decode_fast_kernel(AttnArgs a, int use_li
             a.ws_o[((int64_t)split * rows + row) * D + c] = l > 0.f ? sum / l : 0.f;
         }
     }
-    if (a.splits > 1 && tid < GH) {
+    if (a.ws_lse && tid < GH) {
         const float l = l_sm[tid];
         const int64_t row = (int64_t)qi * a.hq + h0 + tid;
         a.ws_lse[(int64_t)split * rows + row] = l > 0.f ? (m_sm[tid] + log2f(l)) * kLn2 : -INFINITY;
@@ -417,6 +419,8 @@ __global__ void __launch_bounds__(128) decode_generic_kernel(AttnArgs a, int use
                 for (int e = 0; e < a.p; ++e) dot = fmaf(qpf[e], to_f<T>(kpr[e]), dot);
             }
             s = dot;
+            if (a.scores && j - lo < a.score_cap)
+                a.scores[((int64_t)item * a.hq + h) * a.score_cap + (j - lo)] = s;
         }
         const float mt = block_max128(s, scratch);
         const float nm = fmaxf(m, mt);
@@ -452,7 +456,7 @@ __global__ void __launch_bounds__(128) decode_generic_kernel(AttnArgs a, int use
                 a.ws_o[((int64_t)split * nrows + row) * a.dv + c] = l > 0.f ? acc[i] / l : 0.f;
         }
     }
-    if (a.splits > 1 && tid == 0)
+    if (a.ws_lse && tid == 0)
         a.ws_lse[(int64_t)split * nrows + row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 

@@ -118,7 +118,10 @@ __device__ __forceinline__ bool __syncthreads_and_softmax(bool pred) {
     return r != 0;
 }
 
-template <typename T, int CW>
+// kMass: for the per-key totals of paged_attn_forward_mass, also leave every
+// visible key's score (log2 domain, when a.scores is set) and, unsplit too, the
+// log-sum-exp in the workspace.
+template <typename T, int CW, bool kMass>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      AttnArgs a, int use_list, TcParams tp) {
@@ -141,8 +144,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const int items = use_list ? a.plan.n_decode : a.plan.queries;
     const int units = items * a.splits * a.hkv;
     struct Unit {
-        int kvh, split, qi, seq_len, n_kt;
-        int64_t j0, j1, jb;
+        int kvh, split, item, qi, seq_len, n_kt;
+        int64_t lo, j0, j1, jb;
         const int32_t *trow;
     };
     auto unit_at = [&](int u) -> Unit {
@@ -150,12 +153,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         x.kvh = u % a.hkv;
         const int rest = u / a.hkv;
         x.split = rest % a.splits;
-        const int item = rest / a.splits;
-        x.qi = use_list ? a.plan.decode[item] : item;
+        x.item = rest / a.splits;
+        x.qi = use_list ? a.plan.decode[x.item] : x.item;
         const int4 meta = a.plan.qmeta[x.qi];
         x.seq_len = a.plan.seq_lens[meta.x];
         int64_t lo, hi;
         visible_range(meta.y, x.seq_len, a.causal, a.window, lo, hi);
+        x.lo = lo;
         split_bounds(lo, hi, a.splits, x.split, ps, x.j0, x.j1);
         // Tiles start on a TMA box boundary (no box crosses a page); keys of the
         // first tile below j0 (window or split start) are masked.
@@ -361,6 +365,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     for (int c = 0; c < CW; ++c)
                         if (c0 + c >= valid || c0 + c < first) sc[c] = -INFINITY;
                 }
+                if constexpr (kMass) {
+                    // my columns of the head's score row: whole 16-byte pieces where the
+                    // tile is whole and the row's offset allows
+                    const int64_t at = kbase + c0 - x.lo;
+                    if (a.scores && h < G) {
+                        float *dst = a.scores + ((int64_t)x.item * a.hq + (int64_t)x.kvh * G + h) * a.score_cap + at;
+                        if (valid == kN && first == 0 && (at & 3) == 0 && at + CW <= a.score_cap) {
+#pragma unroll
+                            for (int c = 0; c < CW; c += 4)
+                                *reinterpret_cast<float4 *>(dst + c) =
+                                    make_float4(sc[c] * tp.scale_log2, sc[c + 1] * tp.scale_log2,
+                                                sc[c + 2] * tp.scale_log2, sc[c + 3] * tp.scale_log2);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < CW; ++c)
+                                if (c0 + c < valid && c0 + c >= first && at + c < a.score_cap)
+                                    dst[c] = sc[c] * tp.scale_log2;
+                        }
+                    }
+                }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int c = 0; c < CW; c += 8) {
@@ -475,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     L += mk == -INFINITY ? 0.f : exp2f(mk - M) * s.ml[2 * (k * R + h) + 1];
                 }
                 const float wk = (m_ref == -INFINITY || !(L > 0.f)) ? 0.f : exp2f(m_ref - M) / L;
-                if (copy == 0 && h < G && a.splits > 1)
+                if (copy == 0 && h < G && (kMass || a.splits > 1))
                     a.ws_lse[(int64_t)x.split * rows + orow0 + h] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
                 // one pass per 64 output columns; the scaled partials [C][G][64] fill the Q buffer
                 float *ob = reinterpret_cast<float *>(s.q[0]);
@@ -545,18 +569,18 @@ int log2_exact(int v) {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <typename T, int CW>
+template <typename T, int CW, bool kMass>
 cudaError_t launch_cw(const AttnArgs &a, int items, int use_list, const CUtensorMap &tk, const CUtensorMap &tv,
                       const TcParams &tp, cudaStream_t st) {
     // Persistent grid: as many CTAs as fit on the GPU at once (one per SM), or
     // fewer when the caller keeps SMs for a concurrent kernel.
     static int resident = 0;
     if (resident == 0) {
-        cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<T, CW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<T, CW, kMass>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)kSmemBytes);
         if (e != cudaSuccess) return e;
         int per_sm = 0, dev = 0, sms = 0;
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_tc_kernel<T, CW>, kThreads, kSmemBytes);
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_tc_kernel<T, CW, kMass>, kThreads, kSmemBytes);
         if (e != cudaSuccess) return e;
         e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
@@ -568,19 +592,26 @@ cudaError_t launch_cw(const AttnArgs &a, int items, int use_list, const CUtensor
     int64_t ctas = units < resident ? units : resident;
     if (a.max_ctas > 0 && a.max_ctas < ctas) ctas = a.max_ctas;
     const dim3 grid((unsigned)ctas);
-    cudaError_t e = launch_pdl(decode_tc_kernel<T, CW>, grid, dim3(kThreads), kSmemBytes, st, tk, tv, a, use_list, tp);
+    cudaError_t e = launch_pdl(decode_tc_kernel<T, CW, kMass>, grid, dim3(kThreads), kSmemBytes, st, tk, tv, a, use_list, tp);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 
 // Copies of the group in the 128 MMA rows: 4 for G <= 32, 2 for G <= 64, 1 above;
 // each copy's softmax covers 128 / copies columns of a tile.
+template <typename T, bool kMass>
+cudaError_t launch_s(const AttnArgs &a, int items, int use_list, const CUtensorMap &tk, const CUtensorMap &tv,
+                     const TcParams &tp, cudaStream_t st) {
+    if (tp.group <= 32) return launch_cw<T, 32, kMass>(a, items, use_list, tk, tv, tp, st);
+    if (tp.group <= 64) return launch_cw<T, 64, kMass>(a, items, use_list, tk, tv, tp, st);
+    return launch_cw<T, 128, kMass>(a, items, use_list, tk, tv, tp, st);
+}
+
 template <typename T>
 cudaError_t launch_t(const AttnArgs &a, int items, int use_list, const CUtensorMap &tk, const CUtensorMap &tv,
                      const TcParams &tp, cudaStream_t st) {
-    if (tp.group <= 32) return launch_cw<T, 32>(a, items, use_list, tk, tv, tp, st);
-    if (tp.group <= 64) return launch_cw<T, 64>(a, items, use_list, tk, tv, tp, st);
-    return launch_cw<T, 128>(a, items, use_list, tk, tv, tp, st);
+    return a.scores || (a.splits == 1 && a.ws_lse) ? launch_s<T, true>(a, items, use_list, tk, tv, tp, st)
+                    : launch_s<T, false>(a, items, use_list, tk, tv, tp, st);
 }
 
 }  // namespace

@@ -111,7 +111,10 @@ struct TmaParams {
     int box_rows;     // rows per TMA box (min(page_size, 16))
 };
 
-template <typename T, int D, int GH>
+// kMass: for the per-key totals of paged_attn_forward_mass, also leave every
+// visible key's score (log2 domain, when a.scores is set) and, unsplit too, the
+// log-sum-exp in the workspace.
+template <typename T, int D, int GH, bool kMass>
 __global__ void __launch_bounds__(128) decode_tma_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                          const __grid_constant__ CUtensorMap tm_v, AttnArgs a,
                                                          int use_list, TmaParams tp) {
@@ -260,7 +263,12 @@ __global__ void __launch_bounds__(128) decode_tma_kernel(const __grid_constant__
         for (int k = 0; k < HP; ++k) {
             const int g = 2 * k + (lane >> 4);
             const bool gv = g < GH;
-            const float s = (gv && t16 < valid && t16 >= first) ? sp[2 * C::TT * GH + t16 * GH + g] : -INFINITY;
+            const bool vis = gv && t16 < valid && t16 >= first;
+            const float s = vis ? sp[2 * C::TT * GH + t16 * GH + g] : -INFINITY;
+            if constexpr (kMass) {
+                if (a.scores && vis && jt + t16 - lo < a.score_cap)
+                    a.scores[((int64_t)item * a.hq + h0 + g) * a.score_cap + (jt + t16 - lo)] = s;
+            }
             float alpha = 1.f;
             if (__any_sync(0xffffffffu, s > m_ref[k] + kSlack)) {
                 float mt = s;
@@ -373,10 +381,11 @@ __global__ void __launch_bounds__(128) decode_tma_kernel(const __grid_constant__
             }
         }
         const int64_t row = (int64_t)qi * a.hq + h0 + g;
-        if (a.splits == 1) {
+        if (a.splits == 1)
             static_cast<T *>(a.out)[row * D + c] = from_f<T>(O / L);
-        } else {
+        else
             a.ws_o[((int64_t)split * rows + row) * D + c] = L > 0.f ? O / L : 0.f;
+        if (kMass || a.splits > 1) {
             if (c == 0) a.ws_lse[(int64_t)split * rows + row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
         }
     }
@@ -391,23 +400,31 @@ int log2_exact(int v) {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <typename T, int D, int GH>
-cudaError_t launch_t(const AttnArgs &a, int items, int use_list, const CUtensorMap &tk, const CUtensorMap &tv,
+template <typename T, int D, int GH, bool kMass>
+cudaError_t launch_s(const AttnArgs &a, int items, int use_list, const CUtensorMap &tk, const CUtensorMap &tv,
                      const TmaParams &tp, cudaStream_t st) {
     using C = Cfg<D, GH>;
     static bool configured = false;
     if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(decode_tma_kernel<T, D, GH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)C::SMEM);
+        cudaError_t e = cudaFuncSetAttribute(decode_tma_kernel<T, D, GH, kMass>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
         if (e != cudaSuccess) return e;
         configured = true;
     }
     TmaParams p = tp;
     p.groups = (a.hq / a.hkv) / GH;
     const dim3 grid((unsigned)((int64_t)items * a.splits * a.hkv * p.groups));
-    cudaError_t e = launch_pdl(decode_tma_kernel<T, D, GH>, grid, dim3(128), C::SMEM, st, tk, tv, a, use_list, p);
+    cudaError_t e =
+        launch_pdl(decode_tma_kernel<T, D, GH, kMass>, grid, dim3(128), C::SMEM, st, tk, tv, a, use_list, p);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
+}
+
+template <typename T, int D, int GH>
+cudaError_t launch_t(const AttnArgs &a, int items, int use_list, const CUtensorMap &tk, const CUtensorMap &tv,
+                     const TmaParams &tp, cudaStream_t st) {
+    return a.scores || (a.splits == 1 && a.ws_lse) ? launch_s<T, D, GH, true>(a, items, use_list, tk, tv, tp, st)
+                    : launch_s<T, D, GH, false>(a, items, use_list, tk, tv, tp, st);
 }
 
 template <typename T, int D>

@@ -1,0 +1,290 @@
+// Per-key totals of the softmax weights (paged_attn_forward_mass).
+//
+// For key j of a sequence and KV head kv the call adds
+//   sum over the sequence's queries q and the heads h of group kv of
+//   softmax_j = 2^(s_qhj - lse_qh)            (s and lse in log2 units)
+// to key_mass[page, kv, row].  The log-sum-exp is only known once a query's
+// whole history has been seen, so the attention kernels run first and this pass
+// follows:
+//  * decode items: the decode kernels leave their scores (4 bytes per key and
+//    head, against 2*(D+Dv)/G bytes of cache per key and head) in the workspace,
+//    and `mass_items_kernel` turns them into weights: the cache is read once;
+//  * prefill tiles: the scores are recomputed from K and Q, tile by tile.
+// Every key has one owner that adds its terms in a fixed order: no atomics, and
+// the same bits on every run.  Sequences do not share pages (checked on the
+// host).
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "pa_internal.h"
+
+namespace pa {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <typename T> __device__ __forceinline__ float to_f(T x);
+template <> __device__ __forceinline__ float to_f<float>(float x) { return x; }
+template <> __device__ __forceinline__ float to_f<__half>(__half x) { return __half2float(x); }
+template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// Log-sum-exp of a row over its splits, in log2 units.
+__device__ __forceinline__ float merged_lse2(const MassArgs &a, int64_t row) {
+    const int64_t rows = (int64_t)a.plan.queries * a.hq;
+    float m = -INFINITY;
+    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.lse[s * rows + row]);
+    if (a.splits == 1 || m == -INFINITY) return m * kLog2e;
+    float t = 0.f;
+    for (int s = 0; s < a.splits; ++s) t += exp2f((a.lse[s * rows + row] - m) * kLog2e);
+    return m * kLog2e + log2f(t);
+}
+
+__global__ void lse_final_kernel(MassArgs a, float *out) {
+    griddep_wait();
+    griddep_launch();
+    const int64_t row = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (row < (int64_t)a.plan.queries * a.hq) out[row] = merged_lse2(a, row) / kLog2e;
+}
+
+// ---------------------------------------------------------------- grouping --
+__device__ __forceinline__ int record_seq(const PlanView &p, int kind, int i) {
+    if (kind == kMassTiles) return p.tiles[i].x;
+    return p.qmeta[kind == kMassItems ? p.decode[i] : i].x;
+}
+
+constexpr int kIndexThreads = 1024;
+
+// One CTA: group_start[s] .. group_start[s+1] delimit the records of sequence s
+// in group_list, in ascending record order (a stable counting sort).
+__global__ void __launch_bounds__(kIndexThreads) mass_index_kernel(MassArgs a, int kind, int n) {
+    griddep_wait();
+    griddep_launch();
+    __shared__ int seqs[kIndexThreads];
+    __shared__ int carry, sums[32];
+    const int S = a.plan.sequences, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int s = tid; s <= S; s += kIndexThreads) a.group_start[s] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kIndexThreads) atomicAdd(&a.group_start[record_seq(a.plan, kind, i)], 1);
+    if (tid == 0) carry = 0;
+    __syncthreads();
+    // exclusive prefix sums of the counts, 1024 sequences a step; the entry of s
+    // then serves as the cursor of its records and ends at its upper bound
+    for (int base = 0; base <= S; base += kIndexThreads) {
+        const int s = base + tid;
+        const int c = s < S ? a.group_start[s] : 0;
+        int x = c;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) sums[warp] = x;
+        __syncthreads();
+        int before = carry, all = 0;
+        for (int w = 0; w < 32; ++w) {
+            if (w < warp) before += sums[w];
+            all += sums[w];
+        }
+        if (s <= S) a.group_start[s] = before + x - c;
+        __syncthreads();
+        if (tid == 0) carry += all;
+        __syncthreads();
+    }
+    for (int base = 0; base < n; base += kIndexThreads) {
+        const int i = base + tid, cnt = min(n - base, kIndexThreads);
+        const int mine = i < n ? record_seq(a.plan, kind, i) : -1;
+        seqs[tid] = mine;
+        __syncthreads();
+        int before = 0, after = 0;
+        for (int t = 0; t < cnt; ++t) {
+            const bool same = seqs[t] == mine;
+            before += same && t < tid;
+            after += same && t > tid;
+        }
+        const int at = i < n ? a.group_start[mine] : 0;
+        __syncthreads();
+        if (i < n) {
+            a.group_list[at + before] = i;
+            if (after == 0) a.group_start[mine] = at + before + 1;
+        }
+        __syncthreads();
+    }
+    // the cursors stand at the upper bounds: shift them into place, from the end
+    for (int base = (S / kIndexThreads) * kIndexThreads; base >= 0; base -= kIndexThreads) {
+        const int s = base + tid;
+        const int v = s <= S ? (s == 0 ? 0 : a.group_start[s - 1]) : 0;
+        __syncthreads();
+        if (s <= S) a.group_start[s] = v;
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------ decode items --
+constexpr int kItemThreads = 256;
+constexpr int kMaxStagedHeads = 128;
+
+// One CTA per (sequence or item, KV head, block of keys), a key per thread and
+// step; the CTA strides over the blocks of its keys.
+__global__ void __launch_bounds__(kItemThreads) mass_items_kernel(MassArgs a, int repeated, int blocks) {
+    griddep_wait();
+    griddep_launch();
+    __shared__ float lse[kMaxStagedHeads];
+    const int blk = blockIdx.x % blocks;
+    const int rest = blockIdx.x / blocks;
+    const int kvh = rest % a.hkv, unit = rest / a.hkv;
+    const int G = a.hq / a.hkv;
+    const int first = repeated ? a.group_start[unit] : unit, last = repeated ? a.group_start[unit + 1] : unit + 1;
+    for (int e = first; e < last; ++e) {
+        const int item = repeated ? a.group_list[e] : e;
+        const int qi = a.plan.decode[item];
+        const int4 meta = a.plan.qmeta[qi];
+        int64_t lo, hi;
+        visible_range(meta.y, a.plan.seq_lens[meta.x], a.causal, a.window, lo, hi);
+        if (hi - lo > a.cap) {
+            // the workspace holds no scores past cap: this item adds nothing
+            if (threadIdx.x == 0) atomicCAS(a.status, 0, PA_DEVICE_RANGE);
+            continue;
+        }
+        const int32_t *trow = a.plan.table + (int64_t)meta.x * a.plan.width;
+        const int ps = a.plan.page_size;
+        for (int g0 = 0; g0 < G; g0 += kMaxStagedHeads) {
+            const int gn = min(G - g0, kMaxStagedHeads);
+            __syncthreads();
+            for (int g = threadIdx.x; g < gn; g += kItemThreads)
+                lse[g] = merged_lse2(a, (int64_t)qi * a.hq + kvh * G + g0 + g);
+            __syncthreads();
+            for (int64_t i = (int64_t)blk * kItemThreads + threadIdx.x; i < hi - lo; i += (int64_t)blocks * kItemThreads) {
+                const float *sc = a.scores + ((int64_t)item * a.hq + kvh * G + g0) * a.cap + i;
+                float p = 0.f;
+                for (int g = 0; g < gn; ++g) p += exp2f(sc[g * a.cap] - lse[g]);
+                const int64_t j = lo + i;
+                const int64_t page = trow[j / ps];
+                a.key_mass[(page * a.hkv + kvh) * ps + j % ps] += p;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------- recomputed scores --
+constexpr int kReThreads = 256, kReKeys = 32, kReRows = kReThreads / kReKeys;
+
+// One CTA per (sequence, KV head, block of 32 keys): the keys stay in shared
+// memory (fp32), the sequence's queries stream past, eight (query, head) rows at
+// a time, one dot product per thread.
+template <typename T>
+__global__ void __launch_bounds__(kReThreads) mass_recompute_kernel(MassArgs a, int kind, int blocks) {
+    griddep_wait();
+    griddep_launch();
+    extern __shared__ float sm[];
+    const int stride = a.d | 1;                        // odd: the 32 keys of a warp hit 32 banks
+    float *keys = sm;                                   // [32][stride]
+    float *rows = keys + kReKeys * stride;              // [8][d]
+    __shared__ float part[kReRows][kReKeys];
+    const int blk = blockIdx.x % blocks;
+    const int rest = blockIdx.x / blocks;
+    const int kvh = rest % a.hkv, s = rest / a.hkv;
+    const int G = a.hq / a.hkv, ps = a.plan.page_size;
+    const int first = a.group_start[s], last = a.group_start[s + 1];
+    if (first == last) return;
+    const int n = a.plan.seq_lens[s];
+    const int32_t *trow = a.plan.table + (int64_t)s * a.plan.width;
+    const T *kc = static_cast<const T *>(a.k), *qc = static_cast<const T *>(a.q);
+    const int key = threadIdx.x % kReKeys, slot = threadIdx.x / kReKeys;
+    for (int j0 = blk * kReKeys; j0 < n; j0 += blocks * kReKeys) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < kReKeys * a.d; i += kReThreads) {
+            const int t = i / a.d, e = i - t * a.d, j = j0 + t;
+            keys[t * stride + e] =
+                j < n ? to_f<T>(kc[(((int64_t)trow[j / ps] * ps + j % ps) * a.hkv + kvh) * a.d + e]) : 0.f;
+        }
+        float sum = 0.f;
+        for (int e = first; e < last; ++e) {
+            const int rec = a.group_list[e];
+            const int q0 = kind == kMassTiles ? a.plan.tiles[rec].y : rec;
+            const int nrows = (kind == kMassTiles ? a.plan.tiles[rec].z : 1) * G;
+            for (int r0 = 0; r0 < nrows; r0 += kReRows) {
+                // any row of these eight that sees a key of the block?
+                const int r = r0 + slot;
+                const bool live = r < nrows;
+                const int qi = q0 + (live ? r : r0) / G, h = kvh * G + (live ? r : r0) % G;
+                int64_t lo, hi;
+                visible_range(a.plan.qmeta[qi].y, n, a.causal, a.window, lo, hi);
+                const bool sees = live && lo < j0 + kReKeys && hi > j0;
+                if (!__syncthreads_or(sees)) continue;
+                for (int i = threadIdx.x; i < kReRows * a.d; i += kReThreads) {
+                    const int t = i / a.d, c = i - t * a.d, rr = r0 + t;
+                    rows[i] = rr < nrows
+                                  ? to_f<T>(qc[((int64_t)(q0 + rr / G) * a.hq + kvh * G + rr % G) * a.d + c]) *
+                                        (a.scale * kLog2e)
+                                  : 0.f;
+                }
+                __syncthreads();
+                const int64_t j = j0 + key;
+                if (sees && j >= lo && j < hi) {
+                    float dot = 0.f;
+                    for (int c = 0; c < a.d; ++c) dot = fmaf(rows[slot * a.d + c], keys[key * stride + c], dot);
+                    sum += exp2f(dot - a.lse_final[(int64_t)qi * a.hq + h] * kLog2e);
+                }
+            }
+        }
+        __syncthreads();
+        part[slot][key] = sum;
+        __syncthreads();
+        if (slot == 0 && j0 + key < n) {
+            float t = 0.f;
+            for (int w = 0; w < kReRows; ++w) t += part[w][key];
+            const int64_t page = trow[(j0 + key) / ps];
+            a.key_mass[(page * a.hkv + kvh) * ps + (j0 + key) % ps] += t;
+        }
+    }
+}
+
+int blocks_for(int64_t units, int64_t want) {
+    const int64_t most = INT32_MAX / (units > 0 ? units : 1);
+    const int64_t b = want < most ? want : most;
+    return (int)(b < 1 ? 1 : b);
+}
+
+template <typename T> cudaError_t launch_re(const MassArgs &a, MassRecords kind, cudaStream_t st) {
+    const size_t smem = (size_t)(kReKeys * (a.d | 1) + kReRows * a.d) * sizeof(float);
+    cudaError_t e = cudaFuncSetAttribute(mass_recompute_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int64_t units = (int64_t)a.plan.sequences * a.hkv;
+    const int blocks = blocks_for(units, ((int64_t)a.longest + kReKeys - 1) / kReKeys);
+    return launch_pdl(mass_recompute_kernel<T>, dim3((unsigned)(units * blocks)), dim3(kReThreads), smem, st, a, (int)kind,
+                      blocks);
+}
+
+}  // namespace
+
+cudaError_t launch_mass_index(const MassArgs &a, MassRecords kind, cudaStream_t st) {
+    const int n = kind == kMassItems ? a.plan.n_decode : (kind == kMassTiles ? a.plan.n_tiles : a.plan.queries);
+    return launch_pdl(mass_index_kernel, dim3(1), dim3(kIndexThreads), 0, st, a, (int)kind, n);
+}
+
+cudaError_t launch_lse_final(const MassArgs &a, float *out, cudaStream_t st) {
+    const int64_t rows = (int64_t)a.plan.queries * a.hq;
+    return launch_pdl(lse_final_kernel, dim3((unsigned)((rows + 255) / 256)), dim3(256), 0, st, a, out);
+}
+
+cudaError_t launch_mass_items(const MassArgs &a, bool repeated, cudaStream_t st) {
+    const int64_t units = (int64_t)(repeated ? a.plan.sequences : a.plan.n_decode) * a.hkv;
+    const int blocks = blocks_for(units, ((int64_t)a.longest + kItemThreads - 1) / kItemThreads);
+    cudaError_t e = launch_pdl(mass_items_kernel, dim3((unsigned)(units * blocks)), dim3(kItemThreads), 0, st, a,
+                               repeated ? 1 : 0, blocks);
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+cudaError_t launch_mass_recompute(const MassArgs &a, MassRecords kind, cudaStream_t st) {
+    cudaError_t e;
+    switch (a.dtype) {
+        case PA_F32: e = launch_re<float>(a, kind, st); break;
+        case PA_F16: e = launch_re<__half>(a, kind, st); break;
+        default: e = launch_re<__nv_bfloat16>(a, kind, st); break;
+    }
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+}  // namespace pa

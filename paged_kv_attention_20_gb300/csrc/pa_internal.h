@@ -49,6 +49,8 @@ struct AttnArgs {
     int32_t splits;
     pa_dtype dtype;
     int32_t *status;      // device status word (bounded waits record timeouts here)
+    float *scores;        // per-key totals wanted: log2-domain scores [item, Hq, score_cap] (else null)
+    int64_t score_cap;    // keys a score row holds (key j of an item at j - lo)
     int32_t max_ctas;     // persistent kernels: at most this many CTAs (0: as many as are resident at once)
 };
 
@@ -118,6 +120,61 @@ cudaError_t launch_mla(const AttnArgs &a, bool use_decode_list, cudaStream_t st)
 
 // One decode step forward on the device (pa_plan_advance).
 cudaError_t launch_plan_advance(const PlanView &plan, int32_t *status, cudaStream_t st);
+
+// Norm + rotation + append (paged_qk_norm_rope_store).
+struct NormRopeArgs {
+    PlanView plan;
+    const void *q, *k, *v;                 // rows of heads * dim elements, `*_stride` elements apart
+    int64_t q_stride, k_stride, v_stride;
+    void *q_out, *k_cache, *v_cache;
+    float *key_mass;                       // [pages, Hkv, page_size] or null
+    const float *table;                    // [max_positions, rot] cos | sin, or null
+    const int32_t *positions;              // [queries] or null: the plan's positions
+    const void *q_weight, *k_weight;       // [d] or null: no norm
+    float eps;
+    int32_t max_positions, rot, interleaved;
+    int32_t hq, hkv, d, dv;
+    pa_dtype dtype;
+    int32_t *status;
+};
+cudaError_t launch_norm_rope_store(const NormRopeArgs &a, cudaStream_t st);
+
+// Per-key softmax weight totals (paged_attn_forward_mass).
+struct MassArgs {
+    PlanView plan;
+    const void *q, *k;
+    float *key_mass;          // [pages, Hkv, page_size]
+    const float *lse;         // natural-log log-sum-exp [splits, queries, Hq]
+    const float *lse_final;   // the same merged over the splits, [queries, Hq] (splits == 1: lse)
+    const float *scores;      // [decode item, Hq, cap], log2 domain
+    int64_t cap;
+    int32_t *group_start;     // [sequences + 1] records grouped by sequence (launch_mass_index)
+    int32_t *group_list;      // [records]
+    int32_t hq, hkv, d, splits, causal, window;
+    float scale;
+    pa_dtype dtype;
+    int32_t *status;
+    int32_t longest;          // longest history in the host copy (grid sizing only)
+};
+enum MassRecords { kMassItems = 0, kMassTiles = 1, kMassQueries = 2 };
+// Records of one kind (decode items, prefill tiles, single queries) grouped by sequence.
+cudaError_t launch_mass_index(const MassArgs &a, MassRecords kind, cudaStream_t st);
+cudaError_t launch_lse_final(const MassArgs &a, float *out, cudaStream_t st);
+// Decode items from their stored scores; `repeated`: sequences may have several items (grouped first).
+cudaError_t launch_mass_items(const MassArgs &a, bool repeated, cudaStream_t st);
+// Grouped tiles or queries, scores recomputed.
+cudaError_t launch_mass_recompute(const MassArgs &a, MassRecords kind, cudaStream_t st);
+
+// Eviction (paged_kv_evict).
+struct EvictArgs {
+    PlanView src, dst;
+    float *key_mass;
+    void *k_cache, *v_cache;
+    int32_t *kept;            // [sequences, Hkv, kept_stride]
+    int32_t kept_stride, sink, recent, hkv, d, dv, elem;
+    int32_t *status;
+};
+cudaError_t launch_evict(const EvictArgs &a, cudaStream_t st);
 
 // Device status word (bounded waits record their timeouts here).
 cudaError_t read_device_status(int32_t *code, bool clear);

@@ -16,40 +16,22 @@
 #include <string>
 #include <vector>
 
-#include "pa_internal.h"
+#include "plan_host.h"
 
-struct pa_plan {
-    int32_t queries = 0, sequences = 0, width = 0, page_size = 0, pages = 0;
-    int32_t n_decode = 0, n_tiles = 0, n_tile_queries = 0;
-    int64_t max_seq_len = 0;          // longest sequence any decode item reads
-    std::vector<int32_t> words;       // host copy of the device metadata
-    size_t off_qmeta = 0, off_seqlen = 0, off_table = 0, off_decode = 0, off_tiles = 0, off_order = 0;
-    const int32_t *dev = nullptr;     // caller's device copy (after upload)
-    // visible keys of the prefill tiles' queries and of the decode items, without
-    // a window, non-causal [0] and causal [1] (the mixed call's SM share needs them)
-    double keys_tiles[2] = {0, 0}, keys_decode[2] = {0, 0};
-};
+using pa::aligned16;
+using pa::elem_bytes;
+using pa::fail;
+using pa::fail_cuda;
+using pa::operands_on_device;
+using pa::valid_dtype;
+using pa::view_of;
 
 namespace {
 
 thread_local std::string g_error;
 thread_local cudaEvent_t g_time_start = nullptr, g_time_stop = nullptr;  // pa_time_next_kernel
 
-pa_status fail(pa_status st, const char *msg) {
-    g_error = msg;
-    return st;
-}
-
-pa_status fail_cuda(cudaError_t e, const char *what) {
-    g_error = std::string(what) + ": " + cudaGetErrorString(e);
-    return PA_ERR_CUDA;
-}
-
 size_t align_words(size_t n, size_t a) { return (n + a - 1) / a * a; }
-
-bool valid_dtype(pa_dtype d) { return d == PA_F32 || d == PA_F16 || d == PA_BF16; }
-
-int elem_bytes(pa_dtype d) { return d == PA_F32 ? 4 : 2; }
 
 // A mixed call's decode items can run beside its prefill tiles: the tiles are
 // bound by the tensor core and the softmax, the decode items by HBM, and one
@@ -123,8 +105,40 @@ void visible_key_sums(const pa_plan *plan, int causal, int window, double &keys_
     for (int i = 0; i < plan->n_decode; ++i) keys_decode += visible(w[plan->off_decode + i]);
 }
 
-pa::PlanView view_of(const pa_plan *p) {
-    pa::PlanView v{};
+// True when `ptr` is device memory of the current device.  The kernels'
+// tensor maps and loads address only this GPU's own memory, so host memory
+// (pinned or not), managed memory and other GPUs' memory are refused.
+bool on_current_device(const void *ptr, int dev) {
+    cudaPointerAttributes at{};
+    if (cudaPointerGetAttributes(&at, ptr) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return at.type == cudaMemoryTypeDevice && at.device == dev;
+}
+
+}  // namespace
+
+namespace pa {
+
+pa_status fail(pa_status st, const char *msg) {
+    g_error = msg;
+    return st;
+}
+
+pa_status fail_cuda(cudaError_t e, const char *what) {
+    g_error = std::string(what) + ": " + cudaGetErrorString(e);
+    return PA_ERR_CUDA;
+}
+
+bool valid_dtype(pa_dtype d) { return d == PA_F32 || d == PA_F16 || d == PA_BF16; }
+
+int elem_bytes(pa_dtype d) { return d == PA_F32 ? 4 : 2; }
+
+bool aligned16(const void *ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
+
+PlanView view_of(const pa_plan *p) {
+    PlanView v{};
     v.qmeta = reinterpret_cast<const int4 *>(p->dev + p->off_qmeta);
     v.seq_lens = p->dev + p->off_seqlen;
     v.table = p->dev + p->off_table;
@@ -141,22 +155,6 @@ pa::PlanView view_of(const pa_plan *p) {
     return v;
 }
 
-bool aligned16(const void *ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
-
-// True when `ptr` is device memory of the current device.  The kernels'
-// tensor maps and loads address only this GPU's own memory, so host memory
-// (pinned or not), managed memory and other GPUs' memory are refused.
-bool on_current_device(const void *ptr, int dev) {
-    cudaPointerAttributes at{};
-    if (cudaPointerGetAttributes(&at, ptr) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    return at.type == cudaMemoryTypeDevice && at.device == dev;
-}
-
-// PA_OK when every non-null pointer of `ptrs` is device memory of the current
-// device, else PA_ERR_ARG naming the operand.
 pa_status operands_on_device(const void *const *ptrs, const char *const *names, int n, const char *call) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -173,8 +171,39 @@ pa_status operands_on_device(const void *const *ptrs, const char *const *names, 
     return PA_OK;
 }
 
+int32_t plan_facts(const pa_plan *plan) {
+    int32_t facts = plan->facts.load(std::memory_order_acquire);
+    if (facts) return facts;
+    std::lock_guard<std::mutex> lock(plan->facts_mutex);
+    facts = plan->facts.load(std::memory_order_relaxed);
+    if (facts) return facts;
+    facts = kFactsKnown;
+    const int32_t *w = plan->words.data();
+    plan->held.assign(((size_t)plan->pages + 63) / 64, 0);
+    for (int32_t s = 0; s < plan->sequences; ++s) {
+        const int64_t used = ((int64_t)w[plan->off_seqlen + s] + plan->page_size - 1) / plan->page_size;
+        const int32_t *row = w + plan->off_table + (size_t)s * plan->width;
+        for (int64_t g = 0; g < used; ++g) {
+            uint64_t &word = plan->held[(size_t)row[g] / 64];
+            const uint64_t bit = 1ull << (row[g] % 64);
+            if (word & bit) facts |= kFactSharedPages;
+            word |= bit;
+        }
+    }
+    std::vector<bool> seen((size_t)plan->sequences, false);
+    for (int32_t i = 0; i < plan->n_decode; ++i) {
+        const size_t s = (size_t)w[plan->off_qmeta + 4 * (size_t)w[plan->off_decode + i]];
+        if (seen[s]) {
+            facts |= kFactRepeatedItems;
+            break;
+        }
+        seen[s] = true;
+    }
+    plan->facts.store(facts, std::memory_order_release);
+    return facts;
+}
 
-}  // namespace
+}  // namespace pa
 
 pa_status pa_fail_with(pa_status status, const char *msg) { return fail(status, msg); }
 
@@ -568,7 +597,7 @@ int decode_sms_beside_prefill(const pa_plan *plan, int hq, int hkv, int d, int d
 pa_status attention(const pa_plan *plan, const void *q, const void *k, const void *v, const void *qp,
                     const void *kp, void *out, int32_t hq, int32_t hkv, int32_t d, int32_t dv, int32_t p,
                     float scale, int32_t causal, int32_t window, pa_dtype dtype, void *ws, size_t ws_bytes, int32_t splits,
-                    bool split_call, bool mla, cudaStream_t st, const char *name) {
+                    bool split_call, bool mla, cudaStream_t st, const char *name, float *key_mass = nullptr) {
     char msg[256];
     auto bad = [&](pa_status s, const char *what) {
         std::snprintf(msg, sizeof msg, "%s: %s", name, what);
@@ -576,7 +605,15 @@ pa_status attention(const pa_plan *plan, const void *q, const void *k, const voi
     };
     pa_status checked = pa::check_attention_args(plan, hq, hkv, d, dv, p, scale, causal, window, dtype, mla, name);
     if (checked != PA_OK) return checked;
-    if (split_call) {
+    const bool mass = key_mass != nullptr;
+    pa::MassLayout lay{};
+    if (mass) {
+        if (splits < 1 || splits > PA_MAX_SPLITS) return bad(PA_ERR_SPLITS, "splits must be in 1..64");
+        lay = pa::mass_layout(plan, hq, dv, splits, causal ? window : 0, 0);
+        if (!ws && plan->queries > 0) return bad(PA_ERR_WORKSPACE, "workspace is null");
+        if (ws_bytes < lay.bytes) return bad(PA_ERR_WORKSPACE, "workspace too small");
+        if (ws && !aligned16(ws)) return bad(PA_ERR_WORKSPACE, "workspace not 16-byte aligned");
+    } else if (split_call) {
         if (splits < 1 || splits > PA_MAX_SPLITS) return bad(PA_ERR_SPLITS, "splits must be in 1..64");
         if (splits > 1 || ws) {
             size_t need = pa_workspace_bytes(plan->queries, hq, dv, splits);
@@ -592,10 +629,10 @@ pa_status attention(const pa_plan *plan, const void *q, const void *k, const voi
     if (!plan->dev) return bad(PA_ERR_STATE, "plan not uploaded");
     if (!q || !k || !v || !out || (mla && (!qp || !kp))) return bad(PA_ERR_ARG, "null tensor");
     {
-        const void *ptrs[] = {q, k, v, out, qp, kp, splits > 1 ? ws : nullptr};
+        const void *ptrs[] = {q, k, v, out, qp, kp, splits > 1 || mass ? ws : nullptr, key_mass};
         const char *names[] = {"q", "the key cache", "the value cache", "out", "the position query",
-                               "the position cache", "the workspace"};
-        pa_status on_dev = operands_on_device(ptrs, names, 7, name);
+                               "the position cache", "the workspace", "key_mass"};
+        pa_status on_dev = operands_on_device(ptrs, names, 8, name);
         if (on_dev != PA_OK) return on_dev;
     }
 
@@ -606,7 +643,17 @@ pa_status attention(const pa_plan *plan, const void *q, const void *k, const voi
     a.scale = scale; a.causal = causal; a.window = window; a.splits = splits; a.dtype = dtype;
     a.status = pa::device_status_ptr();
     if (!a.status) return bad(PA_ERR_CUDA, "device status word unavailable");
-    if (splits > 1) {
+    if (mass) {
+        char *base = static_cast<char *>(ws);
+        a.ws_o = splits > 1 ? reinterpret_cast<float *>(base) : nullptr;
+        a.ws_lse = reinterpret_cast<float *>(base + lay.lse);
+        if (plan->n_decode > 0 && (plan->n_tiles == 0 || pa::prefill_supported(a))) {
+            // whatever the caller gave beyond the need makes longer score rows, so a
+            // captured decode loop can outgrow the histories it was captured with
+            a.score_cap = lay.cap + (int64_t)((ws_bytes - lay.bytes) / 128 / ((size_t)plan->n_decode * hq)) * 32;
+            a.scores = reinterpret_cast<float *>(base + lay.scores);
+        }
+    } else if (splits > 1) {
         size_t rows = (size_t)splits * plan->queries * hq;
         a.ws_o = static_cast<float *>(ws);
         a.ws_lse = reinterpret_cast<float *>(static_cast<char *>(ws) + (rows * dv * sizeof(float) + 255) / 256 * 256);
@@ -664,11 +711,20 @@ pa_status attention(const pa_plan *plan, const void *q, const void *k, const voi
             if (e == cudaSuccess && splits > 1) e = pa::launch_merge(a, all_decode, st);
         }
     }
+    if (e == cudaSuccess && mass) e = pa::add_mass(plan, a, lay, static_cast<char *>(ws), key_mass, st);
     if (e != cudaSuccess) return fail_cuda(e, name);
     return PA_OK;
 }
 
 }  // namespace
+
+pa_status pa::attention_with_mass(const pa_plan *plan, const void *q, const void *k, const void *v, void *out,
+                                  float *key_mass, int32_t hq, int32_t hkv, int32_t d, int32_t dv, float scale,
+                                  int32_t causal, int32_t window, pa_dtype dtype, void *ws, size_t ws_bytes,
+                                  int32_t splits, cudaStream_t st, const char *name) {
+    return attention(plan, q, k, v, nullptr, nullptr, out, hq, hkv, d, dv, 0, scale, causal, window, dtype, ws, ws_bytes,
+                     splits, true, false, st, name, key_mass);
+}
 
 extern "C" {
 
@@ -713,6 +769,7 @@ pa_status pa_plan_advance(pa_plan *plan, pa_stream_t stream) {
     if (!status) return fail(PA_ERR_CUDA, "pa_plan_advance: device status word unavailable");
     cudaError_t e = pa::launch_plan_advance(view_of(plan), status, (cudaStream_t)stream);
     if (e != cudaSuccess) return fail_cuda(e, "pa_plan_advance launch");
+    plan->facts.store(0, std::memory_order_relaxed);   // lengths, and so the used pages, change
     // keep the host copy in step with one advance (graph replays advance only the device copy)
     int32_t *w = plan->words.data();
     for (int32_t q = 0; q < plan->queries; ++q) {

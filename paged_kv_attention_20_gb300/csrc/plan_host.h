@@ -1,0 +1,67 @@
+// Host-side internals shared by the entry points: the plan object, error
+// reporting and the operand checks that come before every launch.
+#pragma once
+
+#include <atomic>
+#include <cstdint>
+#include <mutex>
+#include <vector>
+
+#include "pa_internal.h"
+
+struct pa_plan {
+    int32_t queries = 0, sequences = 0, width = 0, page_size = 0, pages = 0;
+    int32_t n_decode = 0, n_tiles = 0, n_tile_queries = 0;
+    int64_t max_seq_len = 0;          // longest sequence any decode item reads
+    std::vector<int32_t> words;       // host copy of the device metadata
+    size_t off_qmeta = 0, off_seqlen = 0, off_table = 0, off_decode = 0, off_tiles = 0, off_order = 0;
+    const int32_t *dev = nullptr;     // caller's device copy (after upload)
+    // visible keys of the prefill tiles' queries and of the decode items, without
+    // a window, non-causal [0] and causal [1] (the mixed call's SM share needs them)
+    double keys_tiles[2] = {0, 0}, keys_decode[2] = {0, 0};
+    // facts of the host copy that only some calls need, worked out on first use
+    // (plan_facts): 0 = not yet, else kFactsKnown | flags; `held` then has a bit
+    // for every page that a used block-table entry names
+    mutable std::atomic<int32_t> facts{0};
+    mutable std::mutex facts_mutex;
+    mutable std::vector<uint64_t> held;
+};
+
+namespace pa {
+
+constexpr int32_t kFactsKnown = 1;
+constexpr int32_t kFactSharedPages = 2;     // some page is held by two used block-table entries
+constexpr int32_t kFactRepeatedItems = 4;   // some sequence has more than one decode item
+
+// Facts about the plan's host copy (kFact* flags); std::bad_alloc when the host
+// has no memory for them.
+int32_t plan_facts(const pa_plan *plan);
+
+pa_status fail(pa_status st, const char *msg);
+pa_status fail_cuda(cudaError_t e, const char *what);
+bool valid_dtype(pa_dtype d);
+int elem_bytes(pa_dtype d);
+bool aligned16(const void *ptr);
+PlanView view_of(const pa_plan *p);
+// PA_OK when every non-null pointer of `ptrs` is device memory of the current
+// device, else PA_ERR_ARG naming the operand.
+pa_status operands_on_device(const void *const *ptrs, const char *const *names, int n, const char *call);
+
+// Workspace of paged_attn_forward_mass: byte offsets of its parts.
+struct MassLayout {
+    size_t lse, lse_final, groups, scores, bytes;   // the split partials start at 0
+    int64_t cap;                                     // keys of one score row
+};
+// max_keys: keys the score rows hold at least; 0: the longest history of the host copy.
+// window: the call's, 0 when it is not causal (a causal query sees at most `window` keys).
+MassLayout mass_layout(const pa_plan *plan, int32_t hq, int32_t dv, int32_t splits, int32_t window, int64_t max_keys);
+// The kernels that follow the attention of `a` and add its weights to key_mass.
+cudaError_t add_mass(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass,
+                     cudaStream_t st);
+// Attention entry body with totals; key_mass is not null.
+pa_status attention_with_mass(const pa_plan *plan, const void *q, const void *k, const void *v, void *out,
+                              float *key_mass, int32_t hq, int32_t hkv, int32_t d, int32_t dv, float scale,
+                              int32_t causal, int32_t window, pa_dtype dtype, void *ws, size_t ws_bytes, int32_t splits,
+                              cudaStream_t st, const char *name);
+
+}  // namespace pa

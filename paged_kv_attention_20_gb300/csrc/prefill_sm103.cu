@@ -624,6 +624,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint4 *>(dst) = make_uint4(ch[4 * c], ch[4 * c + 1], ch[4 * c + 2], ch[4 * c + 3]);
                     }
                 }
+                // the per-key totals need the row's log-sum-exp of an unsplit call too
+                if (prm.ws_lse && r < u.nq && h2 == 0) prm.ws_lse[orow] = (m_ref + log2f(lsum)) * 0.6931471805599453f;
                 }
                 // O of this unit has been read: the next unit's first P.V may overwrite it
                 tc_fence_before();
