@@ -153,11 +153,15 @@ __global__ void __launch_bounds__(kItemThreads) mass_items_kernel(MassArgs a, in
             for (int g = threadIdx.x; g < gn; g += kItemThreads)
                 lse[g] = merged_lse2(a, (int64_t)qi * a.hq + kvh * G + g0 + g);
             __syncthreads();
-            for (int64_t i = (int64_t)blk * kItemThreads + threadIdx.x; i < hi - lo; i += (int64_t)blocks * kItemThreads) {
-                const float *sc = a.scores + ((int64_t)item * a.hq + kvh * G + g0) * a.cap + i;
+            // key j always falls to block (j / kItemThreads) % blocks, whatever the
+            // item's own range: the items of a sequence never meet on a key from
+            // two CTAs
+            const int64_t step = (int64_t)blocks * kItemThreads;
+            for (int64_t j = lo / step * step + (int64_t)blk * kItemThreads + threadIdx.x; j < hi; j += step) {
+                if (j < lo) continue;
+                const float *sc = a.scores + ((int64_t)item * a.hq + kvh * G + g0) * a.cap + (j - lo);
                 float p = 0.f;
                 for (int g = 0; g < gn; ++g) p += exp2f(sc[g * a.cap] - lse[g]);
-                const int64_t j = lo + i;
                 const int64_t page = trow[j / ps];
                 a.key_mass[(page * a.hkv + kvh) * ps + j % ps] += p;
             }

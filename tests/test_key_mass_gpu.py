@@ -87,6 +87,14 @@ def test_several_queries_of_a_sequence(cuda_device, hq, hkv, d, ps, dt, window):
     verify(case, 4, True, window)
 
 
+def test_drafted_tokens_under_a_window(cuda_device):
+    """Queries a few positions apart see ranges a few keys apart: every key still has one owner."""
+    lens = [2000, 1111, 700]
+    queries = [(s, n - 5 + i) for s, n in enumerate(lens) for i in range(5)]
+    case = build_case("mass", 7, lens, queries, 4, 2, 64, 64, 32, HF, 0.125)
+    verify(case, 3, True, 1000)
+
+
 @pytest.mark.parametrize("window", [0, 70])
 @pytest.mark.parametrize("splits", [1, 3])
 @pytest.mark.parametrize("hq,hkv,d,ps,dt", [
