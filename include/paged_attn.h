@@ -434,7 +434,8 @@ pa_status paged_attn_forward_mass(const pa_plan *plan, const void *q, const void
  * sequence with equal lengths keeps every key (and is copied where the pages
  * differ); otherwise its budget is at least sink + recent (PA_ERR_SHAPE).  Rows past
  * a kept length are left as they were.  Lengths are read from the plans' device
- * copies: a source advanced by graph replays is evicted at its true length.  The
+ * copies: a source advanced by graph replays is evicted at its true length
+ * (kept_plan is used as it was built).  The
  * next step's plan is built from the kept lengths; rotated positions no longer
  * equal cache rows then (see `positions` above).
  */

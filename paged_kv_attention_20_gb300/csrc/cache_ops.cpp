@@ -191,10 +191,11 @@ pa_status paged_kv_evict(const pa_plan *plan, const pa_plan *kept_plan, float *k
         BAD(PA_ERR_SHAPE, "the plans differ in sequences, page size or pool");
     if ((int64_t)plan->pages * plan->page_size * num_kv_heads * std::max(head_dim, value_dim) > (int64_t)1 << 40)
         BAD(PA_ERR_RANGE, "cache too large");
+    int32_t longest = 0, longest_src = 0;
+    bool in_place = false;
     try {
         const int32_t *w = plan->words.data(), *d = kept_plan->words.data();
         const int32_t ps = plan->page_size;
-        int32_t longest = 0;
         // Rows are written into a page that nothing else reads or writes: a page no
         // used entry of the source schedule names, named once, or the sequence's own
         // page of the same index, held by nobody else.  Pages inside the sink keep
@@ -207,6 +208,7 @@ pa_status paged_kv_evict(const pa_plan *plan, const pa_plan *kept_plan, float *k
             if (m > n) BAD(PA_ERR_SHAPE, "a sequence would keep more keys than it has");
             if (m < n && m < (int64_t)sink + recent) BAD(PA_ERR_SHAPE, "a sequence's budget is below sink + recent");
             longest = std::max(longest, m);
+            longest_src = std::max(longest_src, n);
             const int32_t *from = w + plan->off_table + (size_t)s * plan->width;
             const int32_t *to = d + kept_plan->off_table + (size_t)s * kept_plan->width;
             const int64_t used = ((int64_t)n + ps - 1) / ps, kept_pages = ((int64_t)m + ps - 1) / ps;
@@ -214,7 +216,10 @@ pa_status paged_kv_evict(const pa_plan *plan, const pa_plan *kept_plan, float *k
                 const bool fresh = to[g] != from[g];
                 if (fresh && (plan->held[(size_t)to[g] / 64] >> (to[g] % 64) & 1))
                     BAD(PA_ERR_WRITE_CONFLICT, "the kept schedule writes a page that the source schedule reads");
-                if ((src_shared || dst_shared) && (fresh || (m < n && (g + 1) * ps > sink))) written.push_back(to[g]);
+                in_place |= !fresh;
+                // (rows may move even where the host copies' lengths agree: the source
+                // may have been advanced on the device)
+                if ((src_shared || dst_shared) && (fresh || (g + 1) * ps > sink)) written.push_back(to[g]);
             }
             if (src_shared) all.insert(all.end(), from, from + used);
         }
@@ -257,7 +262,7 @@ pa_status paged_kv_evict(const pa_plan *plan, const pa_plan *kept_plan, float *k
     a.elem = pa::elem_bytes(dtype);
     a.status = pa::device_status_ptr();
     if (!a.status) BAD(PA_ERR_CUDA, "device status word unavailable");
-    cudaError_t e = pa::launch_evict(a, (cudaStream_t)stream);
+    cudaError_t e = pa::launch_evict(a, longest_src, longest, in_place, (cudaStream_t)stream);
     if (e != cudaSuccess) return pa::fail_cuda(e, "paged_kv_evict launch");
     return PA_OK;
 #undef BAD

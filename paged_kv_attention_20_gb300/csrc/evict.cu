@@ -16,20 +16,22 @@
 // barrier between the reads and the writes of a chunk is all it takes.
 
 #include "pa_internal.h"
+#include "sm103_tc.cuh"
 
 namespace pa {
 namespace {
 
 // Physical row of key j of sequence s, -1 when the table maps none.
-__device__ __forceinline__ int64_t slot_of(const PlanView &p, int s, int j) {
-    const int g = j / p.page_size;
+// ps_shift: log2(page size), -1 when it is no power of two.
+__device__ __forceinline__ int64_t slot_of(const PlanView &p, int s, int j, int ps_shift) {
+    const int g = ps_shift >= 0 ? j >> ps_shift : j / p.page_size;
     if (g >= p.width) return -1;
     const int pg = p.table[(int64_t)s * p.width + g];
     return pg < 0 || pg >= p.pages ? -1 : (int64_t)pg * p.page_size + (j - g * p.page_size);
 }
 
-__device__ __forceinline__ int64_t mass_at(int64_t slot, int h, int hkv, int ps) {
-    const int64_t pg = slot / ps;
+__device__ __forceinline__ int64_t mass_at(int64_t slot, int h, int hkv, int ps, int ps_shift) {
+    const int64_t pg = ps_shift >= 0 ? slot >> ps_shift : slot / ps;
     return (pg * hkv + h) * ps + (slot - pg * ps);
 }
 
@@ -55,166 +57,349 @@ __device__ __forceinline__ Budget budget_of(const EvictArgs &a, int s) {
     return b;
 }
 
-constexpr int kSelectThreads = 1024;
+// ------------------------------------------------------------------ choice --
+// One cluster of C CTAs per (sequence, head); CTA r holds the r-th part of the
+// candidates' order keys in shared memory (they are re-read from global memory
+// when a part is longer than fits).  The keep-th largest key is found by
+// narrowing an interval [lo, hi] of keys: 2048 equal bins over it, counted with
+// shared-memory atomics, the bin that holds the threshold becomes the interval
+// (11 bits a round, so at most three; bins follow the data's own range, which
+// spreads the counts: totals crowd into a few exponents).  Each CTA adds up the
+// cluster's histograms itself, through distributed shared memory.
+constexpr int kSelectThreads = 512;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kBins = 2048;
+static_assert(kBins == 4 * kSelectThreads, "four bins a thread");
 
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictArgs a) {
+struct SelectShared {
+    int hist[kBins];
+    int warp_a[kSelectWarps], warp_b[kSelectWarps];
+    uint32_t lo, hi;          // this CTA's smallest and largest key
+    int above, equal;         // this CTA's keys above / at the threshold
+    int found_bin, found_above, found_count;
+};
+
+template <typename V> __device__ __forceinline__ const V *peer(const V *p, uint32_t rank) {
+    uint64_t out;
+    asm("mapa.u64 %0, %1, %2;\n" : "=l"(out) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+    return reinterpret_cast<const V *>(out);
+}
+
+// room: keys the dynamic shared memory holds.  A part that is longer (the device
+// lengths can exceed the host's that sized the launch) is re-read instead.
+__global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictArgs a, int ps_shift, int room) {
     griddep_wait();
     griddep_launch();
-    __shared__ int hist[256];
-    __shared__ uint32_t s_prefix;
-    __shared__ int s_need;
-    __shared__ int warp_gt[32], warp_eq[32];
-    const int h = blockIdx.x % a.hkv, s = blockIdx.x / a.hkv;
+    extern __shared__ uint32_t staged[];
+    __shared__ __align__(16) SelectShared sh;
+    const uint32_t C = tc::cluster_nctarank(), rank = tc::cluster_ctarank();
+    const int pair = (int)(blockIdx.x / C);
+    const int h = pair % a.hkv, s = pair / a.hkv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Budget b = budget_of(a, s);
     int32_t *kept = a.kept + ((int64_t)s * a.hkv + h) * a.kept_stride;
-    for (int i = b.keep + tid; i < a.kept_stride; i += kSelectThreads) kept[i] = -1;
-    if (b.keep == b.n) {
-        for (int i = tid; i < b.keep; i += kSelectThreads) kept[i] = i;
+    const int all = (int)C * kSelectThreads, me = (int)rank * kSelectThreads + tid;
+    for (int i = b.keep + me; i < a.kept_stride; i += all) kept[i] = -1;
+    if (b.keep == b.n) {                      // the whole cluster leaves here together
+        for (int i = me; i < b.keep; i += all) kept[i] = i;
         return;
     }
-    for (int i = tid; i < b.first; i += kSelectThreads) kept[i] = i;
-    for (int i = tid; i < b.n - b.last; i += kSelectThreads) kept[b.first + b.want + i] = b.last + i;
+    for (int i = me; i < b.first; i += all) kept[i] = i;
+    for (int i = me; i < b.n - b.last; i += all) kept[b.first + b.want + i] = b.last + i;
     if (b.want == 0) return;
-    auto key = [&](int j) -> uint32_t {
-        const int64_t slot = slot_of(a.src, s, j);
+
+    // my part of the candidates: whole warps of 32 keys
+    const int n = b.last - b.first;
+    const int span = ((n + (int)C - 1) / (int)C + 31) / 32 * 32;
+    const int part0 = min(n, (int)rank * span), cnt = min(n, part0 + span) - part0;
+    const int j0 = b.first + part0;
+    auto fetch = [&](int i) -> uint32_t {
+        const int64_t slot = slot_of(a.src, s, j0 + i, ps_shift);
         if (slot < 0) {
             atomicCAS(a.status, 0, PA_DEVICE_RANGE);
             return 0u;
         }
-        return order_key(a.key_mass[mass_at(slot, h, a.hkv, a.src.page_size)]);
+        return order_key(a.key_mass[mass_at(slot, h, a.hkv, a.src.page_size, ps_shift)]);
     };
-    // the want-th largest key, eight bits a pass
-    uint32_t prefix = 0u, mask = 0u;
-    int need = b.want;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kSelectThreads) hist[i] = 0;
-        __syncthreads();
-        for (int j = b.first + tid; j < b.last; j += kSelectThreads) {
-            const uint32_t k = key(j);
-            if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
-        }
-        __syncthreads();
-        if (tid == 0) {
-            int d = 255, above = 0;
-            while (d > 0 && above + hist[d] < need) above += hist[d--];
-            s_prefix = prefix | ((uint32_t)d << shift);
-            s_need = need - above;
-        }
-        __syncthreads();
-        prefix = s_prefix;
-        need = s_need;
-        mask |= 255u << shift;
-        __syncthreads();
+    const bool fits = span <= room;
+    auto key = [&](int i) -> uint32_t { return fits ? staged[i] : fetch(i); };
+
+    uint32_t lo = 0xffffffffu, hi = 0u;
+#pragma unroll 8
+    for (int i = tid; i < cnt; i += kSelectThreads) {
+        const uint32_t k = fetch(i);
+        if (fits) staged[i] = k;
+        lo = min(lo, k);
+        hi = max(hi, k);
     }
-    // every key above the threshold and the first `need` equal to it, in order
-    int gt0 = 0, eq0 = 0;
-    for (int base = b.first; base < b.last; base += kSelectThreads) {
-        const int j = base + tid;
-        const uint32_t k = j < b.last ? key(j) : 0u;
-        const bool gt = j < b.last && k > prefix, eq = j < b.last && k == prefix;
-        const unsigned bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+        sh.warp_a[warp] = (int)lo;
+        sh.warp_b[warp] = (int)hi;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const uint32_t x = lane < kSelectWarps ? (uint32_t)sh.warp_a[lane] : 0xffffffffu;
+        const uint32_t y = lane < kSelectWarps ? (uint32_t)sh.warp_b[lane] : 0u;
+        const uint32_t mn = __reduce_min_sync(0xffffffffu, x), mx = __reduce_max_sync(0xffffffffu, y);
         if (lane == 0) {
-            warp_gt[warp] = __popc(bg);
-            warp_eq[warp] = __popc(be);
+            sh.lo = mn;
+            sh.hi = mx;
         }
+    }
+    tc::cluster_barrier();
+    for (uint32_t r = 0; r < C; ++r) {
+        lo = min(lo, *peer(&sh.lo, r));
+        hi = max(hi, *peer(&sh.hi, r));
+    }
+    // invariant: exactly b.want - need keys lie above hi, and need >= 1 of those in [lo, hi] stay
+    int need = b.want;
+    bool whole = false;                        // every key of [lo, hi] stays
+    while (true) {
+        const int width_bits = 32 - __clz((int)(hi - lo));     // 0 when lo == hi
+        const int shift = width_bits > 11 ? width_bits - 11 : 0;
+        reinterpret_cast<int4 *>(sh.hist)[tid] = make_int4(0, 0, 0, 0);
         __syncthreads();
-        int g = gt0, e = eq0, gs = 0, es = 0;
-        for (int w = 0; w < kSelectThreads / 32; ++w) {
-            if (w == warp) {
-                g += gs;
-                e += es;
-            }
-            gs += warp_gt[w];
-            es += warp_eq[w];
+        for (int i = tid; i < cnt; i += kSelectThreads) {
+            const uint32_t k = key(i);
+            if (k >= lo && k <= hi) atomicAdd(&sh.hist[(k - lo) >> shift], 1);
         }
-        gt0 += gs;
-        eq0 += es;
-        const unsigned below = (1u << lane) - 1u;
-        g += __popc(bg & below);
-        e += __popc(be & below);
-        if (gt || (eq && e < need)) kept[b.first + g + min(e, need)] = j;
+        tc::cluster_barrier();
+        // four bins a thread, from the top: thread t holds bins kBins-1-4t .. kBins-4-4t
+        const int first = kBins - 4 - 4 * tid;
+        int4 c = make_int4(0, 0, 0, 0);
+        for (uint32_t r = 0; r < C; ++r) {
+            const int4 x = *reinterpret_cast<const int4 *>(peer(&sh.hist[first], r));
+            c.x += x.x; c.y += x.y; c.z += x.z; c.w += x.w;
+        }
+        const int mine = c.x + c.y + c.z + c.w;
+        int x = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) sh.warp_a[warp] = x;
+        __syncthreads();
+        int before = x - mine;
+        for (int w = 0; w < warp; ++w) before += sh.warp_a[w];
+        if (before < need && before + mine >= need) {
+            const int q[4] = {c.w, c.z, c.y, c.x};             // from the top bin down
+            int acc = before, k = 0;
+            while (acc + q[k] < need) acc += q[k++];
+            sh.found_bin = first + 3 - k;
+            sh.found_above = acc;
+            sh.found_count = q[k];
+        }
+        // also: no CTA clears its histogram while another still reads it
+        tc::cluster_barrier();
+        need -= sh.found_above;
+        const uint32_t bin_lo = lo + ((uint32_t)sh.found_bin << shift);
+        hi = (uint32_t)min((unsigned long long)hi, (unsigned long long)bin_lo + ((1ull << shift) - 1ull));   // the last bin may be cut
+        lo = bin_lo;
+        whole = sh.found_count == need;
+        if (shift == 0 || whole) break;
         __syncthreads();
     }
+    // a key stays when it is above hi, or in [lo, hi] and among the first `need`
+    // of those (all of them when whole; else lo == hi: ties, the lowest indices)
+    int gt = 0, eq = 0;
+    const int per_warp = ((cnt + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
+    const int w0 = min(cnt, warp * per_warp), w1 = min(cnt, w0 + per_warp);
+    for (int i = w0 + lane; i < w1; i += 32) {
+        const uint32_t k = key(i);
+        gt += k > hi;
+        eq += k >= lo && k <= hi;
+    }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    if (lane == 0) {
+        sh.warp_a[warp] = gt;
+        sh.warp_b[warp] = eq;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        int g = 0, e = 0;
+        for (int w = 0; w < kSelectWarps; ++w) {
+            g += sh.warp_a[w];
+            e += sh.warp_b[w];
+        }
+        sh.above = g;
+        sh.equal = e;
+    }
+    tc::cluster_barrier();
+    int g0 = 0, e0 = 0;
+    for (uint32_t r = 0; r < rank; ++r) {
+        g0 += *peer(&sh.above, r);
+        e0 += *peer(&sh.equal, r);
+    }
+    for (int w = 0; w < warp; ++w) {
+        g0 += sh.warp_a[w];
+        e0 += sh.warp_b[w];
+    }
+    const unsigned below = (1u << lane) - 1u;
+    for (int base = w0; base < w1; base += 32) {
+        const int i = base + lane;
+        const uint32_t k = i < w1 ? key(i) : 0u;
+        const bool above = i < w1 && k > hi, in = i < w1 && k >= lo && k <= hi;
+        const unsigned bg = __ballot_sync(0xffffffffu, above), be = __ballot_sync(0xffffffffu, in);
+        const int g = g0 + __popc(bg & below), e = e0 + __popc(be & below);
+        if (above || (in && e < need)) kept[b.first + g + min(e, need)] = j0 + i;
+        g0 += __popc(bg);
+        e0 += __popc(be);
+    }
+    tc::cluster_barrier();                     // no CTA leaves while another reads its counts
 }
 
-constexpr int kMoveThreads = 256, kMoveUnroll = 8;
+// -------------------------------------------------------------------- move --
+constexpr int kMoveThreads = 256, kMoveRanks = 128, kMoveUnroll = 8;
 
-// One CTA: a slice of `w` units of the rows of one (sequence, head), of K, of V
-// or the totals.
-template <typename U> __device__ __forceinline__ void move_slice(const EvictArgs &a, U *cache, int units, int c0, int w,
-                                                                 int s, int h, bool totals) {
+// Copies columns [c0, c0 + w) of the chunk's rows of one tensor: 256 / w rows a
+// step, eight steps in flight.
+template <typename U, bool kOrdered>
+__device__ __forceinline__ void move_columns(U *cache, const int64_t *from, const int64_t *to, int64_t stride, int64_t head,
+                                             int units, int c0, int w, int ranks) {
     const int lane = threadIdx.x % w, sub = threadIdx.x / w, per = kMoveThreads / w;
-    const Budget b = budget_of(a, s);
-    const int32_t *kept = a.kept + ((int64_t)s * a.hkv + h) * a.kept_stride;
-    const int c = c0 + lane;
-    const bool col = c < units;
-    const int ps = a.src.page_size;
-    for (int base = 0; base < b.keep; base += per * kMoveUnroll) {
+    const bool col = c0 + lane < units;
+    U *at = cache + head + c0 + lane;
+    for (int base = 0; base < ranks; base += per * kMoveUnroll) {
         U v[kMoveUnroll];
-        int64_t to[kMoveUnroll];
 #pragma unroll
         for (int u = 0; u < kMoveUnroll; ++u) {
             const int i = base + u * per + sub;
-            to[u] = -1;
-            if (i < b.keep && col) {
-                const int64_t from = slot_of(a.src, s, kept[i]), dst = slot_of(a.dst, s, i);
-                if (from < 0 || dst < 0) {
-                    atomicCAS(a.status, 0, PA_DEVICE_RANGE);
-                } else if (from != dst) {
-                    v[u] = cache[totals ? mass_at(from, h, a.hkv, ps) : (from * a.hkv + h) * units + c];
-                    to[u] = totals ? mass_at(dst, h, a.hkv, ps) : (dst * a.hkv + h) * units + c;
-                }
-            }
+            if (i < ranks && col && to[i] >= 0) v[u] = at[from[i] * stride];
         }
-        __syncthreads();       // every read of this chunk before any write of it
+        if (kOrdered) __syncthreads();       // every read of these ranks before any write of them
 #pragma unroll
-        for (int u = 0; u < kMoveUnroll; ++u)
-            if (to[u] >= 0) cache[to[u]] = v[u];
+        for (int u = 0; u < kMoveUnroll; ++u) {
+            const int i = base + u * per + sub;
+            if (i < ranks && col && to[i] >= 0) at[to[i] * stride] = v[u];
+        }
     }
 }
 
-template <typename U>
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(EvictArgs a, int uk, int uv, int w, int nk, int nv) {
+// kOrdered (some page is written in place): part p of a (sequence, head) owns
+// column slice p of all its ranks and walks them upwards.  Otherwise nothing
+// written is read, and part p takes every parts-th chunk of ranks, all columns.
+template <typename U, bool kOrdered>
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(EvictArgs a, int ps_shift, int uk, int uv, int w, int nk, int parts) {
     griddep_wait();
     griddep_launch();
-    const int parts = nk + nv + 1;
+    __shared__ int64_t from[kMoveRanks], to[kMoveRanks];
     const int part = blockIdx.x % parts;
-    const int64_t sh = blockIdx.x / parts;
-    const int h = (int)(sh % a.hkv), s = (int)(sh / a.hkv);
-    if (part < nk)
-        move_slice<U>(a, static_cast<U *>(a.k_cache), uk, part * w, w, s, h, false);
-    else if (part < nk + nv)
-        move_slice<U>(a, static_cast<U *>(a.v_cache), uv, (part - nk) * w, w, s, h, false);
-    else
-        move_slice<float>(a, a.key_mass, 1, 0, 1, s, h, true);
+    const int sh = blockIdx.x / parts;
+    const int h = sh % a.hkv, s = sh / a.hkv;
+    const int32_t *kept = a.kept + ((int64_t)s * a.hkv + h) * a.kept_stride;
+    const int keep = budget_of(a, s).keep, ps = a.src.page_size;
+    U *kc = static_cast<U *>(a.k_cache), *vc = static_cast<U *>(a.v_cache);
+    const int64_t sk = (int64_t)a.hkv * uk, sv = (int64_t)a.hkv * uv;
+    for (int base = kOrdered ? 0 : part * kMoveRanks; base < keep; base += kOrdered ? kMoveRanks : parts * kMoveRanks) {
+        const int ranks = min(kMoveRanks, keep - base);
+        float m = 0.f;
+        int64_t m_to = -1;
+        bool moves = false;
+        __syncthreads();                     // the last chunk's rows are done with
+        if (threadIdx.x < ranks) {
+            const int i = base + threadIdx.x;
+            const int64_t f = slot_of(a.src, s, kept[i], ps_shift), t = slot_of(a.dst, s, i, ps_shift);
+            if (f < 0 || t < 0) atomicCAS(a.status, 0, PA_DEVICE_RANGE);
+            moves = f >= 0 && t >= 0 && f != t;
+            from[threadIdx.x] = f;
+            to[threadIdx.x] = moves ? t : -1;
+            if (moves && (!kOrdered || part == 0)) {
+                m = a.key_mass[mass_at(f, h, a.hkv, ps, ps_shift)];
+                m_to = mass_at(t, h, a.hkv, ps, ps_shift);
+            }
+        }
+        if (!__syncthreads_or(moves)) continue;
+        if (m_to >= 0) a.key_mass[m_to] = m;
+        if (kOrdered) {
+            if (part < nk)
+                move_columns<U, true>(kc, from, to, sk, (int64_t)h * uk, uk, part * w, w, ranks);
+            else
+                move_columns<U, true>(vc, from, to, sv, (int64_t)h * uv, uv, (part - nk) * w, w, ranks);
+        } else {
+            for (int c0 = 0; c0 < uk; c0 += w) move_columns<U, false>(kc, from, to, sk, (int64_t)h * uk, uk, c0, w, ranks);
+            for (int c0 = 0; c0 < uv; c0 += w) move_columns<U, false>(vc, from, to, sv, (int64_t)h * uv, uv, c0, w, ranks);
+        }
+    }
 }
 
-template <typename U> cudaError_t launch_move(const EvictArgs &a, cudaStream_t st) {
+int ps_shift_of(int ps) {
+    if (ps & (ps - 1)) return -1;
+    int s = 0;
+    while ((1 << s) < ps) ++s;
+    return s;
+}
+
+template <typename U> cudaError_t launch_move(const EvictArgs &a, bool in_place, int longest, cudaStream_t st) {
     const int uk = (int)((int64_t)a.d * a.elem / sizeof(U)), uv = (int)((int64_t)a.dv * a.elem / sizeof(U));
+    const int64_t pairs = (int64_t)a.src.sequences * a.hkv;
     int w = 1;
     while (w < 16 && w < (uk > uv ? uk : uv)) w *= 2;
-    const int nk = (uk + w - 1) / w, nv = (uv + w - 1) / w;
-    const int64_t blocks = (int64_t)a.src.sequences * a.hkv * (nk + nv + 1);
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_pdl(move_kernel<U>, dim3((unsigned)blocks), dim3(kMoveThreads), 0, st, a, uk, uv, w, nk, nv);
+    int64_t parts;
+    int nk = 0;
+    if (in_place) {
+        nk = (uk + w - 1) / w;
+        parts = nk + (uv + w - 1) / w;
+    } else {
+        parts = (longest + kMoveRanks - 1) / kMoveRanks;
+        if (parts < 1) parts = 1;
+        if (parts * pairs > INT32_MAX) parts = INT32_MAX / pairs;
+    }
+    if (pairs * parts > INT32_MAX) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)(pairs * parts)), block(kMoveThreads);
+    const int sh = ps_shift_of(a.src.page_size);
+    return in_place ? launch_pdl(move_kernel<U, true>, grid, block, 0, st, a, sh, uk, uv, w, nk, (int)parts)
+                    : launch_pdl(move_kernel<U, false>, grid, block, 0, st, a, sh, uk, uv, w, nk, (int)parts);
+}
+
+// Keys a CTA holds in shared memory at most (half of an SM's).
+constexpr int kStagedKeys = 24576;
+
+cudaError_t launch_select(const EvictArgs &a, int cluster, int room, cudaStream_t st) {
+    const size_t smem = (size_t)room * sizeof(uint32_t);
+    cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kStagedKeys * (int)sizeof(uint32_t));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(a.src.sequences * a.hkv * cluster));
+    cfg.blockDim = dim3(kSelectThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, select_kernel, a, ps_shift_of(a.src.page_size), room);
 }
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictArgs &a, cudaStream_t st) {
-    const int64_t blocks = (int64_t)a.src.sequences * a.hkv;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    cudaError_t e = launch_pdl(select_kernel, dim3((unsigned)blocks), dim3(kSelectThreads), 0, st, a);
+cudaError_t launch_evict(const EvictArgs &a, int longest, int longest_kept, bool in_place, cudaStream_t st) {
+    const int64_t pairs = (int64_t)a.src.sequences * a.hkv;
+    if (pairs > INT32_MAX / 8) return cudaErrorInvalidValue;
+    // CTAs per (sequence, head): enough that the pairs cover the SMs and a part
+    // fits in shared memory, but no part below 2048 keys
+    int cluster = 1;
+    while (cluster < 8 && longest / (2 * cluster) >= 2048 &&
+           (pairs * cluster < 152 || longest / cluster > kStagedKeys))
+        cluster *= 2;
+    const int span = ((longest + cluster - 1) / cluster + 31) / 32 * 32;
+    cudaError_t e = launch_select(a, cluster, span <= kStagedKeys ? span : 0, st);
     if (e != cudaSuccess) return e;
     auto al = [](const void *p, int n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; };
     const int64_t kb = (int64_t)a.d * a.elem, vb = (int64_t)a.dv * a.elem;
     if (kb % 16 == 0 && vb % 16 == 0 && al(a.k_cache, 16) && al(a.v_cache, 16))
-        e = launch_move<uint4>(a, st);
+        e = launch_move<uint4>(a, in_place, longest_kept, st);
     else if (a.elem == 4)
-        e = launch_move<uint32_t>(a, st);
+        e = launch_move<uint32_t>(a, in_place, longest_kept, st);
     else
-        e = launch_move<uint16_t>(a, st);
+        e = launch_move<uint16_t>(a, in_place, longest_kept, st);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }

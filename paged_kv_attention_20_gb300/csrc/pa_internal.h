@@ -174,7 +174,8 @@ struct EvictArgs {
     int32_t kept_stride, sink, recent, hkv, d, dv, elem;
     int32_t *status;
 };
-cudaError_t launch_evict(const EvictArgs &a, cudaStream_t st);
+// longest, longest_kept: of the host copies; in_place: some kept page is the source's own
+cudaError_t launch_evict(const EvictArgs &a, int longest, int longest_kept, bool in_place, cudaStream_t st);
 
 // Device status word (bounded waits record their timeouts here).
 cudaError_t read_device_status(int32_t *code, bool clear);

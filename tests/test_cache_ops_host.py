@@ -111,7 +111,8 @@ def test_evict(built_lib):
     assert call(shared, plan([20, 16], [[0, 1, 2], [0, 4, -1]]), sink=15) == CONFLICT
     assert call(shared, plan([20, 17], [[0, 1, 2], [0, 4, -1]]), sink=16) == STATE     # the shared page stays
     assert call(shared, plan([20, 10], [[5, 6, -1], [7, -1, -1]])) == STATE            # and may be copied from
-    assert call(shared, plan([40, 30], [[0, 1, 2], [0, 4, -1]])) == STATE              # nothing moves
+    assert call(shared, plan([40, 30], [[0, 1, 2], [0, 4, -1]])) == CONFLICT           # the device copy may be longer
+    assert call(src, plan([40, 30], same)) == STATE
     staged = plan([40, 30], same, staged=True), plan([20, 10], same, staged=True)
     assert call(*staged, mass=None) == ARG
     none = plan([], [])
