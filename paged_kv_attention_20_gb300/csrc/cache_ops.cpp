@@ -34,7 +34,7 @@ MassLayout mass_layout(const pa_plan *plan, int32_t hq, int32_t dv, int32_t spli
     l.lse = part;
     l.lse_final = l.lse + align256((size_t)splits * rows * sizeof(float));
     l.groups = l.lse_final + (splits > 1 && plan->n_tiles > 0 ? align256(rows * sizeof(float)) : 0);
-    l.scores = l.groups + align256(((size_t)plan->sequences + 1 + plan->queries) * sizeof(int32_t));
+    l.scores = l.groups + align256((2 * ((size_t)plan->sequences + 1) + plan->queries) * sizeof(int32_t));
     int64_t keys = std::max<int64_t>(max_keys, plan->max_seq_len);
     if (window > 0) keys = std::min<int64_t>(keys, window);
     l.cap = plan->n_decode > 0 ? (keys + 31) / 32 * 32 : 0;
@@ -53,7 +53,8 @@ cudaError_t add_mass(const pa_plan *plan, const AttnArgs &a, const MassLayout &l
     m.scores = a.scores;
     m.cap = a.score_cap;
     m.group_start = reinterpret_cast<int32_t *>(ws + lay.groups);
-    m.group_list = m.group_start + plan->sequences + 1;
+    m.unit_start = m.group_start + plan->sequences + 1;
+    m.group_list = m.unit_start + plan->sequences + 1;
     m.hq = a.hq; m.hkv = a.hkv; m.d = a.d;
     m.splits = a.splits; m.causal = a.causal; m.window = a.window;
     m.scale = a.scale;
@@ -68,11 +69,11 @@ cudaError_t add_mass(const pa_plan *plan, const AttnArgs &a, const MassLayout &l
     }
     if (e == cudaSuccess && plan->n_tiles > 0) {
         // prefill tiles on the tensor-core kernel; otherwise every query of the plan
-        const MassRecords kind = prefill_supported(a) ? kMassTiles : kMassQueries;
-        m.longest = (int32_t)std::max<int64_t>(longest_tile_seq(plan), kind == kMassQueries ? plan->max_seq_len : 0);
-        e = launch_mass_index(m, kind, st);
+        const bool tensor = prefill_supported(a);
+        m.longest = (int32_t)std::max(longest_tile_seq(plan), plan->max_seq_len);
+        e = launch_mass_index(m, tensor ? kMassTiles : kMassQueries, st);
         if (e == cudaSuccess && a.splits > 1) e = launch_lse_final(m, reinterpret_cast<float *>(ws + lay.lse_final), st);
-        if (e == cudaSuccess) e = launch_mass_recompute(m, kind, st);
+        if (e == cudaSuccess) e = tensor ? launch_mass_tiles(m, st) : launch_mass_recompute(m, st);
     }
     return e;
 }

@@ -55,6 +55,22 @@ __device__ __forceinline__ int record_seq(const PlanView &p, int kind, int i) {
 
 constexpr int kIndexThreads = 1024;
 
+// Inclusive prefix sum over the CTA (32 warps); `sums` is scratch of 32 ints.
+__device__ __forceinline__ int block_prefix(int c, int *sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = c;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += sums[w];
+    __syncthreads();
+    return before + x;
+}
+
 // One CTA: group_start[s] .. group_start[s+1] delimit the records of sequence s
 // in group_list, in ascending record order (a stable counting sort).
 __global__ void __launch_bounds__(kIndexThreads) mass_index_kernel(MassArgs a, int kind, int n) {
@@ -62,7 +78,7 @@ __global__ void __launch_bounds__(kIndexThreads) mass_index_kernel(MassArgs a, i
     griddep_launch();
     __shared__ int seqs[kIndexThreads];
     __shared__ int carry, sums[32];
-    const int S = a.plan.sequences, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int S = a.plan.sequences, tid = threadIdx.x;
     for (int s = tid; s <= S; s += kIndexThreads) a.group_start[s] = 0;
     __syncthreads();
     for (int i = tid; i < n; i += kIndexThreads) atomicAdd(&a.group_start[record_seq(a.plan, kind, i)], 1);
@@ -73,21 +89,10 @@ __global__ void __launch_bounds__(kIndexThreads) mass_index_kernel(MassArgs a, i
     for (int base = 0; base <= S; base += kIndexThreads) {
         const int s = base + tid;
         const int c = s < S ? a.group_start[s] : 0;
-        int x = c;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) sums[warp] = x;
+        const int x = block_prefix(c, sums);
+        if (s <= S) a.group_start[s] = carry + x - c;
         __syncthreads();
-        int before = carry, all = 0;
-        for (int w = 0; w < 32; ++w) {
-            if (w < warp) before += sums[w];
-            all += sums[w];
-        }
-        if (s <= S) a.group_start[s] = before + x - c;
-        __syncthreads();
-        if (tid == 0) carry += all;
+        if (tid == kIndexThreads - 1) carry += x;
         __syncthreads();
     }
     for (int base = 0; base < n; base += kIndexThreads) {
@@ -117,53 +122,110 @@ __global__ void __launch_bounds__(kIndexThreads) mass_index_kernel(MassArgs a, i
         if (s <= S) a.group_start[s] = v;
         __syncthreads();
     }
+    if (kind != kMassTiles) return;
+    // blocks of 128 keys of the sequences that have tiles, and their prefix sums
+    if (tid == 0) carry = 0;
+    __syncthreads();
+    for (int base = 0; base <= S; base += kIndexThreads) {
+        const int s = base + tid;
+        const int c = s < S && a.group_start[s + 1] > a.group_start[s] ? (a.plan.seq_lens[s] + 127) / 128 : 0;
+        const int x = block_prefix(c, sums);
+        if (s <= S) a.unit_start[s] = carry + x - c;
+        __syncthreads();
+        if (tid == kIndexThreads - 1) carry += x;
+        __syncthreads();
+    }
 }
 
 // ------------------------------------------------------------ decode items --
-constexpr int kItemThreads = 256;
-constexpr int kMaxStagedHeads = 128;
+constexpr int kItemThreads = 256, kItemWarps = kItemThreads / 32;
+constexpr int kItemKeys = 4 * kItemThreads;     // four keys a thread and step
+constexpr int kMaxStagedHeads = 64;
 
-// One CTA per (sequence or item, KV head, block of keys), a key per thread and
-// step; the CTA strides over the blocks of its keys.
-__global__ void __launch_bounds__(kItemThreads) mass_items_kernel(MassArgs a, int repeated, int blocks) {
+// One CTA per (sequence or item, KV head, block of keys): four consecutive keys
+// per thread and step, the group's heads in turn.  The scores come from L2 when
+// they fit there (4 bytes a key and head), the totals are read and written once.
+// Key j always falls to block (j / kItemKeys) % blocks and to one thread of it,
+// whatever an item's own range: the items of a sequence never meet on a key.
+// kQuads: pages hold whole aligned fours of keys and the totals are 16-byte
+// aligned.
+template <bool kQuads>
+__global__ void __launch_bounds__(kItemThreads) mass_items_kernel(MassArgs a, int repeated, int blocks, int ps_shift) {
     griddep_wait();
     griddep_launch();
     __shared__ float lse[kMaxStagedHeads];
     const int blk = blockIdx.x % blocks;
     const int rest = blockIdx.x / blocks;
     const int kvh = rest % a.hkv, unit = rest / a.hkv;
-    const int G = a.hq / a.hkv;
+    const int G = a.hq / a.hkv, ps = a.plan.page_size;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int first = repeated ? a.group_start[unit] : unit, last = repeated ? a.group_start[unit + 1] : unit + 1;
+    const int64_t rows = (int64_t)a.plan.queries * a.hq;
     for (int e = first; e < last; ++e) {
         const int item = repeated ? a.group_list[e] : e;
         const int qi = a.plan.decode[item];
         const int4 meta = a.plan.qmeta[qi];
-        int64_t lo, hi;
-        visible_range(meta.y, a.plan.seq_lens[meta.x], a.causal, a.window, lo, hi);
+        int64_t lo64, hi64;
+        visible_range(meta.y, a.plan.seq_lens[meta.x], a.causal, a.window, lo64, hi64);
+        const int lo = (int)lo64, hi = (int)hi64;       // positions fit 32 bits
         if (hi - lo > a.cap) {
             // the workspace holds no scores past cap: this item adds nothing
             if (threadIdx.x == 0) atomicCAS(a.status, 0, PA_DEVICE_RANGE);
             continue;
         }
+        const int64_t step = (int64_t)blocks * kItemKeys;
+        const int64_t start = lo / step * step + (int64_t)blk * kItemKeys;
+        if (start >= hi || (start + kItemKeys <= lo && start + step >= hi)) continue;   // nothing here (uniform)
         const int32_t *trow = a.plan.table + (int64_t)meta.x * a.plan.width;
-        const int ps = a.plan.page_size;
         for (int g0 = 0; g0 < G; g0 += kMaxStagedHeads) {
             const int gn = min(G - g0, kMaxStagedHeads);
             __syncthreads();
-            for (int g = threadIdx.x; g < gn; g += kItemThreads)
-                lse[g] = merged_lse2(a, (int64_t)qi * a.hq + kvh * G + g0 + g);
+            // a head per warp: its log-sum-exp over the splits (two a lane, at most 64), log2 units
+            for (int g = warp; g < gn; g += kItemWarps) {
+                const int64_t row = (int64_t)qi * a.hq + kvh * G + g0 + g;
+                const float l0 = lane < a.splits ? a.lse[lane * rows + row] * kLog2e : -INFINITY;
+                const float l1 = lane + 32 < a.splits ? a.lse[(lane + 32) * rows + row] * kLog2e : -INFINITY;
+                float m = fmaxf(l0, l1);
+                for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                float t = (l0 == -INFINITY ? 0.f : exp2f(l0 - m)) + (l1 == -INFINITY ? 0.f : exp2f(l1 - m));
+                for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+                if (lane == 0) lse[g] = a.splits == 1 ? l0 : m + log2f(t);
+            }
             __syncthreads();
-            // key j always falls to block (j / kItemThreads) % blocks, whatever the
-            // item's own range: the items of a sequence never meet on a key from
-            // two CTAs
-            const int64_t step = (int64_t)blocks * kItemThreads;
-            for (int64_t j = lo / step * step + (int64_t)blk * kItemThreads + threadIdx.x; j < hi; j += step) {
-                if (j < lo) continue;
-                const float *sc = a.scores + ((int64_t)item * a.hq + kvh * G + g0) * a.cap + (j - lo);
-                float p = 0.f;
-                for (int g = 0; g < gn; ++g) p += exp2f(sc[g * a.cap] - lse[g]);
-                const int64_t page = trow[j / ps];
-                a.key_mass[(page * a.hkv + kvh) * ps + j % ps] += p;
+            const float *head0 = a.scores + ((int64_t)item * a.hq + kvh * G + g0) * a.cap - lo;
+            for (int64_t base = start; base < hi; base += step) {
+                const int j = (int)base + 4 * (int)threadIdx.x;
+                if (j >= hi || j + 4 <= lo) continue;
+                const float *sc = head0 + j;
+                const bool all = j >= lo && j + 4 <= hi;
+                float p[4] = {0.f, 0.f, 0.f, 0.f};
+                if (all && (lo & 3) == 0) {
+#pragma unroll 4
+                    for (int g = 0; g < gn; ++g) {
+                        const float4 v = *reinterpret_cast<const float4 *>(sc + g * a.cap);
+                        const float l = lse[g];
+                        p[0] += exp2f(v.x - l); p[1] += exp2f(v.y - l); p[2] += exp2f(v.z - l); p[3] += exp2f(v.w - l);
+                    }
+                } else {
+                    for (int g = 0; g < gn; ++g)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (j + i >= lo && j + i < hi) p[i] += exp2f(sc[g * a.cap + i] - lse[g]);
+                }
+                if (kQuads && all) {
+                    const int pg = ps_shift >= 0 ? j >> ps_shift : j / ps;
+                    float4 *m = reinterpret_cast<float4 *>(a.key_mass + ((int64_t)trow[pg] * a.hkv + kvh) * ps + (j - pg * ps));
+                    float4 v = *m;
+                    v.x += p[0]; v.y += p[1]; v.z += p[2]; v.w += p[3];
+                    *m = v;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (j + i >= lo && j + i < hi) {
+                            const int pg = (j + i) / ps;
+                            a.key_mass[((int64_t)trow[pg] * a.hkv + kvh) * ps + (j + i - pg * ps)] += p[i];
+                        }
+                }
             }
         }
     }
@@ -176,7 +238,7 @@ constexpr int kReThreads = 256, kReKeys = 32, kReRows = kReThreads / kReKeys;
 // memory (fp32), the sequence's queries stream past, eight (query, head) rows at
 // a time, one dot product per thread.
 template <typename T>
-__global__ void __launch_bounds__(kReThreads) mass_recompute_kernel(MassArgs a, int kind, int blocks) {
+__global__ void __launch_bounds__(kReThreads) mass_recompute_kernel(MassArgs a, int blocks) {
     griddep_wait();
     griddep_launch();
     extern __shared__ float sm[];
@@ -203,9 +265,7 @@ __global__ void __launch_bounds__(kReThreads) mass_recompute_kernel(MassArgs a, 
         }
         float sum = 0.f;
         for (int e = first; e < last; ++e) {
-            const int rec = a.group_list[e];
-            const int q0 = kind == kMassTiles ? a.plan.tiles[rec].y : rec;
-            const int nrows = (kind == kMassTiles ? a.plan.tiles[rec].z : 1) * G;
+            const int q0 = a.group_list[e], nrows = G;
             for (int r0 = 0; r0 < nrows; r0 += kReRows) {
                 // any row of these eight that sees a key of the block?
                 const int r = r0 + slot;
@@ -249,14 +309,13 @@ int blocks_for(int64_t units, int64_t want) {
     return (int)(b < 1 ? 1 : b);
 }
 
-template <typename T> cudaError_t launch_re(const MassArgs &a, MassRecords kind, cudaStream_t st) {
+template <typename T> cudaError_t launch_re(const MassArgs &a, cudaStream_t st) {
     const size_t smem = (size_t)(kReKeys * (a.d | 1) + kReRows * a.d) * sizeof(float);
     cudaError_t e = cudaFuncSetAttribute(mass_recompute_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)a.plan.sequences * a.hkv;
     const int blocks = blocks_for(units, ((int64_t)a.longest + kReKeys - 1) / kReKeys);
-    return launch_pdl(mass_recompute_kernel<T>, dim3((unsigned)(units * blocks)), dim3(kReThreads), smem, st, a, (int)kind,
-                      blocks);
+    return launch_pdl(mass_recompute_kernel<T>, dim3((unsigned)(units * blocks)), dim3(kReThreads), smem, st, a, blocks);
 }
 
 }  // namespace
@@ -273,19 +332,26 @@ cudaError_t launch_lse_final(const MassArgs &a, float *out, cudaStream_t st) {
 
 cudaError_t launch_mass_items(const MassArgs &a, bool repeated, cudaStream_t st) {
     const int64_t units = (int64_t)(repeated ? a.plan.sequences : a.plan.n_decode) * a.hkv;
-    const int blocks = blocks_for(units, ((int64_t)a.longest + kItemThreads - 1) / kItemThreads);
-    cudaError_t e = launch_pdl(mass_items_kernel, dim3((unsigned)(units * blocks)), dim3(kItemThreads), 0, st, a,
-                               repeated ? 1 : 0, blocks);
+    const int blocks = blocks_for(units, ((int64_t)a.longest + kItemKeys - 1) / kItemKeys);
+    const int ps = a.plan.page_size;
+    int shift = -1;
+    if ((ps & (ps - 1)) == 0)
+        for (shift = 0; (1 << shift) < ps; ++shift) {}
+    const bool quads = ps % 4 == 0 && reinterpret_cast<uintptr_t>(a.key_mass) % 16 == 0;
+    const dim3 grid((unsigned)(units * blocks)), block(kItemThreads);
+    const int rep = repeated ? 1 : 0;
+    cudaError_t e = quads ? launch_pdl(mass_items_kernel<true>, grid, block, 0, st, a, rep, blocks, shift)
+                          : launch_pdl(mass_items_kernel<false>, grid, block, 0, st, a, rep, blocks, shift);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 
-cudaError_t launch_mass_recompute(const MassArgs &a, MassRecords kind, cudaStream_t st) {
+cudaError_t launch_mass_recompute(const MassArgs &a, cudaStream_t st) {
     cudaError_t e;
     switch (a.dtype) {
-        case PA_F32: e = launch_re<float>(a, kind, st); break;
-        case PA_F16: e = launch_re<__half>(a, kind, st); break;
-        default: e = launch_re<__nv_bfloat16>(a, kind, st); break;
+        case PA_F32: e = launch_re<float>(a, st); break;
+        case PA_F16: e = launch_re<__half>(a, st); break;
+        default: e = launch_re<__nv_bfloat16>(a, st); break;
     }
     if (e != cudaSuccess) return e;
     return cudaGetLastError();

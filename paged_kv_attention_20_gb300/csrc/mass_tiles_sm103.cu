@@ -1,0 +1,386 @@
+// Per-key totals of prefill tiles on tcgen05 tensor cores.
+//
+// The attention has run and left every query's log-sum-exp.  For a block of 128
+// keys of one sequence and KV head this kernel recomputes the scores against all
+// the sequence's tile queries and adds up the weights:
+//   total_j += sum over (query n, head h of the group) of 2^(scale_log2 * k_j . q_n - lse_n)
+// The keys are the M rows of the MMA (S^T = K Q^T: K stays in shared memory, Q
+// tiles of 128 queries of one head stream past), so a key is a TMEM lane and its
+// sum lives in one thread's register: no exchange between threads, no atomics,
+// one fixed order, one add to memory per key.  A step (128 keys x 128 queries)
+// costs 2 * 128^3 flops on the tensor core and 128^2 exponentials; P is never
+// written and V never read.  The exponentials bound it (16384 per step and SM
+// quarter rate) before the tensor core does; two CTAs of 96 KB per SM keep one's
+// exponentials running over the other's waits.
+//
+// Roles: warps 0-3 add up (thread r = key row r), warp 4 walks the CTA's units
+// and loads K (one box per page and 64-column half), Q and the log-sum-exps, warp 5
+// issues the MMAs.  A ring of step descriptors in shared memory tells warps 0-3
+// and 5 what each step is.  All waits are bounded (timeout -> device status word).
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "pa_internal.h"
+#include "sm103_tc.cuh"
+#include "tma_host.h"
+
+namespace pa {
+namespace {
+
+using namespace tc;
+
+constexpr int kKeys = 128;              // keys per unit: MMA rows
+constexpr int kQ = 128;                 // queries per step: MMA columns
+constexpr int kD = 128;                 // head dim
+constexpr int kHalf = 128 * 128;        // bytes of 128 rows x 64 columns
+constexpr int kTile = 2 * kHalf;
+constexpr int kStages = 2;              // Q ring and S buffers
+constexpr int kSlots = 4;               // step descriptors
+constexpr int kThreads = 192;
+constexpr uint32_t kTmemCols = kStages * kQ;
+constexpr float kLog2e = 1.4426950408889634f;
+
+enum StepKind { kWork = 0, kUnitEnd = 1, kExit = 2 };
+
+struct Step {
+    int kind, first;        // first: this step opens a unit (its K tile is new)
+    int pos0, nq;           // position of column 0, live columns
+    int key0, seq_len, kvh;
+    int trow_lo, trow_hi;   // block-table row
+};
+
+struct Smem {
+    uint8_t k[kTile];
+    uint8_t q[kStages][kTile];
+    float lse[kSlots][kQ];                    // log2 units
+    Step step[kSlots];
+    uint64_t k_full, k_empty;
+    uint64_t q_full[kStages], q_empty[kStages];
+    uint64_t s_full[kStages], s_empty[kStages];
+    uint64_t d_full[kSlots], d_empty[kSlots];
+    uint32_t tmem_base;
+};
+
+struct TileParams {
+    PlanView plan;
+    float *key_mass;
+    const float *lse;                         // [queries, Hq], natural log
+    const int32_t *group_start, *group_list;  // tiles by sequence
+    const int32_t *unit_start;                // [sequences + 1] key blocks before a sequence
+    int hq, hkv, causal, window, bf16;
+    float scale_log2;
+    int32_t *status;
+};
+
+__global__ void __launch_bounds__(kThreads, 2)
+    mass_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, TileParams prm) {
+    griddep_wait();
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    if ((smem_u32(smem_raw) & 1023u) != 0u) {
+        if (threadIdx.x == 0) atomicCAS(prm.status, 0, PA_DEVICE_LAYOUT);
+        return;
+    }
+    Smem &s = *reinterpret_cast<Smem *>(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int ps = prm.plan.page_size, G = prm.hq / prm.hkv;
+
+    if (tid == 0) {
+        mbar_init(&s.k_full, 1);
+        mbar_init(&s.k_empty, 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&s.q_full[i], 1);
+            mbar_init(&s.q_empty[i], 1);
+            mbar_init(&s.s_full[i], 1);
+            mbar_init(&s.s_empty[i], 128);
+        }
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&s.d_full[i], 1);
+            mbar_init(&s.d_empty[i], 5);      // four adding warps and the MMA issuer
+        }
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&s.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem_base;
+
+    if (warp == 4) {
+        // ---------------------------------------------------- producer --
+        if (lane == 0) {
+            tma_prefetch_desc(&tm_q);
+            tma_prefetch_desc(&tm_k);
+        }
+        const int S = prm.plan.sequences;
+        const int units = prm.unit_start[S] * prm.hkv;
+        const int oob_row = prm.plan.pages * ps;
+        const int boxes = kKeys / ps;
+        int t = 0, d = 0, u_open = 0;          // steps, descriptors and units (K loads) so far
+        bool go = true;
+        // lane 0 waits, the warp follows
+        auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+            int ok = 1;
+            if (lane == 0) ok = mbar_wait(bar, parity) ? 1 : 0;
+            return __shfl_sync(0xffffffffu, ok, 0) != 0;
+        };
+        auto open_slot = [&]() -> bool { return d < kSlots || wait(&s.d_empty[d % kSlots], (uint32_t)((d / kSlots - 1) & 1)); };
+        auto publish = [&](const Step &st) {
+            if (lane == 0) s.step[d % kSlots] = st;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.d_full[d % kSlots]);
+            ++d;
+        };
+        for (int u = blockIdx.x; go && u < units; u += gridDim.x) {
+            const int blk = u / prm.hkv, kvh = u - blk * prm.hkv;
+            // the sequence whose blocks hold blk: last one that starts at or before it
+            int seq = 0;
+            for (int n = S; n > 1;) {
+                const int step = (n + 31) / 32, at = lane * step;
+                const bool le = at < n && prm.unit_start[seq + at] <= blk;
+                const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;
+                seq += k * step;
+                n = min(step, n - k * step);
+            }
+            Step st{};
+            st.kvh = kvh;
+            st.key0 = (blk - prm.unit_start[seq]) * kKeys;
+            st.seq_len = prm.plan.seq_lens[seq];
+            const int32_t *trow = prm.plan.table + (int64_t)seq * prm.plan.width;
+            st.trow_lo = (int32_t)(uint32_t)reinterpret_cast<uint64_t>(trow);
+            st.trow_hi = (int32_t)(uint32_t)(reinterpret_cast<uint64_t>(trow) >> 32);
+            const int used_pages = (st.seq_len + ps - 1) / ps;
+            const int e1 = prm.group_start[seq + 1];
+            bool open = false;
+            for (int e = prm.group_start[seq]; go && e < e1; ++e) {
+                const int4 tile = prm.plan.tiles[prm.group_list[e]];
+                st.pos0 = tile.w;
+                st.nq = tile.z;
+                const int hi = prm.causal ? st.pos0 + st.nq : st.seq_len;
+                const int64_t lo = prm.window > 0 ? (int64_t)st.pos0 - prm.window + 1 : 0;
+                if (st.key0 >= hi || (int64_t)st.key0 + kKeys <= lo) continue;
+                for (int g = 0; go && g < G; ++g) {
+                    const int h = kvh * G + g;
+                    // log-sum-exps of the step's columns: loads first, they land during the waits
+                    float l[kQ / 32];
+#pragma unroll
+                    for (int i = 0; i < kQ / 32; ++i) {
+                        const int c = lane + 32 * i;
+                        l[i] = c < st.nq ? prm.lse[(int64_t)(tile.y + c) * prm.hq + h] * kLog2e : 0.f;
+                    }
+                    if (!open) {
+                        if (u_open > 0 && !wait(&s.k_empty, (uint32_t)((u_open - 1) & 1))) { go = false; break; }
+                        ++u_open;
+                        if (lane == 0) mbar_arrive_expect_tx(&s.k_full, kTile);
+                        __syncwarp();
+                        if (lane < boxes) {
+                            const int lp = st.key0 / ps + lane;
+                            const int row = lp < used_pages ? trow[lp] * ps : oob_row;
+                            tma_load_3d(s.k + lane * ps * 128, &tm_k, 0, kvh, row, &s.k_full);
+                            tma_load_3d(s.k + kHalf + lane * ps * 128, &tm_k, 64, kvh, row, &s.k_full);
+                        }
+                    }
+                    const int b = t % kStages;
+                    if (t >= kStages && !wait(&s.q_empty[b], (uint32_t)((t / kStages - 1) & 1))) { go = false; break; }
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&s.q_full[b], kTile);
+                        tma_load_3d(s.q[b], &tm_q, 0, h, tile.y, &s.q_full[b]);
+                        tma_load_3d(s.q[b] + kHalf, &tm_q, 64, h, tile.y, &s.q_full[b]);
+                    }
+                    ++t;
+                    if (!open_slot()) { go = false; break; }
+#pragma unroll
+                    for (int i = 0; i < kQ / 32; ++i) s.lse[d % kSlots][lane + 32 * i] = l[i];
+                    st.kind = kWork;
+                    st.first = open ? 0 : 1;
+                    open = true;
+                    publish(st);
+                }
+            }
+            if (go && open) {
+                st.kind = kUnitEnd;
+                go = open_slot();
+                if (go) publish(st);
+            }
+        }
+        if (go && open_slot()) {
+            Step st{};
+            st.kind = kExit;
+            publish(st);
+        } else if (lane == 0) {
+            atomicCAS(prm.status, 0, PA_DEVICE_TIMEOUT_TMA);
+        }
+        // leave only when the last loads have landed (on a timeout some may be unread)
+        if (lane == 0) {
+            for (int i = t > kStages ? t - kStages : 0; i < t; ++i)
+                mbar_wait(&s.q_full[i % kStages], (uint32_t)((i / kStages) & 1), 2000000ll);
+            if (u_open > 0) mbar_wait(&s.k_full, (uint32_t)((u_open - 1) & 1), 2000000ll);
+        }
+    } else if (warp == 5) {
+        // -------------------------------------------------- MMA issuer --
+        if (lane == 0) {
+            const uint32_t idesc = idesc_f16(kKeys, kQ, prm.bf16 != 0, false, false);
+            const uint64_t k_desc = smem_desc(smem_u32(s.k), 16, 1024, kLayoutSwizzle128B);
+            int t = 0, units = 0;
+            bool ok = true;
+            for (int d = 0;; ++d) {
+                if (!mbar_wait(&s.d_full[d % kSlots], (uint32_t)((d / kSlots) & 1))) { ok = false; break; }
+                const int kind = s.step[d % kSlots].kind, first = s.step[d % kSlots].first;
+                mbar_arrive(&s.d_empty[d % kSlots]);
+                if (kind == kExit) break;
+                if (kind == kUnitEnd) {
+                    mma_commit(&s.k_empty);          // K is free once the unit's MMAs are done
+                    continue;
+                }
+                const int b = t % kStages;
+                if (first && !mbar_wait(&s.k_full, (uint32_t)(units++ & 1))) { ok = false; break; }
+                if (!mbar_wait(&s.q_full[b], (uint32_t)((t / kStages) & 1))) { ok = false; break; }
+                if (t >= kStages && !mbar_wait(&s.s_empty[b], (uint32_t)((t / kStages - 1) & 1))) { ok = false; break; }
+                tc_fence_after();
+                const uint64_t q_desc = smem_desc(smem_u32(s.q[b]), 16, 1024, kLayoutSwizzle128B);
+#pragma unroll
+                for (int ks = 0; ks < kD / 16; ++ks) {
+                    const uint64_t o = (uint64_t)(((ks / 4) * kHalf + (ks % 4) * 32) >> 4);
+                    mma_f16_ss(tmem + (uint32_t)(b * kQ), k_desc + o, q_desc + o, idesc, ks > 0 ? 1u : 0u);
+                }
+                mma_commit(&s.s_full[b]);
+                mma_commit(&s.q_empty[b]);
+                ++t;
+            }
+            if (!ok) atomicCAS(prm.status, 0, PA_DEVICE_TIMEOUT_MMA);
+        }
+    } else {
+        // ------------------------------------------------ adding warps --
+        const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
+        const float2 sc2 = make_float2(prm.scale_log2, prm.scale_log2);
+        float total = 0.f;
+        int t = 0;
+        bool ok = true;
+        for (int d = 0;; ++d) {
+            const int sl = d % kSlots;
+            ok = __all_sync(0xffffffffu, mbar_wait(&s.d_full[sl], (uint32_t)((d / kSlots) & 1)));
+            if (!ok) break;
+            const Step st = s.step[sl];
+            if (st.kind == kExit) break;
+            const int j = st.key0 + tid;               // my key
+            if (st.kind == kUnitEnd) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.d_empty[sl]);
+                if (j < st.seq_len && !(total == 0.f)) {
+                    const int32_t *trow = reinterpret_cast<const int32_t *>((uint64_t)(uint32_t)st.trow_lo |
+                                                                            ((uint64_t)(uint32_t)st.trow_hi << 32));
+                    const int64_t page = trow[j / ps];
+                    prm.key_mass[(page * prm.hkv + st.kvh) * ps + j % ps] += total;
+                }
+                total = 0.f;
+                continue;
+            }
+            const int b = t % kStages;
+            ok = __all_sync(0xffffffffu, mbar_wait(&s.s_full[b], (uint32_t)((t / kStages) & 1)));
+            if (!ok) break;
+            ++t;
+            tc_fence_after();
+            // columns (queries) that see my key: an interval
+            int n0 = prm.causal ? j - st.pos0 : 0, n1 = st.nq - 1;
+            if (prm.window > 0) n1 = (int)min((int64_t)n1, (int64_t)j - st.pos0 + prm.window - 1);
+            const bool edge = n0 > 0 || n1 < kQ - 1;
+            const float4 *ls = reinterpret_cast<const float4 *>(s.lse[sl]);
+            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            if (!__any_sync(0xffffffffu, edge)) {
+#pragma unroll
+                for (int c = 0; c < kQ; c += 32) {
+                    float v[32];
+                    tmem_ld32f(tmem + lane_off + (uint32_t)(b * kQ + c), v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 l = ls[(c + i) / 4];
+                        const float2 x = ffma2(make_float2(v[i], v[i + 1]), sc2, make_float2(-l.x, -l.y));
+                        const float2 y = ffma2(make_float2(v[i + 2], v[i + 3]), sc2, make_float2(-l.z, -l.w));
+                        acc[0] = fadd2(acc[0], make_float2(ex2(x.x), ex2(x.y)));
+                        acc[1] = fadd2(acc[1], make_float2(ex2(y.x), ex2(y.y)));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < kQ; c += 32) {
+                    float v[32];
+                    tmem_ld32f(tmem + lane_off + (uint32_t)(b * kQ + c), v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 x = ffma2(make_float2(v[i], v[i + 1]), sc2,
+                                               make_float2(-s.lse[sl][c + i], -s.lse[sl][c + i + 1]));
+                        // columns outside the interval hold other queries' scores, NaN included
+                        acc[0] = fadd2(acc[0], make_float2(c + i >= n0 && c + i <= n1 ? ex2(x.x) : 0.f,
+                                                           c + i + 1 >= n0 && c + i + 1 <= n1 ? ex2(x.y) : 0.f));
+                    }
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&s.s_empty[b]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.d_empty[sl]);
+            const float2 sum = fadd2(acc[0], acc[1]);
+            total += sum.x + sum.y;
+        }
+        if (!ok && lane == 0) atomicCAS(prm.status, 0, PA_DEVICE_TIMEOUT_SOFTMAX);
+    }
+    griddep_launch();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+bool make_map(CUtensorMap *m, const void *base, int heads, int64_t rows, int box_rows, bool bf16) {
+    return encode_map_3d(m, base, bf16, kD, (uint64_t)heads, (uint64_t)rows, (uint64_t)kD * 2, (uint64_t)kD * 2 * heads, 64,
+                         1, (uint32_t)box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+}  // namespace
+
+cudaError_t launch_mass_tiles(const MassArgs &a, cudaStream_t st) {
+    const bool bf16 = a.dtype == PA_BF16;
+    CUtensorMap tq, tk;
+    if (!make_map(&tq, a.q, a.hq, a.plan.queries, kQ, bf16) ||
+        !make_map(&tk, a.k, a.hkv, (int64_t)a.plan.pages * a.plan.page_size, a.plan.page_size, bf16))
+        return cudaErrorInvalidValue;
+    static int resident = 0;
+    if (resident == 0) {
+        cudaError_t e = cudaFuncSetAttribute(mass_tiles_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+        if (e != cudaSuccess) return e;
+        int per_sm = 0, dev = 0, sms = 0;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, mass_tiles_kernel, kThreads, sizeof(Smem));
+        if (e != cudaSuccess) return e;
+        e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        if (per_sm > 2) per_sm = 2;             // tensor memory: 256 columns each
+        resident = per_sm * sms > 0 ? per_sm * sms : 1;
+    }
+    TileParams prm{};
+    prm.plan = a.plan;
+    prm.key_mass = a.key_mass;
+    prm.lse = a.lse_final;
+    prm.group_start = a.group_start;
+    prm.group_list = a.group_list;
+    prm.unit_start = a.unit_start;
+    prm.hq = a.hq; prm.hkv = a.hkv;
+    prm.causal = a.causal; prm.window = a.window;
+    prm.bf16 = bf16 ? 1 : 0;
+    prm.scale_log2 = a.scale * kLog2e;
+    prm.status = a.status;
+    cudaError_t e = launch_pdl(mass_tiles_kernel, dim3((unsigned)resident), dim3(kThreads), sizeof(Smem), st, tq, tk, prm);
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+}  // namespace pa

@@ -150,6 +150,7 @@ struct MassArgs {
     int64_t cap;
     int32_t *group_start;     // [sequences + 1] records grouped by sequence (launch_mass_index)
     int32_t *group_list;      // [records]
+    int32_t *unit_start;      // [sequences + 1] blocks of 128 keys before a sequence that has tiles
     int32_t hq, hkv, d, splits, causal, window;
     float scale;
     pa_dtype dtype;
@@ -162,8 +163,10 @@ cudaError_t launch_mass_index(const MassArgs &a, MassRecords kind, cudaStream_t 
 cudaError_t launch_lse_final(const MassArgs &a, float *out, cudaStream_t st);
 // Decode items from their stored scores; `repeated`: sequences may have several items (grouped first).
 cudaError_t launch_mass_items(const MassArgs &a, bool repeated, cudaStream_t st);
-// Grouped tiles or queries, scores recomputed.
-cudaError_t launch_mass_recompute(const MassArgs &a, MassRecords kind, cudaStream_t st);
+// Grouped tiles, scores recomputed on the tensor cores (prefill_supported shapes).
+cudaError_t launch_mass_tiles(const MassArgs &a, cudaStream_t st);
+// Grouped queries of any shape, scores recomputed.
+cudaError_t launch_mass_recompute(const MassArgs &a, cudaStream_t st);
 
 // Eviction (paged_kv_evict).
 struct EvictArgs {
