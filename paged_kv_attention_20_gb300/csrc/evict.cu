@@ -35,11 +35,12 @@ __device__ __forceinline__ int64_t mass_at(int64_t slot, int h, int hkv, int ps,
     return (pg * hkv + h) * ps + (slot - pg * ps);
 }
 
-// Keys whose unsigned order is the order of the totals: NaN lowest, -0 = +0.
+// Keys whose unsigned order is the order of the totals: 0 is no key at all, NaN
+// counts below every number, -0 = +0.
 __device__ __forceinline__ uint32_t order_key(float x) {
-    if (x != x) return 0u;
+    if (x != x) return 1u;
     const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return ((u & 0x80000000u) ? ~u : (u | 0x80000000u)) + 1u;    // -inf: 0x00800000, +inf: 0xff800001
 }
 
 struct Budget {
@@ -85,12 +86,13 @@ template <typename V> __device__ __forceinline__ const V *peer(const V *p, uint3
     return reinterpret_cast<const V *>(out);
 }
 
-// room: keys the dynamic shared memory holds.  A part that is longer (the device
-// lengths can exceed the host's that sized the launch) is re-read instead.
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictArgs a, int ps_shift, int room) {
+// room: fours of keys the dynamic shared memory holds.  A part that is longer
+// (the device lengths can exceed the host's that sized the launch) is re-read
+// instead.  quads: the totals of four keys at a multiple of four lie together.
+__global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(EvictArgs a, int ps_shift, int room, int quads) {
     griddep_wait();
     griddep_launch();
-    extern __shared__ uint32_t staged[];
+    extern __shared__ uint4 staged[];
     __shared__ __align__(16) SelectShared sh;
     const uint32_t C = tc::cluster_nctarank(), rank = tc::cluster_ctarank();
     const int pair = (int)(blockIdx.x / C);
@@ -108,30 +110,48 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictArgs a, int
     for (int i = me; i < b.n - b.last; i += all) kept[b.first + b.want + i] = b.last + i;
     if (b.want == 0) return;
 
-    // my part of the candidates: whole warps of 32 keys
-    const int n = b.last - b.first;
-    const int span = ((n + (int)C - 1) / (int)C + 31) / 32 * 32;
-    const int part0 = min(n, (int)rank * span), cnt = min(n, part0 + span) - part0;
-    const int j0 = b.first + part0;
-    auto fetch = [&](int i) -> uint32_t {
-        const int64_t slot = slot_of(a.src, s, j0 + i, ps_shift);
-        if (slot < 0) {
-            atomicCAS(a.status, 0, PA_DEVICE_RANGE);
-            return 0u;
+    // the candidates as aligned fours (places outside [first, last) hold no key), my
+    // part of them
+    const int j0 = b.first & ~3, fours = (b.last - j0 + 3) / 4;
+    const int span = (fours + (int)C - 1) / (int)C;
+    const int part0 = min(fours, (int)rank * span), cnt = min(fours, part0 + span) - part0;
+    auto fetch = [&](int q) -> uint4 {
+        const int j = j0 + 4 * (part0 + q);
+        float m[4] = {0.f, 0.f, 0.f, 0.f};
+        if (quads) {
+            const int64_t slot = slot_of(a.src, s, j, ps_shift);
+            if (slot < 0) {
+                atomicCAS(a.status, 0, PA_DEVICE_RANGE);
+            } else {
+                const float4 v = *reinterpret_cast<const float4 *>(a.key_mass + mass_at(slot, h, a.hkv, a.src.page_size, ps_shift));
+                m[0] = v.x; m[1] = v.y; m[2] = v.z; m[3] = v.w;
+            }
+        } else {
+            for (int i = 0; i < 4; ++i) {
+                if (j + i < b.first || j + i >= b.last) continue;
+                const int64_t slot = slot_of(a.src, s, j + i, ps_shift);
+                if (slot < 0)
+                    atomicCAS(a.status, 0, PA_DEVICE_RANGE);
+                else
+                    m[i] = a.key_mass[mass_at(slot, h, a.hkv, a.src.page_size, ps_shift)];
+            }
         }
-        return order_key(a.key_mass[mass_at(slot, h, a.hkv, a.src.page_size, ps_shift)]);
+        auto k = [&](int i) { return j + i >= b.first && j + i < b.last ? order_key(m[i]) : 0u; };
+        return make_uint4(k(0), k(1), k(2), k(3));
     };
     const bool fits = span <= room;
-    auto key = [&](int i) -> uint32_t { return fits ? staged[i] : fetch(i); };
+    auto key4 = [&](int q) -> uint4 { return fits ? staged[q] : fetch(q); };
 
     uint32_t lo = 0xffffffffu, hi = 0u;
-#pragma unroll 8
-    for (int i = tid; i < cnt; i += kSelectThreads) {
-        const uint32_t k = fetch(i);
-        if (fits) staged[i] = k;
-        lo = min(lo, k);
-        hi = max(hi, k);
+#pragma unroll 4
+    for (int q = tid; q < cnt; q += kSelectThreads) {
+        const uint4 k = fetch(q);
+        if (fits) staged[q] = k;
+        // 0 wraps to the top for the minimum and is never the maximum
+        lo = min(min(lo, min(k.x - 1u, k.y - 1u)), min(k.z - 1u, k.w - 1u));
+        hi = max(max(hi, max(k.x, k.y)), max(k.z, k.w));
     }
+    lo = lo == 0xffffffffu ? lo : lo + 1u;
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
     if (lane == 0) {
@@ -161,9 +181,13 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictArgs a, int
         const int shift = width_bits > 11 ? width_bits - 11 : 0;
         reinterpret_cast<int4 *>(sh.hist)[tid] = make_int4(0, 0, 0, 0);
         __syncthreads();
-        for (int i = tid; i < cnt; i += kSelectThreads) {
-            const uint32_t k = key(i);
-            if (k >= lo && k <= hi) atomicAdd(&sh.hist[(k - lo) >> shift], 1);
+        const uint32_t width = hi - lo;
+        for (int q = tid; q < cnt; q += kSelectThreads) {
+            const uint4 k = key4(q);
+            if (k.x - lo <= width) atomicAdd(&sh.hist[(k.x - lo) >> shift], 1);
+            if (k.y - lo <= width) atomicAdd(&sh.hist[(k.y - lo) >> shift], 1);
+            if (k.z - lo <= width) atomicAdd(&sh.hist[(k.z - lo) >> shift], 1);
+            if (k.w - lo <= width) atomicAdd(&sh.hist[(k.w - lo) >> shift], 1);
         }
         tc::cluster_barrier();
         // four bins a thread, from the top: thread t holds bins kBins-1-4t .. kBins-4-4t
@@ -203,13 +227,16 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictArgs a, int
     }
     // a key stays when it is above hi, or in [lo, hi] and among the first `need`
     // of those (all of them when whole; else lo == hi: ties, the lowest indices)
+    const uint32_t width = hi - lo;
+    auto count = [&](uint32_t k) -> int { return k > hi ? 1 : (k - lo <= width ? 1 << 16 : 0); };
     int gt = 0, eq = 0;
     const int per_warp = ((cnt + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
     const int w0 = min(cnt, warp * per_warp), w1 = min(cnt, w0 + per_warp);
-    for (int i = w0 + lane; i < w1; i += 32) {
-        const uint32_t k = key(i);
-        gt += k > hi;
-        eq += k >= lo && k <= hi;
+    for (int q = w0 + lane; q < w1; q += 32) {
+        const uint4 k = key4(q);
+        const int c = count(k.x) + count(k.y) + count(k.z) + count(k.w);
+        gt += c & 0xffff;
+        eq += c >> 16;
     }
     gt = __reduce_add_sync(0xffffffffu, gt);
     eq = __reduce_add_sync(0xffffffffu, eq);
@@ -237,44 +264,58 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictArgs a, int
         g0 += sh.warp_a[w];
         e0 += sh.warp_b[w];
     }
-    const unsigned below = (1u << lane) - 1u;
     for (int base = w0; base < w1; base += 32) {
-        const int i = base + lane;
-        const uint32_t k = i < w1 ? key(i) : 0u;
-        const bool above = i < w1 && k > hi, in = i < w1 && k >= lo && k <= hi;
-        const unsigned bg = __ballot_sync(0xffffffffu, above), be = __ballot_sync(0xffffffffu, in);
-        const int g = g0 + __popc(bg & below), e = e0 + __popc(be & below);
-        if (above || (in && e < need)) kept[b.first + g + min(e, need)] = j0 + i;
-        g0 += __popc(bg);
-        e0 += __popc(be);
+        const int q = base + lane;
+        const uint4 k4 = q < w1 ? key4(q) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+        // above | equal << 16 of my four and of the lanes before me
+        const int mine = count(k[0]) + count(k[1]) + count(k[2]) + count(k[3]);
+        int x = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        int g = g0 + ((x - mine) & 0xffff), e = e0 + ((x - mine) >> 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = count(k[i]);
+            if (c == 1 || (c && e < need)) kept[b.first + g + min(e, need)] = j0 + 4 * (part0 + q) + i;
+            g += c & 0xffff;
+            e += c >> 16;
+        }
+        const int sum = __shfl_sync(0xffffffffu, x, 31);
+        g0 += sum & 0xffff;
+        e0 += sum >> 16;
     }
     tc::cluster_barrier();                     // no CTA leaves while another reads its counts
 }
 
 // -------------------------------------------------------------------- move --
-constexpr int kMoveThreads = 256, kMoveRanks = 128, kMoveUnroll = 8;
+constexpr int kMoveThreads = 256, kMoveRanks = 128, kMoveUnroll = 4;
 
-// Copies columns [c0, c0 + w) of the chunk's rows of one tensor: 256 / w rows a
-// step, eight steps in flight.
+__device__ __forceinline__ int2 lds_move(uint32_t addr) {
+    int2 m;
+    asm volatile("ld.shared.v2.s32 {%0, %1}, [%2];\n" : "=r"(m.x), "=r"(m.y) : "r"(addr));
+    return m;
+}
+
+// Copies one column of kMoveUnroll rows of a chunk, `per` ranks apart: `at` is
+// the thread's column of row 0, the rows are moves[r].x -> moves[r].y (y < 0:
+// stays), looked up again for the stores so that registers hold little but the
+// data in flight.
 template <typename U, bool kOrdered>
-__device__ __forceinline__ void move_columns(U *cache, const int64_t *from, const int64_t *to, int64_t stride, int64_t head,
-                                             int units, int c0, int w, int ranks) {
-    const int lane = threadIdx.x % w, sub = threadIdx.x / w, per = kMoveThreads / w;
-    const bool col = c0 + lane < units;
-    U *at = cache + head + c0 + lane;
-    for (int base = 0; base < ranks; base += per * kMoveUnroll) {
-        U v[kMoveUnroll];
+__device__ __forceinline__ void move_column(U *at, uint32_t moves, int per, int64_t stride) {
+    U v[kMoveUnroll];
 #pragma unroll
-        for (int u = 0; u < kMoveUnroll; ++u) {
-            const int i = base + u * per + sub;
-            if (i < ranks && col && to[i] >= 0) v[u] = at[from[i] * stride];
-        }
-        if (kOrdered) __syncthreads();       // every read of these ranks before any write of them
+    for (int u = 0; u < kMoveUnroll; ++u) {
+        const int2 m = lds_move(moves + (uint32_t)(u * per) * 8u);
+        if (m.y >= 0) v[u] = at[m.x * stride];
+    }
+    if (kOrdered) __syncthreads();           // every read of these ranks before any write of them
 #pragma unroll
-        for (int u = 0; u < kMoveUnroll; ++u) {
-            const int i = base + u * per + sub;
-            if (i < ranks && col && to[i] >= 0) at[to[i] * stride] = v[u];
-        }
+    for (int u = 0; u < kMoveUnroll; ++u) {
+        const int2 m = lds_move(moves + (uint32_t)(u * per) * 8u);
+        if (m.y >= 0) at[m.y * stride] = v[u];
     }
 }
 
@@ -282,45 +323,61 @@ __device__ __forceinline__ void move_columns(U *cache, const int64_t *from, cons
 // column slice p of all its ranks and walks them upwards.  Otherwise nothing
 // written is read, and part p takes every parts-th chunk of ranks, all columns.
 template <typename U, bool kOrdered>
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(EvictArgs a, int ps_shift, int uk, int uv, int w, int nk, int parts) {
+__global__ void __launch_bounds__(kMoveThreads, kOrdered ? 4 : 5)
+    move_kernel(EvictArgs a, int ps_shift, int uk, int uv, int w_shift, int nk, int parts) {
     griddep_wait();
     griddep_launch();
-    __shared__ int64_t from[kMoveRanks], to[kMoveRanks];
-    const int part = blockIdx.x % parts;
-    const int sh = blockIdx.x / parts;
-    const int h = sh % a.hkv, s = sh / a.hkv;
+    // source and destination rows of the chunk's ranks; past them nothing moves
+    __shared__ int2 moves[kMoveRanks + kMoveThreads * kMoveUnroll];
+    // heads fastest: the CTAs that run together write neighbouring rows of the same slots
+    const int h = blockIdx.x % a.hkv;
+    const int part = (int)(blockIdx.x / a.hkv) % parts, s = (int)(blockIdx.x / a.hkv) / parts;
     const int32_t *kept = a.kept + ((int64_t)s * a.hkv + h) * a.kept_stride;
     const int keep = budget_of(a, s).keep, ps = a.src.page_size;
-    U *kc = static_cast<U *>(a.k_cache), *vc = static_cast<U *>(a.v_cache);
+    const int w = 1 << w_shift, lane = threadIdx.x & (w - 1), sub = threadIdx.x >> w_shift, per = kMoveThreads >> w_shift;
+    U *kc = static_cast<U *>(a.k_cache) + (int64_t)h * uk + lane, *vc = static_cast<U *>(a.v_cache) + (int64_t)h * uv + lane;
     const int64_t sk = (int64_t)a.hkv * uk, sv = (int64_t)a.hkv * uv;
+    for (int r = kMoveRanks + threadIdx.x; r < kMoveRanks + per * kMoveUnroll; r += kMoveThreads) moves[r] = make_int2(-1, -1);
     for (int base = kOrdered ? 0 : part * kMoveRanks; base < keep; base += kOrdered ? kMoveRanks : parts * kMoveRanks) {
-        const int ranks = min(kMoveRanks, keep - base);
         float m = 0.f;
         int64_t m_to = -1;
-        bool moves = false;
+        bool moving = false;
         __syncthreads();                     // the last chunk's rows are done with
-        if (threadIdx.x < ranks) {
+        if (threadIdx.x < kMoveRanks) {
+            int2 mv = make_int2(-1, -1);
             const int i = base + threadIdx.x;
-            const int64_t f = slot_of(a.src, s, kept[i], ps_shift), t = slot_of(a.dst, s, i, ps_shift);
-            if (f < 0 || t < 0) atomicCAS(a.status, 0, PA_DEVICE_RANGE);
-            moves = f >= 0 && t >= 0 && f != t;
-            from[threadIdx.x] = f;
-            to[threadIdx.x] = moves ? t : -1;
-            if (moves && (!kOrdered || part == 0)) {
-                m = a.key_mass[mass_at(f, h, a.hkv, ps, ps_shift)];
-                m_to = mass_at(t, h, a.hkv, ps, ps_shift);
+            if (i < keep) {
+                const int64_t f = slot_of(a.src, s, kept[i], ps_shift), t = slot_of(a.dst, s, i, ps_shift);
+                if (f < 0 || t < 0)
+                    atomicCAS(a.status, 0, PA_DEVICE_RANGE);
+                else if (f != t)
+                    mv = make_int2((int)f, (int)t);
+                if (mv.y >= 0 && (!kOrdered || part == 0)) {
+                    m = a.key_mass[mass_at(f, h, a.hkv, ps, ps_shift)];
+                    m_to = mass_at(t, h, a.hkv, ps, ps_shift);
+                }
             }
+            moving = mv.y >= 0;
+            moves[threadIdx.x] = mv;
         }
-        if (!__syncthreads_or(moves)) continue;
+        if (!__syncthreads_or(moving)) continue;
         if (m_to >= 0) a.key_mass[m_to] = m;
-        if (kOrdered) {
-            if (part < nk)
-                move_columns<U, true>(kc, from, to, sk, (int64_t)h * uk, uk, part * w, w, ranks);
-            else
-                move_columns<U, true>(vc, from, to, sv, (int64_t)h * uv, uv, (part - nk) * w, w, ranks);
-        } else {
-            for (int c0 = 0; c0 < uk; c0 += w) move_columns<U, false>(kc, from, to, sk, (int64_t)h * uk, uk, c0, w, ranks);
-            for (int c0 = 0; c0 < uv; c0 += w) move_columns<U, false>(vc, from, to, sv, (int64_t)h * uv, uv, c0, w, ranks);
+#pragma unroll 1
+        for (int r0 = 0; r0 < kMoveRanks; r0 += per * kMoveUnroll) {
+            uint32_t mv = tc::smem_u32(moves + r0 + sub);
+            if (kOrdered) {
+                const bool is_k = part < nk;
+                const int c0 = (is_k ? part : part - nk) << w_shift;
+                if (c0 + lane >= (is_k ? uk : uv)) mv = tc::smem_u32(moves + kMoveRanks + sub);     // no such column
+                move_column<U, true>((is_k ? kc : vc) + c0, mv, per, is_k ? sk : sv);
+            } else {
+                // one loop over the columns of both tensors: a single copy of the body
+#pragma unroll 1
+                for (int c = lane; c < uk + uv; c += w) {
+                    U *at = c < uk ? kc + (c - lane) : vc + (c - lane - uk);
+                    move_column<U, false>(at, mv, per, c < uk ? sk : sv);
+                }
+            }
         }
     }
 }
@@ -335,8 +392,9 @@ int ps_shift_of(int ps) {
 template <typename U> cudaError_t launch_move(const EvictArgs &a, bool in_place, int longest, cudaStream_t st) {
     const int uk = (int)((int64_t)a.d * a.elem / sizeof(U)), uv = (int)((int64_t)a.dv * a.elem / sizeof(U));
     const int64_t pairs = (int64_t)a.src.sequences * a.hkv;
-    int w = 1;
-    while (w < 16 && w < (uk > uv ? uk : uv)) w *= 2;
+    int w_shift = 0;
+    while (w_shift < 4 && (1 << w_shift) < (uk > uv ? uk : uv)) ++w_shift;
+    const int w = 1 << w_shift;
     int64_t parts;
     int nk = 0;
     if (in_place) {
@@ -350,17 +408,17 @@ template <typename U> cudaError_t launch_move(const EvictArgs &a, bool in_place,
     if (pairs * parts > INT32_MAX) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)(pairs * parts)), block(kMoveThreads);
     const int sh = ps_shift_of(a.src.page_size);
-    return in_place ? launch_pdl(move_kernel<U, true>, grid, block, 0, st, a, sh, uk, uv, w, nk, (int)parts)
-                    : launch_pdl(move_kernel<U, false>, grid, block, 0, st, a, sh, uk, uv, w, nk, (int)parts);
+    return in_place ? launch_pdl(move_kernel<U, true>, grid, block, 0, st, a, sh, uk, uv, w_shift, nk, (int)parts)
+                    : launch_pdl(move_kernel<U, false>, grid, block, 0, st, a, sh, uk, uv, w_shift, nk, (int)parts);
 }
 
-// Keys a CTA holds in shared memory at most (half of an SM's).
-constexpr int kStagedKeys = 24576;
+// Fours of keys a CTA holds in shared memory at most (half of an SM's).
+constexpr int kStagedFours = 6144;
 
 cudaError_t launch_select(const EvictArgs &a, int cluster, int room, cudaStream_t st) {
-    const size_t smem = (size_t)room * sizeof(uint32_t);
+    const size_t smem = (size_t)room * sizeof(uint4);
     cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kStagedKeys * (int)sizeof(uint32_t));
+                                         kStagedFours * (int)sizeof(uint4));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.src.sequences * a.hkv * cluster));
@@ -375,7 +433,8 @@ cudaError_t launch_select(const EvictArgs &a, int cluster, int room, cudaStream_
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, select_kernel, a, ps_shift_of(a.src.page_size), room);
+    const int quads = a.src.page_size % 4 == 0 && reinterpret_cast<uintptr_t>(a.key_mass) % 16 == 0;
+    return cudaLaunchKernelEx(&cfg, select_kernel, a, ps_shift_of(a.src.page_size), room, quads);
 }
 
 }  // namespace
@@ -387,10 +446,10 @@ cudaError_t launch_evict(const EvictArgs &a, int longest, int longest_kept, bool
     // fits in shared memory, but no part below 2048 keys
     int cluster = 1;
     while (cluster < 8 && longest / (2 * cluster) >= 2048 &&
-           (pairs * cluster < 152 || longest / cluster > kStagedKeys))
+           (pairs * cluster < 152 || longest / cluster > 4 * kStagedFours))
         cluster *= 2;
-    const int span = ((longest + cluster - 1) / cluster + 31) / 32 * 32;
-    cudaError_t e = launch_select(a, cluster, span <= kStagedKeys ? span : 0, st);
+    const int span = (longest / 4 + 2 + cluster - 1) / cluster;    // fours a CTA, whatever the sink's alignment
+    cudaError_t e = launch_select(a, cluster, span <= kStagedFours ? span : 0, st);
     if (e != cudaSuccess) return e;
     auto al = [](const void *p, int n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; };
     const int64_t kb = (int64_t)a.d * a.elem, vb = (int64_t)a.dv * a.elem;
