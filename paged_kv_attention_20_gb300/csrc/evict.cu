@@ -15,6 +15,9 @@
 // what a chunk of ranks writes has been read by this or an earlier chunk, and a
 // barrier between the reads and the writes of a chunk is all it takes.
 
+#include <algorithm>
+#include <type_traits>
+
 #include "pa_internal.h"
 #include "sm103_tc.cuh"
 
@@ -67,14 +70,13 @@ __device__ __forceinline__ Budget budget_of(const EvictArgs &a, int s) {
 // (11 bits a round, so at most three; bins follow the data's own range, which
 // spreads the counts: totals crowd into a few exponents).  Each CTA adds up the
 // cluster's histograms itself, through distributed shared memory.
-constexpr int kSelectThreads = 512;
-constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
-static_assert(kBins == 4 * kSelectThreads, "four bins a thread");
+constexpr int kMaxSelectWarps = 32;
+constexpr uint32_t kMaxCluster = 8;
 
 struct SelectShared {
     int hist[kBins];
-    int warp_a[kSelectWarps], warp_b[kSelectWarps];
+    int warp_a[kMaxSelectWarps], warp_b[kMaxSelectWarps];
     uint32_t lo, hi;          // this CTA's smallest and largest key
     int above, equal;         // this CTA's keys above / at the threshold
     int found_bin, found_above, found_count;
@@ -89,51 +91,73 @@ template <typename V> __device__ __forceinline__ const V *peer(const V *p, uint3
 // room: fours of keys the dynamic shared memory holds.  A part that is longer
 // (the device lengths can exceed the host's that sized the launch) is re-read
 // instead.  quads: the totals of four keys at a multiple of four lie together.
-__global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(EvictArgs a, int ps_shift, int room, int quads) {
+// A lone CTA has 512 threads, three of them fit an SM; the CTAs of a cluster have
+// an SM each and 1024 threads.
+template <bool kCluster>
+__global__ void __launch_bounds__(kCluster ? 1024 : 512, kCluster ? 1 : 3) select_kernel(EvictArgs a, int ps_shift, int room, int quads) {
     griddep_wait();
     griddep_launch();
+    constexpr int kSelectThreads = kCluster ? 1024 : 512, kSelectWarps = kSelectThreads / 32;
+    constexpr int kPer = kBins / kSelectThreads;       // bins a thread
+    using Bins = typename std::conditional<kPer == 2, int2, int4>::type;
+    union Pack {
+        Bins v;
+        int i[kPer];
+    };
     extern __shared__ uint4 staged[];
     __shared__ __align__(16) SelectShared sh;
-    const uint32_t C = tc::cluster_nctarank(), rank = tc::cluster_ctarank();
+    const uint32_t C = kCluster ? tc::cluster_nctarank() : 1u, rank = kCluster ? tc::cluster_ctarank() : 0u;
     const int pair = (int)(blockIdx.x / C);
     const int h = pair % a.hkv, s = pair / a.hkv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Budget b = budget_of(a, s);
     int32_t *kept = a.kept + ((int64_t)s * a.hkv + h) * a.kept_stride;
     const int all = (int)C * kSelectThreads, me = (int)rank * kSelectThreads + tid;
-    for (int i = b.keep + me; i < a.kept_stride; i += all) kept[i] = -1;
+    // what needs no choice: the sink, the recent keys, the places past the budget
+    auto write_fixed = [&]() {
+        for (int i = me; i < b.first; i += all) kept[i] = i;
+        for (int i = me; i < b.n - b.last; i += all) kept[b.first + b.want + i] = b.last + i;
+        for (int i = b.keep + me; i < a.kept_stride; i += all) kept[i] = -1;
+    };
     if (b.keep == b.n) {                      // the whole cluster leaves here together
-        for (int i = me; i < b.keep; i += all) kept[i] = i;
+        for (int i = me; i < a.kept_stride; i += all) kept[i] = i < b.n ? i : -1;
         return;
     }
-    for (int i = me; i < b.first; i += all) kept[i] = i;
-    for (int i = me; i < b.n - b.last; i += all) kept[b.first + b.want + i] = b.last + i;
-    if (b.want == 0) return;
+    if (b.want == 0) {
+        write_fixed();
+        return;
+    }
+    // a cluster barrier's release waits for every earlier store and costs ~2000
+    // cycles a time where __syncthreads costs tens: no store comes before the last
+    // one, and a CTA alone uses the latter
+    auto barrier = [&]() {
+        if (kCluster)
+            tc::cluster_barrier();
+        else
+            __syncthreads();
+    };
 
     // the candidates as aligned fours (places outside [first, last) hold no key), my
     // part of them
     const int j0 = b.first & ~3, fours = (b.last - j0 + 3) / 4;
     const int span = (fours + (int)C - 1) / (int)C;
     const int part0 = min(fours, (int)rank * span), cnt = min(fours, part0 + span) - part0;
+    bool mapped = true;                        // every place seen had a page (no branch: loads stay in flight)
     auto fetch = [&](int q) -> uint4 {
         const int j = j0 + 4 * (part0 + q);
-        float m[4] = {0.f, 0.f, 0.f, 0.f};
+        float m[4];
         if (quads) {
             const int64_t slot = slot_of(a.src, s, j, ps_shift);
-            if (slot < 0) {
-                atomicCAS(a.status, 0, PA_DEVICE_RANGE);
-            } else {
-                const float4 v = *reinterpret_cast<const float4 *>(a.key_mass + mass_at(slot, h, a.hkv, a.src.page_size, ps_shift));
-                m[0] = v.x; m[1] = v.y; m[2] = v.z; m[3] = v.w;
-            }
+            mapped &= slot >= 0;
+            const float4 v = *reinterpret_cast<const float4 *>(
+                a.key_mass + mass_at(slot < 0 ? 0 : slot, h, a.hkv, a.src.page_size, ps_shift));
+            m[0] = v.x; m[1] = v.y; m[2] = v.z; m[3] = v.w;
         } else {
+#pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (j + i < b.first || j + i >= b.last) continue;
-                const int64_t slot = slot_of(a.src, s, j + i, ps_shift);
-                if (slot < 0)
-                    atomicCAS(a.status, 0, PA_DEVICE_RANGE);
-                else
-                    m[i] = a.key_mass[mass_at(slot, h, a.hkv, a.src.page_size, ps_shift)];
+                const int64_t slot = slot_of(a.src, s, min(max(j + i, b.first), b.last - 1), ps_shift);
+                mapped &= slot >= 0;
+                m[i] = a.key_mass[mass_at(slot < 0 ? 0 : slot, h, a.hkv, a.src.page_size, ps_shift)];
             }
         }
         auto k = [&](int i) { return j + i >= b.first && j + i < b.last ? order_key(m[i]) : 0u; };
@@ -143,7 +167,7 @@ __global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(EvictArgs a, 
     auto key4 = [&](int q) -> uint4 { return fits ? staged[q] : fetch(q); };
 
     uint32_t lo = 0xffffffffu, hi = 0u;
-#pragma unroll 4
+#pragma unroll 8
     for (int q = tid; q < cnt; q += kSelectThreads) {
         const uint4 k = fetch(q);
         if (fits) staged[q] = k;
@@ -159,19 +183,22 @@ __global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(EvictArgs a, 
         sh.warp_b[warp] = (int)hi;
     }
     __syncthreads();
-    if (warp == 0) {
-        const uint32_t x = lane < kSelectWarps ? (uint32_t)sh.warp_a[lane] : 0xffffffffu;
-        const uint32_t y = lane < kSelectWarps ? (uint32_t)sh.warp_b[lane] : 0u;
-        const uint32_t mn = __reduce_min_sync(0xffffffffu, x), mx = __reduce_max_sync(0xffffffffu, y);
-        if (lane == 0) {
-            sh.lo = mn;
-            sh.hi = mx;
+    if (kCluster) {
+        if (tid == 0) {
+#pragma unroll
+            for (int w = 0; w < kSelectWarps; ++w) {
+                lo = min(lo, (uint32_t)sh.warp_a[w]);
+                hi = max(hi, (uint32_t)sh.warp_b[w]);
+            }
+            sh.lo = lo;
+            sh.hi = hi;
         }
-    }
-    tc::cluster_barrier();
-    for (uint32_t r = 0; r < C; ++r) {
-        lo = min(lo, *peer(&sh.lo, r));
-        hi = max(hi, *peer(&sh.hi, r));
+        barrier();
+        lo = __reduce_min_sync(0xffffffffu, lane < (int)C ? *peer(&sh.lo, lane) : 0xffffffffu);
+        hi = __reduce_max_sync(0xffffffffu, lane < (int)C ? *peer(&sh.hi, lane) : 0u);
+    } else {
+        lo = __reduce_min_sync(0xffffffffu, lane < kSelectWarps ? (uint32_t)sh.warp_a[lane] : 0xffffffffu);
+        hi = __reduce_max_sync(0xffffffffu, lane < kSelectWarps ? (uint32_t)sh.warp_b[lane] : 0u);
     }
     // invariant: exactly b.want - need keys lie above hi, and need >= 1 of those in [lo, hi] stay
     int need = b.want;
@@ -179,7 +206,10 @@ __global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(EvictArgs a, 
     while (true) {
         const int width_bits = 32 - __clz((int)(hi - lo));     // 0 when lo == hi
         const int shift = width_bits > 11 ? width_bits - 11 : 0;
-        reinterpret_cast<int4 *>(sh.hist)[tid] = make_int4(0, 0, 0, 0);
+        Pack c;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) c.i[i] = 0;
+        reinterpret_cast<Bins *>(sh.hist)[tid] = c.v;
         __syncthreads();
         const uint32_t width = hi - lo;
         for (int q = tid; q < cnt; q += kSelectThreads) {
@@ -189,15 +219,24 @@ __global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(EvictArgs a, 
             if (k.z - lo <= width) atomicAdd(&sh.hist[(k.z - lo) >> shift], 1);
             if (k.w - lo <= width) atomicAdd(&sh.hist[(k.w - lo) >> shift], 1);
         }
-        tc::cluster_barrier();
-        // four bins a thread, from the top: thread t holds bins kBins-1-4t .. kBins-4-4t
-        const int first = kBins - 4 - 4 * tid;
-        int4 c = make_int4(0, 0, 0, 0);
-        for (uint32_t r = 0; r < C; ++r) {
-            const int4 x = *reinterpret_cast<const int4 *>(peer(&sh.hist[first], r));
-            c.x += x.x; c.y += x.y; c.z += x.z; c.w += x.w;
+        barrier();
+        // bins from the top: thread t holds bins kBins - kPer * (t + 1) .. kBins - 1 - kPer * t
+        const int first = kBins - kPer * (tid + 1);
+        if (!kCluster) {
+            c.v = *reinterpret_cast<const Bins *>(&sh.hist[first]);
+        } else {
+            Pack x[kMaxCluster];
+#pragma unroll
+            for (uint32_t r = 0; r < kMaxCluster; ++r)
+                x[r].v = *reinterpret_cast<const Bins *>(peer(&sh.hist[first], r < C ? r : rank));
+#pragma unroll
+            for (uint32_t r = 0; r < kMaxCluster; ++r)
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) c.i[i] += r < C ? x[r].i[i] : 0;
         }
-        const int mine = c.x + c.y + c.z + c.w;
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) mine += c.i[i];
         int x = mine;
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -206,17 +245,26 @@ __global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(EvictArgs a, 
         if (lane == 31) sh.warp_a[warp] = x;
         __syncthreads();
         int before = x - mine;
-        for (int w = 0; w < warp; ++w) before += sh.warp_a[w];
+#pragma unroll
+        for (int w = 0; w < kSelectWarps; ++w) before += w < warp ? sh.warp_a[w] : 0;
         if (before < need && before + mine >= need) {
-            const int q[4] = {c.w, c.z, c.y, c.x};             // from the top bin down
-            int acc = before, k = 0;
-            while (acc + q[k] < need) acc += q[k++];
-            sh.found_bin = first + 3 - k;
+            int acc = before, bin = 0, in_bin = 0;
+            bool found = false;
+#pragma unroll
+            for (int i = kPer - 1; i >= 0; --i) {          // from the top bin down
+                if (!found && acc + c.i[i] >= need) {
+                    found = true;
+                    bin = first + i;
+                    in_bin = c.i[i];
+                }
+                if (!found) acc += c.i[i];
+            }
+            sh.found_bin = bin;
             sh.found_above = acc;
-            sh.found_count = q[k];
+            sh.found_count = in_bin;
         }
         // also: no CTA clears its histogram while another still reads it
-        tc::cluster_barrier();
+        barrier();
         need -= sh.found_above;
         const uint32_t bin_lo = lo + ((uint32_t)sh.found_bin << shift);
         hi = (uint32_t)min((unsigned long long)hi, (unsigned long long)bin_lo + ((1ull << shift) - 1ull));   // the last bin may be cut
@@ -245,25 +293,27 @@ __global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(EvictArgs a, 
         sh.warp_b[warp] = eq;
     }
     __syncthreads();
-    if (tid == 0) {
-        int g = 0, e = 0;
-        for (int w = 0; w < kSelectWarps; ++w) {
-            g += sh.warp_a[w];
-            e += sh.warp_b[w];
+    int g0 = 0, e0 = 0, g_all = 0, e_all = 0;
+#pragma unroll
+    for (int w = 0; w < kSelectWarps; ++w) {
+        const int g = sh.warp_a[w], e = sh.warp_b[w];
+        g0 += w < warp ? g : 0;
+        e0 += w < warp ? e : 0;
+        g_all += g;
+        e_all += e;
+    }
+    if (kCluster) {
+        if (tid == 0) {
+            sh.above = g_all;
+            sh.equal = e_all;
         }
-        sh.above = g;
-        sh.equal = e;
+        barrier();
+        g0 += __reduce_add_sync(0xffffffffu, lane < (int)rank ? *peer(&sh.above, lane) : 0);
+        e0 += __reduce_add_sync(0xffffffffu, lane < (int)rank ? *peer(&sh.equal, lane) : 0);
+        barrier();                             // no CTA leaves while another reads its counts
     }
-    tc::cluster_barrier();
-    int g0 = 0, e0 = 0;
-    for (uint32_t r = 0; r < rank; ++r) {
-        g0 += *peer(&sh.above, r);
-        e0 += *peer(&sh.equal, r);
-    }
-    for (int w = 0; w < warp; ++w) {
-        g0 += sh.warp_a[w];
-        e0 += sh.warp_b[w];
-    }
+    write_fixed();
+    if (!mapped) atomicCAS(a.status, 0, PA_DEVICE_RANGE);
     for (int base = w0; base < w1; base += 32) {
         const int q = base + lane;
         const uint4 k4 = q < w1 ? key4(q) : make_uint4(0u, 0u, 0u, 0u);
@@ -287,7 +337,6 @@ __global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(EvictArgs a, 
         g0 += sum & 0xffff;
         e0 += sum >> 16;
     }
-    tc::cluster_barrier();                     // no CTA leaves while another reads its counts
 }
 
 // -------------------------------------------------------------------- move --
@@ -416,13 +465,18 @@ template <typename U> cudaError_t launch_move(const EvictArgs &a, bool in_place,
 constexpr int kStagedFours = 6144;
 
 cudaError_t launch_select(const EvictArgs &a, int cluster, int room, cudaStream_t st) {
-    const size_t smem = (size_t)room * sizeof(uint4);
-    cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kStagedFours * (int)sizeof(uint4));
+    size_t smem = (size_t)room * sizeof(uint4);
+    // a few clusters land on a few SMs, several CTAs to each, unless a CTA asks for
+    // more than half of an SM's shared memory
+    const size_t alone = 120 * 1024;
+    if (cluster > 1 && (int64_t)a.src.sequences * a.hkv * cluster <= 152 && smem < alone) smem = alone;
+    auto kernel = cluster > 1 ? select_kernel<true> : select_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)std::max(alone, kStagedFours * sizeof(uint4)));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.src.sequences * a.hkv * cluster));
-    cfg.blockDim = dim3(kSelectThreads);
+    cfg.blockDim = dim3(cluster > 1 ? 1024 : 512);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -432,9 +486,9 @@ cudaError_t launch_select(const EvictArgs &a, int cluster, int room, cudaStream_
     attr[1].val.clusterDim.x = (unsigned)cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     const int quads = a.src.page_size % 4 == 0 && reinterpret_cast<uintptr_t>(a.key_mass) % 16 == 0;
-    return cudaLaunchKernelEx(&cfg, select_kernel, a, ps_shift_of(a.src.page_size), room, quads);
+    return cudaLaunchKernelEx(&cfg, kernel, a, ps_shift_of(a.src.page_size), room, quads);
 }
 
 }  // namespace
@@ -445,7 +499,7 @@ cudaError_t launch_evict(const EvictArgs &a, int longest, int longest_kept, bool
     // CTAs per (sequence, head): enough that the pairs cover the SMs and a part
     // fits in shared memory, but no part below 2048 keys
     int cluster = 1;
-    while (cluster < 8 && longest / (2 * cluster) >= 2048 &&
+    while (cluster < (int)kMaxCluster && longest / (2 * cluster) >= 2048 &&
            (pairs * cluster < 152 || longest / cluster > 4 * kStagedFours))
         cluster *= 2;
     const int span = (longest / 4 + 2 + cluster - 1) / cluster;    // fours a CTA, whatever the sink's alignment
