@@ -368,7 +368,8 @@ pa_status paged_attn_forward_split_static(const pa_plan *plan, const void *q, co
  *   key_mass [pages, num_kv_heads, page_size] fp32 or NULL: the written keys' totals
  *           are set to 0 (paged_attn_forward_mass)
  *
- * Except for q_out == q, the written tensors overlap no input.  A position the
+ * Except for q_out == q, the written tensors overlap neither an input nor each
+ * other (PA_ERR_ARG).  A position the
  * table has no row for sets PA_DEVICE_RANGE in the status word and leaves that
  * query's rows (q_out and caches) as they were.  Zero queries: PA_OK, no launch.
  */

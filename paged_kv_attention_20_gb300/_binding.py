@@ -125,7 +125,13 @@ def _i32_array(a) -> np.ndarray:
     return np.ascontiguousarray(np.asarray(a, dtype=np.int32))
 
 
+# the current stream's handle without building a torch.cuda.Stream (2 us of a small call's time)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -226,9 +232,7 @@ def _tensor(t: torch.Tensor, name: str, dtype, device, rank: int) -> None:
 
 def _storage_span(t: torch.Tensor):
     start = t.data_ptr()
-    if t.is_contiguous():
-        return start, start + t.numel() * t.element_size()
-    return start, start + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+    return start, start + t.numel() * t.element_size()
 
 
 def _check_disjoint(out: torch.Tensor, *inputs) -> None:
@@ -300,7 +304,7 @@ def paged_kv_store(plan: Plan, new_k, new_v, k_cache, v_cache) -> None:
                                  v_cache.data_ptr(), heads, d, dv, _DTYPES[dt], _stream(dev)))
 
 
-def _attn_common(plan, q, k_cache, v_cache, out):
+def _attn_common(plan, q, k_cache, v_cache, out, disjoint=True):
     dev, dt = q.device, q.dtype
     if dt not in _DTYPES:
         raise TypeError("dtype must be float32, float16 or bfloat16")
@@ -320,7 +324,8 @@ def _attn_common(plan, q, k_cache, v_cache, out):
         _tensor(out, "out", dt, dev, 3)
         if tuple(out.shape) != shape:
             raise ValueError(f"out must have shape {shape}")
-    _check_disjoint(out, q, k_cache, v_cache)
+    if disjoint:                # else the library checks
+        _check_disjoint(out, q, k_cache, v_cache)
     return out
 
 
@@ -470,14 +475,6 @@ def paged_qk_norm_rope_store(plan: Plan, q, new_k, new_v, k_cache, v_cache, rope
         _tensor(q_out, "q_out", dt, dev, 3)
         if tuple(q_out.shape) != (n, hq, d):
             raise ValueError(f"q_out must have shape {(n, hq, d)}")
-        if not (q_out.data_ptr() == q.data_ptr() and q.is_contiguous()):
-            _check_disjoint(q_out, q)
-        _check_disjoint(q_out, new_k, new_v, k_cache, v_cache, rope_table, positions, q_weight, k_weight, key_mass)
-    for t in (k_cache, v_cache):
-        _check_disjoint(t, q, new_k, new_v, rope_table, positions, q_weight, k_weight, key_mass)
-    _check_disjoint(k_cache, v_cache)
-    if key_mass is not None:
-        _check_disjoint(key_mass, q, new_k, new_v, rope_table, positions, q_weight, k_weight)
     _check(load().paged_qk_norm_rope_store(
         plan.handle, q.data_ptr(), q_stride, new_k.data_ptr(), k_stride, new_v.data_ptr(), v_stride, q_out.data_ptr(),
         k_cache.data_ptr(), v_cache.data_ptr(), mass_ptr, table_ptr, far, rot, 1 if interleaved else 0, pos_ptr, qw_ptr,
@@ -504,16 +501,13 @@ def paged_attn_forward_mass(plan: Plan, q, k_cache, v_cache, key_mass, scale: fl
     """Paged attention that adds each key's softmax weights, over the plan's queries and a KV head's query heads, to
     key_mass [pages, kv_heads, page_size] (fp32).  splits defaults to the split heuristic; the workspace is allocated
     here when not given (make_mass_workspace)."""
-    out = _attn_common(plan, q, k_cache, v_cache, out)
+    out = _attn_common(plan, q, k_cache, v_cache, out, disjoint=False)
     hq, hkv, dv = q.shape[1], k_cache.shape[2], v_cache.shape[3]
     _key_mass(key_mass, plan, hkv, q.device)
     if splits is None:
         splits = paged_attn_split_heuristic(plan, hq, hkv, window=window)
     if workspace is None:
         workspace = make_mass_workspace(plan, hq, hkv, dv, splits, window if causal else 0, device=q.device)
-    _check_disjoint(out, workspace, key_mass)
-    _check_disjoint(key_mass, q, k_cache, v_cache, workspace)
-    _check_disjoint(workspace, q, k_cache, v_cache)
     _check(load().paged_attn_forward_mass(
         plan.handle, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), key_mass.data_ptr(), hq, hkv,
         q.shape[2], dv, float(scale), 1 if causal else 0, int(window), _DTYPES[q.dtype], workspace.data_ptr(),
@@ -542,9 +536,6 @@ def paged_kv_evict(plan: Plan, kept_plan: Plan, key_mass, k_cache, v_cache, sink
         _tensor(kept, "kept", torch.int32, dev, 3)
         if tuple(kept.shape[:2]) != (plan.sequences, hkv):
             raise ValueError("kept must be [sequences, kv_heads, n]")
-    _check_disjoint(kept, key_mass, k_cache, v_cache)
-    _check_disjoint(k_cache, v_cache, key_mass)
-    _check_disjoint(v_cache, key_mass)
     _check(load().paged_kv_evict(plan.handle, kept_plan.handle, key_mass.data_ptr(), k_cache.data_ptr(),
                                  v_cache.data_ptr(), kept.data_ptr(), kept.shape[2], int(sink), int(recent), hkv, d,
                                  v_cache.shape[3], _DTYPES[dt], _stream(dev)))

@@ -27,6 +27,22 @@ int64_t longest_tile_seq(const pa_plan *plan) {
 
 }  // namespace
 
+pa_status spans_disjoint(const Span *written, int n_written, const Span *read, int n_read, const char *call) {
+    auto meet = [](const Span &a, const Span &b) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+        return a.at && b.at && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+    };
+    for (int i = 0; i < n_written; ++i)
+        for (int j = i + 1; j < n_written + n_read; ++j) {
+            const Span &b = j < n_written ? written[j] : read[j - n_written];
+            if (!meet(written[i], b)) continue;
+            char msg[256];
+            std::snprintf(msg, sizeof msg, "%s: %s overlaps %s", call, written[i].name, b.name);
+            return fail(PA_ERR_ARG, msg);
+        }
+    return PA_OK;
+}
+
 MassLayout mass_layout(const pa_plan *plan, int32_t hq, int32_t dv, int32_t splits, int32_t window, int64_t max_keys) {
     MassLayout l{};
     const size_t rows = (size_t)plan->queries * hq;
@@ -154,6 +170,27 @@ pa_status paged_qk_norm_rope_store(const pa_plan *plan, const void *q, int64_t q
         if (reinterpret_cast<uintptr_t>(p) % 4) BAD(PA_ERR_ARG, "32-bit operand not 4-byte aligned");
     for (const void *p : {q, new_k, new_v, (const void *)q_out, (const void *)k_cache, (const void *)v_cache, q_weight, k_weight})
         if (reinterpret_cast<uintptr_t>(p) % pa::elem_bytes(dtype)) BAD(PA_ERR_ARG, "operand not aligned to its element");
+    {
+        const size_t es = (size_t)pa::elem_bytes(dtype), n = (size_t)plan->queries,
+                     slots = (size_t)plan->pages * plan->page_size * num_kv_heads;
+        auto rows = [&](int64_t stride, int32_t heads, int32_t dim) {
+            return ((n - 1) * (size_t)stride + (size_t)heads * dim) * es;
+        };
+        const pa::Span written[] = {{k_cache, slots * head_dim * es, "k_cache"}, {v_cache, slots * value_dim * es, "v_cache"},
+                                    {key_mass, slots * sizeof(float), "key_mass"},
+                                    {q_out, n * num_heads * head_dim * es, "q_out"}};
+        // q may be its own output when it is dense: every row is read before it is written
+        const bool own = q == q_out && (n == 1 || q_stride == (int64_t)num_heads * head_dim);
+        const pa::Span read[] = {{new_k, rows(k_stride, num_kv_heads, head_dim), "new_k"},
+                                 {new_v, rows(v_stride, num_kv_heads, value_dim), "new_v"},
+                                 {rope_table, (size_t)max_positions * rope_dim * sizeof(float), "the rope table"},
+                                 {positions, n * sizeof(int32_t), "positions"},
+                                 {q_weight, (size_t)head_dim * es, "q_weight"},
+                                 {k_weight, (size_t)head_dim * es, "k_weight"},
+                                 {own ? nullptr : q, rows(q_stride, num_heads, head_dim), "q"}};
+        const pa_status apart = pa::spans_disjoint(written, 4, read, 7, "paged_qk_norm_rope_store");
+        if (apart != PA_OK) return apart;
+    }
     pa::NormRopeArgs a{};
     a.plan = pa::view_of(plan);
     a.q = q; a.k = new_k; a.v = new_v;
@@ -250,6 +287,12 @@ pa_status paged_kv_evict(const pa_plan *plan, const pa_plan *kept_plan, float *k
         if (reinterpret_cast<uintptr_t>(p) % 4) BAD(PA_ERR_ARG, "32-bit operand not 4-byte aligned");
     for (const void *p : {(const void *)k_cache, (const void *)v_cache})
         if (reinterpret_cast<uintptr_t>(p) % pa::elem_bytes(dtype)) BAD(PA_ERR_ARG, "operand not aligned to its element");
+    const size_t slots = (size_t)plan->pages * plan->page_size * num_kv_heads, es = (size_t)pa::elem_bytes(dtype);
+    const pa::Span written[] = {{key_mass, slots * sizeof(float), "key_mass"}, {k_cache, slots * head_dim * es, "k_cache"},
+                                {v_cache, slots * value_dim * es, "v_cache"},
+                                {kept, (size_t)plan->sequences * num_kv_heads * kept_stride * sizeof(int32_t), "kept"}};
+    const pa_status apart = pa::spans_disjoint(written, 4, nullptr, 0, "paged_kv_evict");
+    if (apart != PA_OK) return apart;
     pa::EvictArgs a{};
     a.src = pa::view_of(plan);
     a.dst = pa::view_of(kept_plan);

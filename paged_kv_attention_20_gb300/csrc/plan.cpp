@@ -635,6 +635,16 @@ pa_status attention(const pa_plan *plan, const void *q, const void *k, const voi
         pa_status on_dev = operands_on_device(ptrs, names, 8, name);
         if (on_dev != PA_OK) return on_dev;
     }
+    if (mass) {
+        const size_t es = (size_t)elem_bytes(dtype), rows = (size_t)plan->queries * hq,
+                     slots = (size_t)plan->pages * plan->page_size * hkv;
+        const pa::Span written[] = {{out, rows * dv * es, "out"}, {key_mass, slots * sizeof(float), "key_mass"},
+                                    {ws, ws_bytes, "the workspace"}};
+        const pa::Span read[] = {{q, rows * d * es, "q"}, {k, slots * d * es, "the key cache"},
+                                 {v, slots * dv * es, "the value cache"}};
+        const pa_status apart = pa::spans_disjoint(written, 3, read, 3, name);
+        if (apart != PA_OK) return apart;
+    }
 
     pa::AttnArgs a{};
     a.plan = view_of(plan);

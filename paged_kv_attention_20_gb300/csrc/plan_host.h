@@ -47,6 +47,16 @@ PlanView view_of(const pa_plan *p);
 // device, else PA_ERR_ARG naming the operand.
 pa_status operands_on_device(const void *const *ptrs, const char *const *names, int n, const char *call);
 
+// A byte range of an operand.
+struct Span {
+    const void *at;
+    size_t bytes;
+    const char *name;
+};
+// PA_OK when none of the `written` ranges meets another of them or one of the
+// `read` ranges, else PA_ERR_ARG naming the two.  Null and empty ranges meet nothing.
+pa_status spans_disjoint(const Span *written, int n_written, const Span *read, int n_read, const char *call);
+
 // Workspace of paged_attn_forward_mass: byte offsets of its parts.
 struct MassLayout {
     size_t lse, lse_final, groups, scores, bytes;   // the split partials start at 0

@@ -212,7 +212,10 @@ def test_refusals(cuda_device):
         call(mass.half())
     with pytest.raises(ValueError):
         call(mass.cpu())
-    with pytest.raises(ValueError, match="overlaps"):
+    with pytest.raises(pka.PagedAttentionError, match="overlaps"):
+        call(torch.zeros(mass.numel() + 64, device="cuda")[:mass.numel()].view(mass.shape), splits=1,
+             workspace=dc.v_cache.view(-1).view(torch.float32))
+    with pytest.raises(pka.PagedAttentionError, match="overlaps"):
         call(dc.k_cache.view(-1).view(torch.float32)[:mass.numel()].view(mass.shape))
     status = lambda **k: pytest.raises(pka.PagedAttentionError, call, **k).value.status   # noqa: E731
     assert status(splits=0) == 7 and status(splits=65) == 7

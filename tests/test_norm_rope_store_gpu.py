@@ -162,7 +162,10 @@ def test_empty_plan_and_refusals(cuda_device):
     x = torch.ones(1, 1, 8, device="cuda")
     call = lambda **k: pka.paged_qk_norm_rope_store(plan, k.pop("q", x), k.pop("nk", x), x, kc, kc.clone(), **k)  # noqa: E731
     tab = torch.zeros(4, 8, device="cuda")
-    for kw in (dict(rope_table=tab[:, :7].contiguous()), dict(rope_table=torch.zeros(4, 10, device="cuda")),
+    big = torch.ones(40, device="cuda")
+    for kw in (dict(q_out=kc.view(4, 1, 8)[:1]), dict(q_out=x), dict(q=big[:8].view(1, 1, 8), q_out=big[4:12].view(1, 1, 8)),
+               dict(q=kc.view(4, 1, 8)[:1]), dict(nk=kc.view(4, 1, 8)[3:]), dict(key_mass=kc.view(-1)[:4].view(1, 1, 4)),
+               dict(q_weight=kc.view(-1)[24:]), dict(rope_table=kc.view(4, 8)), dict(rope_table=tab[:, :7].contiguous()), dict(rope_table=torch.zeros(4, 10, device="cuda")),
                dict(positions=torch.zeros(1, dtype=torch.int32, device="cuda")),
                dict(q_weight=torch.ones(8, device="cuda"), eps=float("nan")),
                dict(q_weight=torch.ones(8, device="cuda"), eps=-1.0)):
@@ -171,7 +174,7 @@ def test_empty_plan_and_refusals(cuda_device):
     for kw in (dict(rope_table=tab[:0]), dict(q_weight=torch.ones(7, device="cuda")), dict(rope_table=tab, positions=torch.zeros(2, dtype=torch.int32, device="cuda")),
                dict(key_mass=torch.zeros(1, 4, 1, device="cuda")), dict(q=torch.ones(1, 1, 9, device="cuda")),
                dict(q=torch.ones(1, 8, 2, device="cuda").transpose(1, 2)), dict(nk=torch.ones(1, 2, 8, device="cuda")),
-               dict(q_out=kc.view(4, 1, 8)[:1]), dict(rope_table=tab.cpu())):
+               dict(rope_table=tab.cpu())):
         with pytest.raises(ValueError):
             call(**kw)
     for kw in (dict(rope_table=tab.double()), dict(q=x.half())):
