@@ -20,6 +20,7 @@
 #include <cuda_fp16.h>
 
 #include "pa_internal.h"
+#include "sm103_tc.cuh"
 
 namespace pa {
 namespace {
@@ -62,119 +63,137 @@ struct RowId {
     int token, head, part;     // part 0: Q, 1: K, 2: V
 };
 
-__device__ __forceinline__ RowId row_id(const NormRopeArgs &a, int64_t idx) {
-    const int per = a.hq + 2 * a.hkv;
+__device__ __forceinline__ RowId row_id(const NormRopeArgs &a, uint32_t idx) {
+    const uint32_t per = (uint32_t)(a.hq + 2 * a.hkv);
     RowId r;
     r.token = (int)(idx / per);
-    const int h = (int)(idx - (int64_t)r.token * per);
+    const int h = (int)(idx - (uint32_t)r.token * per);
     r.part = h < a.hq ? 0 : (h < a.hq + a.hkv ? 1 : 2);
     r.head = h - (r.part == 0 ? 0 : (r.part == 1 ? a.hq : a.hq + a.hkv));
+    r.token += a.first_token;
     return r;
 }
 
-// Position of a token, or -1 (recorded once per row) when the table has no row for it.
+// Position of a token, or -1 when the table has no row for it.
 __device__ __forceinline__ int table_position(const NormRopeArgs &a, int token, int plan_pos) {
     const int pos = a.positions ? a.positions[token] : plan_pos;
     return a.table && (pos < 0 || pos >= a.max_positions) ? -1 : pos;
 }
 
+// 1 / sqrt(mean of the row's squares + eps); a row's L lanes call together.
+template <int V, int L>
+__device__ __forceinline__ float row_scale(const float (&x0)[V], const float (&x1)[V], int d, float eps, unsigned group) {
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) ss += x0[e] * x0[e] + x1[e] * x1[e];
+#pragma unroll
+    for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
+    return rsqrtf(ss / (float)d + eps);
+}
+
+// Turns a thread's pairs: (x0[i], x1[i]), or interleaved the neighbours of its 2V
+// consecutive elements.
+template <int V>
+__device__ __forceinline__ void turn(float (&x0)[V], float (&x1)[V], const float (&c)[V], const float (&s)[V], bool interleaved) {
+    if (interleaved) {
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+            const float p = x0[2 * e], q = x0[2 * e + 1];
+            x0[2 * e] = p * c[e] - q * s[e];
+            x0[2 * e + 1] = q * c[e] + p * s[e];
+            const float u = x1[2 * e], v = x1[2 * e + 1];
+            x1[2 * e] = u * c[V / 2 + e] - v * s[V / 2 + e];
+            x1[2 * e + 1] = v * c[V / 2 + e] + u * s[V / 2 + e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float p = x0[e], q = x1[e];
+            x0[e] = p * c[e] - q * s[e];
+            x1[e] = q * c[e] + p * s[e];
+        }
+    }
+}
+
+// One row per group of L lanes: single tokens and small batches, where a launch's
+// latency counts and the rows spread over as many CTAs as there are.
 template <typename T, int L>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeArgs a, int64_t rows) {
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeArgs a, uint32_t rows) {
     constexpr int V = Chunk<T>::V;
     griddep_wait();
     griddep_launch();
-    const int64_t idx = (int64_t)blockIdx.x * (kThreads / L) + threadIdx.x / L;
+    const uint32_t idx0 = blockIdx.x * (uint32_t)(kThreads / L) + threadIdx.x / L;
     const int l = threadIdx.x % L;
-    const bool live = idx < rows;
-    const RowId r = row_id(a, live ? idx : rows - 1);
+    const int turned = a.rot / (2 * V);           // lanes that rotate
+    // my two chunks: a pair of halves (or of neighbours) inside the rotated dims,
+    // neighbours past them
+    int c0 = l * 2 * V, c1 = c0 + V;
+    if (!a.interleaved && l < turned) {
+        c0 = l * V;
+        c1 = a.rot / 2 + l * V;
+    }
+    const bool mine = l * 2 * V < a.d;
+    const bool live = idx0 < rows;
+    const RowId r = row_id(a, live ? idx0 : 0u);
     const int4 meta = a.plan.qmeta[r.token];
+    uint4 w0 = make_uint4(0u, 0u, 0u, 0u), w1 = w0;
+    if (r.part < 2 && mine) {
+        const T *src = r.part == 0 ? static_cast<const T *>(a.q) + (int64_t)r.token * a.q_stride
+                                   : static_cast<const T *>(a.k) + (int64_t)r.token * a.k_stride;
+        src += (int64_t)r.head * a.d;
+        w0 = *reinterpret_cast<const uint4 *>(src + c0);
+        w1 = *reinterpret_cast<const uint4 *>(src + c1);
+    }
     const int pos = table_position(a, r.token, meta.y);
     const int64_t slot = meta.z;
     const bool ok = live && (pos >= 0 || !a.table);
     if (live && !ok && l == 0) atomicCAS(a.status, 0, PA_DEVICE_RANGE);
     if (r.part == 2) {
         // value rows: a copy
-        if (!ok) return;
-        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.v) + (int64_t)r.token * a.v_stride +
-                                                           (int64_t)r.head * a.dv);
-        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(a.v_cache) + (slot * a.hkv + r.head) * a.dv);
-        for (int c = l; c < a.dv / V; c += L) dst[c] = src[c];
+        if (ok) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                static_cast<const T *>(a.v) + (int64_t)r.token * a.v_stride + (int64_t)r.head * a.dv);
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(a.v_cache) + (slot * a.hkv + r.head) * a.dv);
+#pragma unroll 2
+            for (int c = l; c < a.dv / V; c += L) dst[c] = src[c];
+        }
         return;
     }
-    const T *src = r.part == 0 ? static_cast<const T *>(a.q) + (int64_t)r.token * a.q_stride
-                               : static_cast<const T *>(a.k) + (int64_t)r.token * a.k_stride;
-    src += (int64_t)r.head * a.d;
+    float x0[V], x1[V], c[V], s[V];
+    const bool turns = ok && a.table && l < turned;
+    if (turns) {
+        const float *cs = a.table + (int64_t)pos * a.rot + l * V;
+#pragma unroll
+        for (int e = 0; e < V; e += 4) {
+            const float4 cc = *reinterpret_cast<const float4 *>(cs + e);
+            const float4 sn = *reinterpret_cast<const float4 *>(cs + a.rot / 2 + e);
+            c[e] = cc.x; c[e + 1] = cc.y; c[e + 2] = cc.z; c[e + 3] = cc.w;
+            s[e] = sn.x; s[e + 1] = sn.y; s[e + 2] = sn.z; s[e + 3] = sn.w;
+        }
+    }
+    Chunk<T>::unpack(w0, x0);
+    Chunk<T>::unpack(w1, x1);
     const T *w = static_cast<const T *>(r.part == 0 ? a.q_weight : a.k_weight);
-    // my two chunks: a pair of halves (or of neighbours) inside the rotated dims,
-    // neighbours past them
-    const int turned = a.rot / (2 * V);           // lanes that rotate
-    const bool mine = l * 2 * V < a.d;
-    int c0 = l * 2 * V, c1 = c0 + V;
-    if (!a.interleaved && l < turned) {
-        c0 = l * V;
-        c1 = a.rot / 2 + l * V;
-    }
-    float x0[V], x1[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) x0[i] = x1[i] = 0.f;
-    if (mine) {
-        Chunk<T>::unpack(*reinterpret_cast<const uint4 *>(src + c0), x0);
-        Chunk<T>::unpack(*reinterpret_cast<const uint4 *>(src + c1), x1);
-    }
     if (w) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) ss += x0[i] * x0[i] + x1[i] * x1[i];
-        // the lanes of a row sit in one aligned group of a warp; all 32 lanes are here
-        // or have left as whole value rows, so the group's own mask is named
+        // a row's lanes are one aligned group of a warp and take the same branches;
+        // other groups may be elsewhere, so the group names only itself
         const unsigned group = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1u) << ((threadIdx.x & 31) / L * L);
-#pragma unroll
-        for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
-        const float inv = rsqrtf(ss / (float)a.d + a.eps);
+        const float inv = row_scale<V, L>(x0, x1, a.d, a.eps, group);
         if (mine) {
-            float w0[V], w1[V];
-            Chunk<T>::unpack(*reinterpret_cast<const uint4 *>(w + c0), w0);
-            Chunk<T>::unpack(*reinterpret_cast<const uint4 *>(w + c1), w1);
+            float g0[V], g1[V];
+            Chunk<T>::unpack(*reinterpret_cast<const uint4 *>(w + c0), g0);
+            Chunk<T>::unpack(*reinterpret_cast<const uint4 *>(w + c1), g1);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                x0[i] *= inv * w0[i];
-                x1[i] *= inv * w1[i];
+            for (int e = 0; e < V; ++e) {
+                x0[e] *= inv * g0[e];
+                x1[e] *= inv * g1[e];
             }
         }
     }
     if (!ok || !mine) return;
-    if (a.table && l < turned) {
-        const float *cs = a.table + (int64_t)pos * a.rot + l * V;
-        float c[V], s[V];
-#pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            const float4 cc = *reinterpret_cast<const float4 *>(cs + i);
-            const float4 sn = *reinterpret_cast<const float4 *>(cs + a.rot / 2 + i);
-            c[i] = cc.x; c[i + 1] = cc.y; c[i + 2] = cc.z; c[i + 3] = cc.w;
-            s[i] = sn.x; s[i + 1] = sn.y; s[i + 2] = sn.z; s[i + 3] = sn.w;
-        }
-        if (a.interleaved) {
-            // pairs (2i, 2i + 1) of my 2V consecutive elements
-#pragma unroll
-            for (int i = 0; i < V / 2; ++i) {
-                const float p = x0[2 * i], q = x0[2 * i + 1];
-                x0[2 * i] = p * c[i] - q * s[i];
-                x0[2 * i + 1] = q * c[i] + p * s[i];
-                const float u = x1[2 * i], v = x1[2 * i + 1];
-                x1[2 * i] = u * c[V / 2 + i] - v * s[V / 2 + i];
-                x1[2 * i + 1] = v * c[V / 2 + i] + u * s[V / 2 + i];
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float p = x0[i], q = x1[i];
-                x0[i] = p * c[i] - q * s[i];
-                x1[i] = q * c[i] + p * s[i];
-            }
-        }
-    }
+    if (turns) turn<V>(x0, x1, c, s, a.interleaved);
     T *dst = r.part == 0 ? static_cast<T *>(a.q_out) + ((int64_t)r.token * a.hq + r.head) * a.d
-                         : static_cast<T *>(a.k_cache) + (slot * a.hkv + r.head) * a.d;
+                            : static_cast<T *>(a.k_cache) + (slot * a.hkv + r.head) * a.d;
     *reinterpret_cast<uint4 *>(dst + c0) = Chunk<T>::pack(x0);
     *reinterpret_cast<uint4 *>(dst + c1) = Chunk<T>::pack(x1);
     if (r.part == 1 && a.key_mass && l == 0) {
@@ -183,13 +202,212 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeArgs a, int
     }
 }
 
+// ------------------------------------------------------------- many tokens --
+// A prompt's tokens stream through shared memory: each warp has its own stages,
+// lane 0 brings a token's Q, K, V and table row in with bulk copies, the warp
+// norms and rotates the rows in place, and bulk copies take them out (a token's
+// rows are contiguous in Q's output and in each cache).  The bytes in flight no
+// longer hang on registers: one row a thread kept 32 KB of loads in flight per
+// SM, too little for the HBM's latency.  A large token gets one stage and the
+// SM 15 warps, whose loads, arithmetic and stores overlap one another's (three
+// stages and five warps were bound by the arithmetic's latency: 123 us for
+// 16384 tokens of 48 heads of 128); small tokens get three stages a warp.
+constexpr int kManyTokens = 1024;
+constexpr size_t kTokenSmem = 216 * 1024;
+
+struct StageLayout {
+    int q_bytes, k_bytes, v_bytes, t_bytes;    // of one token; t: the table row
+    int stage;                                  // bytes of a stage
+    int stages;                                 // of a warp
+    int warps;                                  // a CTA's (0: a token is too large)
+};
+
+template <typename T> StageLayout stage_layout(const NormRopeArgs &a) {
+    StageLayout l{};
+    const int64_t q = (int64_t)a.hq * a.d * sizeof(T), k = (int64_t)a.hkv * a.d * sizeof(T),
+                  v = (int64_t)a.hkv * a.dv * sizeof(T), t = a.table ? (int64_t)a.rot * 4 : 0;
+    const int64_t stage = (q + k + v + t + 127) / 128 * 128;
+    const int64_t room = (int64_t)kTokenSmem - 2 * a.d * (int64_t)sizeof(T);        // the weights' copy
+    l.stages = room / (stage * 3 + 64) >= 16 ? 3 : 1;
+    const int64_t warps = room / (stage * l.stages + 64);                            // 64: a warp's barriers
+    if (warps < 1) return l;
+    l.warps = (int)(warps > 16 ? 16 : warps);
+    l.q_bytes = (int)q;
+    l.k_bytes = (int)k;
+    l.v_bytes = (int)v;
+    l.t_bytes = (int)t;
+    l.stage = (int)stage;
+    return l;
+}
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, int bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                     tc::smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_store(void *dst, const void *src, int bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(dst), "r"(tc::smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;\n" ::: "memory"); }
+// the stores so far have read their shared memory / are done
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
+
+template <typename T, int L, int kStages>
+__global__ void __launch_bounds__(512, 1) norm_rope_tokens_kernel(NormRopeArgs a, StageLayout lay, int tokens) {
+    constexpr int V = Chunk<T>::V, kRowsAtOnce = 32 / L;
+    griddep_wait();
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % L;
+    uint8_t *ring = smem + (size_t)warp * kStages * lay.stage;
+    uint8_t *tail = smem + (size_t)lay.warps * kStages * lay.stage;
+    uint64_t *full = reinterpret_cast<uint64_t *>(tail + warp * 64);
+    T *weights = reinterpret_cast<T *>(tail + (size_t)lay.warps * 64);              // q_weight, k_weight
+    for (int i = threadIdx.x; i < a.d; i += blockDim.x) {
+        if (a.q_weight) weights[i] = static_cast<const T *>(a.q_weight)[i];
+        if (a.k_weight) weights[a.d + i] = static_cast<const T *>(a.k_weight)[i];
+    }
+    if (lane == 0) {
+        for (int i = 0; i < kStages; ++i) tc::mbar_init(&full[i], 1);
+        tc::fence_mbar_init();
+    }
+    __syncthreads();
+
+    const int turned = a.rot / (2 * V);
+    int c0 = l * 2 * V, c1 = c0 + V;
+    if (!a.interleaved && l < turned) {
+        c0 = l * V;
+        c1 = a.rot / 2 + l * V;
+    }
+    const bool mine = l * 2 * V < a.d;
+    const int walkers = (int)gridDim.x * lay.warps, me = (int)blockIdx.x * lay.warps + warp;
+    struct Token {
+        int slot, pos;       // pos < 0 with a table: it has no such row
+    };
+    auto look_up = [&](int i) -> Token {         // my i-th token
+        const int64_t t = me + (int64_t)i * walkers;
+        if (t >= tokens) return Token{0, 0};
+        const int4 m = a.plan.qmeta[a.first_token + t];
+        return Token{m.z, table_position(a, a.first_token + (int)t, m.y)};
+    };
+    // lane 0 starts the loads of my i-th token into stage i % kStages
+    auto load = [&](int i, const Token &k) {
+        const int64_t t = me + (int64_t)i * walkers;
+        if (t >= tokens || lane != 0) return;
+        const int64_t at = a.first_token + t;
+        uint8_t *st = ring + (size_t)(i % kStages) * lay.stage;
+        uint64_t *bar = &full[i % kStages];
+        const bool row = a.table && k.pos >= 0;
+        tc::mbar_arrive_expect_tx(bar, (uint32_t)(lay.q_bytes + lay.k_bytes + lay.v_bytes + (row ? lay.t_bytes : 0)));
+        bulk_load(st, static_cast<const T *>(a.q) + at * a.q_stride, lay.q_bytes, bar);
+        bulk_load(st + lay.q_bytes, static_cast<const T *>(a.k) + at * a.k_stride, lay.k_bytes, bar);
+        bulk_load(st + lay.q_bytes + lay.k_bytes, static_cast<const T *>(a.v) + at * a.v_stride, lay.v_bytes, bar);
+        if (row) bulk_load(st + lay.q_bytes + lay.k_bytes + lay.v_bytes, a.table + (int64_t)k.pos * a.rot, lay.t_bytes, bar);
+    };
+    const int steps = me < tokens ? (tokens - me + walkers - 1) / walkers : 0;
+    // tokens i .. i + kStages - 1 of step i, the last of them about to be loaded; a
+    // token's metadata is looked up a step before its loads start
+    Token queue[kStages + 1];
+#pragma unroll
+    for (int k = 0; k < kStages; ++k) {
+        queue[k] = look_up(k);
+        if (k < kStages - 1) load(k, queue[k]);
+    }
+    const unsigned group = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1u) << (lane / L * L);
+    bool ok = true;
+    int i = 0;
+    for (; i < steps; ++i) {
+        // the stage of token i + kStages - 1 held token i - 1: its stores must have read it
+        queue[kStages] = look_up(i + kStages);
+        if (lane == 0) bulk_wait_read();
+        __syncwarp();
+        load(i + kStages - 1, queue[kStages - 1]);
+        const Token cur = queue[0];
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[i % kStages], (uint32_t)((i / kStages) & 1)));
+        if (!ok) break;
+        uint8_t *st = ring + (size_t)(i % kStages) * lay.stage;
+        const int64_t at = a.first_token + me + (int64_t)i * walkers;
+        if (!a.table || cur.pos >= 0) {
+            const float *cs = reinterpret_cast<const float *>(st + lay.q_bytes + lay.k_bytes + lay.v_bytes) + l * V;
+            float c[V], sn[V];
+            const bool turns = a.table && l < turned;
+            if (turns) {
+#pragma unroll
+                for (int e = 0; e < V; e += 4) {
+                    *reinterpret_cast<float4 *>(c + e) = *reinterpret_cast<const float4 *>(cs + e);
+                    *reinterpret_cast<float4 *>(sn + e) = *reinterpret_cast<const float4 *>(cs + a.rot / 2 + e);
+                }
+            }
+            // Q rows, then K rows: they lie one after the other in the stage
+            for (int r0 = 0; r0 < a.hq + a.hkv; r0 += kRowsAtOnce) {
+                const int r = r0 + lane / L;
+                const bool live = r < a.hq + a.hkv && mine, is_q = r < a.hq;
+                T *row = reinterpret_cast<T *>(st) + (size_t)r * a.d;
+                float x0[V], x1[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) x0[e] = x1[e] = 0.f;
+                if (live) {
+                    Chunk<T>::unpack(*reinterpret_cast<const uint4 *>(row + c0), x0);
+                    Chunk<T>::unpack(*reinterpret_cast<const uint4 *>(row + c1), x1);
+                }
+                if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr) {
+                    const float inv = row_scale<V, L>(x0, x1, a.d, a.eps, group);
+                    if (live) {
+                        const T *w = weights + (is_q ? 0 : a.d);
+                        float g0[V], g1[V];
+                        Chunk<T>::unpack(*reinterpret_cast<const uint4 *>(w + c0), g0);
+                        Chunk<T>::unpack(*reinterpret_cast<const uint4 *>(w + c1), g1);
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            x0[e] *= inv * g0[e];
+                            x1[e] *= inv * g1[e];
+                        }
+                    }
+                }
+                if (!live) continue;
+                if (turns) turn<V>(x0, x1, c, sn, a.interleaved);
+                *reinterpret_cast<uint4 *>(row + c0) = Chunk<T>::pack(x0);
+                *reinterpret_cast<uint4 *>(row + c1) = Chunk<T>::pack(x1);
+            }
+            const int64_t slot = cur.slot;
+            if (a.key_mass) {
+                const int ps = a.plan.page_size;
+                for (int h = lane; h < a.hkv; h += 32) a.key_mass[(slot / ps * a.hkv + h) * ps + slot % ps] = 0.f;
+            }
+            tc::fence_proxy_async_smem();          // my rows before the bulk copies read them
+            __syncwarp();
+            if (lane == 0) {
+                bulk_store(static_cast<T *>(a.q_out) + at * a.hq * a.d, st, lay.q_bytes);
+                bulk_store(static_cast<T *>(a.k_cache) + slot * a.hkv * a.d, st + lay.q_bytes, lay.k_bytes);
+                bulk_store(static_cast<T *>(a.v_cache) + slot * a.hkv * a.dv, st + lay.q_bytes + lay.k_bytes, lay.v_bytes);
+                bulk_commit();
+            }
+        } else if (lane == 0) {
+            atomicCAS(a.status, 0, PA_DEVICE_RANGE);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kStages; ++k) queue[k] = queue[k + 1];
+    }
+    if (!ok && lane == 0) {
+        atomicCAS(a.status, 0, PA_DEVICE_TIMEOUT_TMA);
+        // tokens i .. i + kStages - 1 may still be landing in shared memory: wait for them, briefly
+        for (int k = i; k < i + kStages && k < steps; ++k)
+            tc::mbar_wait(&full[k % kStages], (uint32_t)((k / kStages) & 1), 2000000ll);
+    }
+    griddep_launch();
+    if (lane == 0) bulk_wait_all();                // shared memory outlives the stores that read it
+}
+
 // Any head dim, stride and alignment: one warp per row, one element per lane
 // and step.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(NormRopeArgs a, int64_t rows) {
+__global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(NormRopeArgs a, uint32_t rows) {
     griddep_wait();
     griddep_launch();
-    const int64_t idx = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t idx = blockIdx.x * (uint32_t)(kThreads / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (idx >= rows) return;
     const RowId r = row_id(a, idx);
@@ -238,14 +456,35 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(NormRopeArgs a,
     }
 }
 
-template <typename T, int L> cudaError_t launch_l(const NormRopeArgs &a, int64_t rows, cudaStream_t st) {
-    const int64_t blocks = (rows + kThreads / L - 1) / (kThreads / L);
-    return launch_pdl(norm_rope_kernel<T, L>, dim3((unsigned)blocks), dim3(kThreads), 0, st, a, rows);
+template <typename T, int L, int kStages>
+cudaError_t launch_tokens(const NormRopeArgs &a, const StageLayout &lay, int tokens, cudaStream_t st) {
+    static int sms = 0;
+    if (sms == 0) {
+        int dev = 0, n = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(norm_rope_tokens_kernel<T, L, kStages>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)kTokenSmem);
+        if (e != cudaSuccess) return e;
+        sms = n;
+    }
+    return launch_pdl(norm_rope_tokens_kernel<T, L, kStages>, dim3((unsigned)sms), dim3(32u * (unsigned)lay.warps),
+                      kTokenSmem, st, a, lay, tokens);
 }
 
-template <typename T> cudaError_t launch_t(const NormRopeArgs &a, cudaStream_t st) {
+template <typename T, int L> cudaError_t launch_l(const NormRopeArgs &a, uint32_t rows, cudaStream_t st) {
+    constexpr uint32_t per = kThreads / L;                // rows a CTA and step
+    const StageLayout lay = stage_layout<T>(a);
+    if (a.plan.queries >= kManyTokens && lay.warps >= 4) {
+        const int tokens = (int)(rows / (uint32_t)(a.hq + 2 * a.hkv));
+        return lay.stages == 3 ? launch_tokens<T, L, 3>(a, lay, tokens, st) : launch_tokens<T, L, 1>(a, lay, tokens, st);
+    }
+    return launch_pdl(norm_rope_kernel<T, L>, dim3((rows + per - 1) / per), dim3(kThreads), 0, st, a, rows);
+}
+
+template <typename T> cudaError_t launch_t(const NormRopeArgs &a, uint32_t rows, cudaStream_t st) {
     constexpr int V = Chunk<T>::V;
-    const int64_t rows = (int64_t)a.plan.queries * (a.hq + 2 * a.hkv);
     auto al = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
     // 16-byte chunks throughout: whole pairs of chunks per row, rotated dims a
     // whole number of them, rows and bases aligned
@@ -253,13 +492,10 @@ template <typename T> cudaError_t launch_t(const NormRopeArgs &a, cudaStream_t s
                       a.q_stride % V == 0 && a.k_stride % V == 0 && a.v_stride % V == 0 && al(a.q) && al(a.k) &&
                       al(a.v) && al(a.q_out) && al(a.k_cache) && al(a.v_cache) && al(a.table) && al(a.q_weight) &&
                       al(a.k_weight);
-    if (!wide) {
-        const int64_t blocks = (rows + kThreads / 32 - 1) / (kThreads / 32);
-        if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-        return launch_pdl(norm_rope_any_kernel<T>, dim3((unsigned)blocks), dim3(kThreads), 0, st, a, rows);
-    }
+    if (!wide)
+        return launch_pdl(norm_rope_any_kernel<T>, dim3((rows + kThreads / 32 - 1) / (kThreads / 32)), dim3(kThreads), 0, st,
+                          a, rows);
     const int lanes = a.d / (2 * V);
-    if (rows / (kThreads / 32) > INT32_MAX) return cudaErrorInvalidValue;
     if (lanes <= 4) return launch_l<T, 4>(a, rows, st);
     if (lanes <= 8) return launch_l<T, 8>(a, rows, st);
     if (lanes <= 16) return launch_l<T, 16>(a, rows, st);
@@ -268,14 +504,24 @@ template <typename T> cudaError_t launch_t(const NormRopeArgs &a, cudaStream_t s
 
 }  // namespace
 
-cudaError_t launch_norm_rope_store(const NormRopeArgs &a, cudaStream_t st) {
-    cudaError_t e;
-    switch (a.dtype) {
-        case PA_F32: e = launch_t<float>(a, st); break;
-        case PA_F16: e = launch_t<__half>(a, st); break;
-        default: e = launch_t<__nv_bfloat16>(a, st); break;
+cudaError_t launch_norm_rope_store(const NormRopeArgs &args, cudaStream_t st) {
+    // rows are counted in 32 bits: a launch takes at most 2^30 of them (one launch,
+    // but for batches of many millions of tokens)
+    const int per = args.hq + 2 * args.hkv, most = (1 << 30) / per;
+    for (int t = 0; t < args.plan.queries; t += most) {
+        NormRopeArgs a = args;
+        a.first_token = t;
+        const int left = args.plan.queries - t;
+        const uint32_t rows = (uint32_t)(left < most ? left : most) * (uint32_t)per;
+        cudaError_t e;
+        switch (a.dtype) {
+            case PA_F32: e = launch_t<float>(a, rows, st); break;
+            case PA_F16: e = launch_t<__half>(a, rows, st); break;
+            default: e = launch_t<__nv_bfloat16>(a, rows, st); break;
+        }
+        if (e != cudaSuccess) return e;
+        if (left <= most) break;
     }
-    if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 

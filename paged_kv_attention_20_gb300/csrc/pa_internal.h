@@ -134,6 +134,7 @@ struct NormRopeArgs {
     float eps;
     int32_t max_positions, rot, interleaved;
     int32_t hq, hkv, d, dv;
+    int32_t first_token;                   // of this launch
     pa_dtype dtype;
     int32_t *status;
 };

@@ -35,7 +35,7 @@ def check(got, ref, size, dt, what):
 
 def step(seq_lens, queries, hq, hkv, d, dv, ps, dt, rot, interleaved=False, norms="qk", positions=None, far=500,
          fused=False, reset=True, eps=1e-6, alias=False, seed=5):
-    case = build_case("rope", seed, seq_lens, queries, hq, hkv, d, dv, ps, dt, 0.1, pool_pages=140)
+    case = build_case("rope", seed, seq_lens, queries, hq, hkv, d, dv, ps, dt, 0.1, pool_pages=None if sum(seq_lens) > 140 else 140)
     dc = case.to("cuda")
     plan = plan_for(case)
     gen = torch.Generator().manual_seed(seed)
@@ -122,6 +122,45 @@ def test_one_query(cuda_device):
 
 def test_prompt_chunk(cuda_device):
     step([700], [(0, i) for i in range(3, 700)], 16, 4, 128, 128, 16, torch.bfloat16, 128, far=700)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("hq,hkv,d,dv,ps,rot,inter,kw", [
+    (8, 2, 128, 128, 16, 128, False, dict(fused=True)), (3, 1, 64, 32, 16, 32, True, {}), (4, 4, 96, 64, 24, 64, False, {}),
+    (2, 2, 256, 256, 64, 128, True, dict(alias=True, norms="q")), (5, 1, 512, 8, 16, 512, False, dict(norms="k")),
+    (2, 1, 16, 16, 16, 16, False, dict(norms="", reset=False)), (6, 2, 128, 128, 16, 0, False, {})])
+def test_many_tokens(cuda_device, dt, hq, hkv, d, dv, ps, rot, inter, kw):
+    """Prompts long enough for the streaming kernel: every shape it takes, its last tokens ragged over the warps."""
+    lens = [900, 401, 33]
+    queries = [(s, i) for s, n in enumerate(lens) for i in range(n) if (s, i) != (0, 5)]
+    step(lens, queries, hq, hkv, d, dv, ps, dt, rot, inter, far=900, **kw)
+
+
+def test_many_tokens_with_positions_outside_the_table(cuda_device):
+    lens = [1500]
+    case = build_case("rope", 9, lens, [(0, i) for i in range(1500)], 4, 2, 64, 64, 16, torch.bfloat16, 0.1)
+    dc, plan = case.to("cuda"), plan_for(case)
+    pos = torch.arange(1500, dtype=torch.int32, device="cuda")
+    bad = [0, 1, 700, 1499]
+    pos[bad] = torch.tensor([-5, 1500, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32, device="cuda")
+    good = torch.ones(1500, dtype=torch.bool, device="cuda")
+    good[bad] = False
+    k0, v0 = dc.k_cache.clone(), dc.v_cache.clone()
+    out = torch.full_like(dc.q, 7.0)
+    tab = table(1500, 64)
+    pka.paged_qk_norm_rope_store(plan, dc.q, dc.new_k, dc.new_v, dc.k_cache, dc.v_cache, rope_table=tab.cuda(),
+                                 positions=pos, q_out=out)
+    torch.cuda.synchronize()
+    assert pka.device_status() == 4
+    t = tab.double().numpy()
+    ref, size = norm_rope(case.q, None, 0, t[np.arange(1500), :32], t[np.arange(1500), 32:], False)
+    check(out[good], ref[good.cpu().numpy()], size[good.cpu().numpy()], torch.bfloat16, "q")
+    assert torch.all(out[~good] == 7)
+    page = np.asarray(case.block_table)[0, np.arange(1500) // 16]
+    row = np.arange(1500) % 16
+    assert bits_equal(dc.k_cache[page, row][~good], k0[page, row][~good])
+    assert bits_equal(dc.v_cache[page, row][~good], v0[page, row][~good])
+    assert bits_equal(dc.v_cache[page, row][good].cpu(), case.new_v[good.cpu()])
 
 
 def test_zero_and_large_rows(cuda_device):
