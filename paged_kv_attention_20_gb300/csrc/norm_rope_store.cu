@@ -204,15 +204,17 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NormRopeArgs a, uin
 
 // ------------------------------------------------------------- many tokens --
 // A prompt's tokens stream through shared memory: each warp has its own stages,
-// lane 0 brings a token's Q, K, V and table row in with bulk copies, the warp
-// norms and rotates the rows in place, and bulk copies take them out (a token's
-// rows are contiguous in Q's output and in each cache).  The bytes in flight no
-// longer hang on registers: one row a thread kept 32 KB of loads in flight per
-// SM, too little for the HBM's latency.  A large token gets one stage and the
-// SM 15 warps, whose loads, arithmetic and stores overlap one another's (three
-// stages and five warps were bound by the arithmetic's latency: 123 us for
-// 16384 tokens of 48 heads of 128); small tokens get three stages a warp.
-constexpr int kManyTokens = 1024;
+// lane 0 brings a token's Q, K, V and table row in with bulk copies, and the warp
+// norms, turns and writes the rows from there.  The bytes in flight no longer
+// hang on registers: with one row a thread an SM has 32 KB of loads in flight,
+// too little for the HBM's latency.  A large token gets one stage and the SM up
+// to 16 warps, whose loads, arithmetic and stores overlap one another's; small
+// tokens get three stages a warp.  16384 tokens of 32 + 8 + 8 heads of 128 (bf16,
+// 411 MB): one row a thread 98 us, three stages and five warps 123 us, one stage
+// and 16 warps with bulk stores 82 us (a stage waited for its stores to be
+// read), weights and turn folded into packed coefficients 79 us, stores from
+// registers 75 us (5.5 TB/s).
+constexpr int kManyTokens = 2048;
 constexpr size_t kTokenSmem = 216 * 1024;
 
 struct StageLayout {
@@ -246,14 +248,103 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, int bytes,
                  "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
                  : "memory");
 }
-__device__ __forceinline__ void bulk_store(void *dst, const void *src, int bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(dst), "r"(tc::smem_u32(src)), "r"(bytes)
-                 : "memory");
+
+// 16 bytes of T as V / 2 float pairs and back.
+template <typename T> struct Pairs {
+    static constexpr int N = 8 / sizeof(T);
+    static __device__ __forceinline__ float2 pair(uint32_t w);
+    static __device__ __forceinline__ uint32_t word(float2 x);
+    static __device__ __forceinline__ void unpack(const uint4 &w, float2 *p) {
+        p[0] = pair(w.x); p[1] = pair(w.y); p[2] = pair(w.z); p[3] = pair(w.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float2 *p) {
+        return make_uint4(word(p[0]), word(p[1]), word(p[2]), word(p[3]));
+    }
+};
+template <> __device__ __forceinline__ float2 Pairs<__nv_bfloat16>::pair(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;\n" ::: "memory"); }
-// the stores so far have read their shared memory / are done
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
+template <> __device__ __forceinline__ uint32_t Pairs<__nv_bfloat16>::word(float2 x) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <> __device__ __forceinline__ float2 Pairs<__half>::pair(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+template <> __device__ __forceinline__ uint32_t Pairs<__half>::word(float2 x) {
+    const __half2 h = __floats2half2_rn(x.x, x.y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <> struct Pairs<float> {
+    static constexpr int N = 2;
+    static __device__ __forceinline__ void unpack(const uint4 &w, float2 *p) {
+        p[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+        p[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
+    }
+    static __device__ __forceinline__ uint4 pack(const float2 *p) {
+        return make_uint4(__float_as_uint(p[0].x), __float_as_uint(p[0].y), __float_as_uint(p[1].x), __float_as_uint(p[1].y));
+    }
+};
+
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;\n"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+// The norm's weights and the turn of a token folded into 2 * 2N coefficient pairs
+// for my 2N element pairs p (chunk c0: p[0..N), chunk c1: p[N..2N)).  The turn is
+// linear, so with p scaled by the norm a row becomes
+//   halves:     out[i] = p[i] cf[i] + p[N+i] cf[N+i],  out[N+i] = p[N+i] cf[2N+i] + p[i] cf[3N+i]
+//   neighbours: out[i] = p[i] cf[i] + swapped(p[i]) cf[2N+i]
+template <typename T>
+__device__ __forceinline__ void coefficients(float2 (&cf)[4 * Pairs<T>::N], uint32_t weights, bool weighted, int c0, int c1,
+                                             bool mine, uint32_t table_row, int half_bytes, int l, bool turns, bool interleaved) {
+    constexpr int N = Pairs<T>::N, V = 2 * N;
+    float2 g[2 * N];
+#pragma unroll
+    for (int i = 0; i < 2 * N; ++i) g[i] = make_float2(1.f, 1.f);
+    if (weighted && mine) {
+        Pairs<T>::unpack(lds16(weights + (uint32_t)(c0 * sizeof(T))), g);
+        Pairs<T>::unpack(lds16(weights + (uint32_t)(c1 * sizeof(T))), g + N);
+    }
+    float2 c[N], sn[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        c[i] = make_float2(1.f, 1.f);
+        sn[i] = make_float2(0.f, 0.f);
+    }
+    if (turns) {
+#pragma unroll
+        for (int e = 0; e < V; e += 4) {
+            Pairs<float>::unpack(lds16(table_row + (uint32_t)(4 * (l * V + e))), c + e / 2);
+            Pairs<float>::unpack(lds16(table_row + (uint32_t)half_bytes + (uint32_t)(4 * (l * V + e))), sn + e / 2);
+        }
+    }
+    if (interleaved) {
+        // pair i of my 2N turns by angle i: (c, c) and (-s, s) for (x, y) and (y, x)
+#pragma unroll
+        for (int i = 0; i < 2 * N; ++i) {
+            const float ci = i & 1 ? c[i / 2].y : c[i / 2].x, si = i & 1 ? sn[i / 2].y : sn[i / 2].x;
+            cf[i] = make_float2(g[i].x * ci, g[i].y * ci);
+            cf[2 * N + i] = make_float2(-g[i].y * si, g[i].x * si);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            cf[i] = fmul2(g[i], c[i]);
+            cf[N + i] = fmul2(g[N + i], make_float2(-sn[i].x, -sn[i].y));
+            cf[2 * N + i] = fmul2(g[N + i], c[i]);
+            cf[3 * N + i] = fmul2(g[i], sn[i]);
+        }
+    }
+}
 
 template <typename T, int L, int kStages>
 __global__ void __launch_bounds__(512, 1) norm_rope_tokens_kernel(NormRopeArgs a, StageLayout lay, int tokens) {
@@ -315,14 +406,11 @@ __global__ void __launch_bounds__(512, 1) norm_rope_tokens_kernel(NormRopeArgs a
         queue[k] = look_up(k);
         if (k < kStages - 1) load(k, queue[k]);
     }
-    const unsigned group = L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1u) << (lane / L * L);
     bool ok = true;
     int i = 0;
     for (; i < steps; ++i) {
-        // the stage of token i + kStages - 1 held token i - 1: its stores must have read it
+        // the stage of token i + kStages - 1 held token i - 1, which every lane is done with
         queue[kStages] = look_up(i + kStages);
-        if (lane == 0) bulk_wait_read();
-        __syncwarp();
         load(i + kStages - 1, queue[kStages - 1]);
         const Token cur = queue[0];
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[i % kStages], (uint32_t)((i / kStages) & 1)));
@@ -330,60 +418,73 @@ __global__ void __launch_bounds__(512, 1) norm_rope_tokens_kernel(NormRopeArgs a
         uint8_t *st = ring + (size_t)(i % kStages) * lay.stage;
         const int64_t at = a.first_token + me + (int64_t)i * walkers;
         if (!a.table || cur.pos >= 0) {
-            const float *cs = reinterpret_cast<const float *>(st + lay.q_bytes + lay.k_bytes + lay.v_bytes) + l * V;
-            float c[V], sn[V];
+            constexpr int N = Pairs<T>::N;
+            const uint32_t stage = tc::smem_u32(st);
             const bool turns = a.table && l < turned;
-            if (turns) {
+            // the Q rows with Q's weights, then the K rows with K's (they follow in the stage)
+#pragma unroll 1
+            for (int part = 0; part < 2; ++part) {
+                const int rows = part == 0 ? a.hq : a.hkv;
+                const bool weighted = (part == 0 ? a.q_weight : a.k_weight) != nullptr;
+                float2 cf[4 * N];
+                coefficients<T>(cf, tc::smem_u32(weights + (part == 0 ? 0 : a.d)), weighted, c0, c1, mine,
+                                stage + (uint32_t)(lay.q_bytes + lay.k_bytes + lay.v_bytes), 2 * a.rot, l, turns,
+                                a.interleaved && turns);
+                T *dst = part == 0 ? static_cast<T *>(a.q_out) + at * a.hq * a.d
+                                   : static_cast<T *>(a.k_cache) + (int64_t)cur.slot * a.hkv * a.d;
+                const uint32_t base = stage + (uint32_t)(part == 0 ? 0 : lay.q_bytes);
+#pragma unroll 2
+                for (int r0 = 0; r0 < rows; r0 += kRowsAtOnce) {
+                    const int r = r0 + lane / L;
+                    const bool live = r < rows && mine;
+                    const uint32_t row = base + (uint32_t)((live ? r : 0) * a.d * (int)sizeof(T));
+                    float2 p[2 * N], o[2 * N];
+                    Pairs<T>::unpack(lds16(row + (uint32_t)((live ? c0 : 0) * sizeof(T))), p);
+                    Pairs<T>::unpack(lds16(row + (uint32_t)((live ? c1 : 0) * sizeof(T))), p + N);
+                    if (weighted) {
+                        float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int e = 0; e < V; e += 4) {
-                    *reinterpret_cast<float4 *>(c + e) = *reinterpret_cast<const float4 *>(cs + e);
-                    *reinterpret_cast<float4 *>(sn + e) = *reinterpret_cast<const float4 *>(cs + a.rot / 2 + e);
-                }
-            }
-            // Q rows, then K rows: they lie one after the other in the stage
-            for (int r0 = 0; r0 < a.hq + a.hkv; r0 += kRowsAtOnce) {
-                const int r = r0 + lane / L;
-                const bool live = r < a.hq + a.hkv && mine, is_q = r < a.hq;
-                T *row = reinterpret_cast<T *>(st) + (size_t)r * a.d;
-                float x0[V], x1[V];
+                        for (int i = 0; i < 2 * N; ++i) ss = tc::ffma2(p[i], p[i], ss);
+                        float sum = live ? ss.x + ss.y : 0.f;
 #pragma unroll
-                for (int e = 0; e < V; ++e) x0[e] = x1[e] = 0.f;
-                if (live) {
-                    Chunk<T>::unpack(*reinterpret_cast<const uint4 *>(row + c0), x0);
-                    Chunk<T>::unpack(*reinterpret_cast<const uint4 *>(row + c1), x1);
-                }
-                if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr) {
-                    const float inv = row_scale<V, L>(x0, x1, a.d, a.eps, group);
-                    if (live) {
-                        const T *w = weights + (is_q ? 0 : a.d);
-                        float g0[V], g1[V];
-                        Chunk<T>::unpack(*reinterpret_cast<const uint4 *>(w + c0), g0);
-                        Chunk<T>::unpack(*reinterpret_cast<const uint4 *>(w + c1), g1);
+                        for (int o2 = L / 2; o2; o2 >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2);
+                        const float inv = rsqrtf(sum / (float)a.d + a.eps);
 #pragma unroll
-                        for (int e = 0; e < V; ++e) {
-                            x0[e] *= inv * g0[e];
-                            x1[e] *= inv * g1[e];
+                        for (int i = 0; i < 2 * N; ++i) p[i] = fmul2(p[i], make_float2(inv, inv));
+                    }
+                    if (!turns) {
+                        // no partner's value enters, not even times 0
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            o[i] = fmul2(p[i], cf[i]);
+                            o[N + i] = fmul2(p[N + i], cf[2 * N + i]);
+                        }
+                    } else if (a.interleaved) {
+#pragma unroll
+                        for (int i = 0; i < 2 * N; ++i)
+                            o[i] = tc::ffma2(p[i], cf[i], fmul2(make_float2(p[i].y, p[i].x), cf[2 * N + i]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            o[i] = tc::ffma2(p[i], cf[i], fmul2(p[N + i], cf[N + i]));
+                            o[N + i] = tc::ffma2(p[N + i], cf[2 * N + i], fmul2(p[i], cf[3 * N + i]));
                         }
                     }
+                    if (live) {
+                        *reinterpret_cast<uint4 *>(dst + (int64_t)r * a.d + c0) = Pairs<T>::pack(o);
+                        *reinterpret_cast<uint4 *>(dst + (int64_t)r * a.d + c1) = Pairs<T>::pack(o + N);
+                    }
                 }
-                if (!live) continue;
-                if (turns) turn<V>(x0, x1, c, sn, a.interleaved);
-                *reinterpret_cast<uint4 *>(row + c0) = Chunk<T>::pack(x0);
-                *reinterpret_cast<uint4 *>(row + c1) = Chunk<T>::pack(x1);
             }
             const int64_t slot = cur.slot;
             if (a.key_mass) {
                 const int ps = a.plan.page_size;
                 for (int h = lane; h < a.hkv; h += 32) a.key_mass[(slot / ps * a.hkv + h) * ps + slot % ps] = 0.f;
             }
-            tc::fence_proxy_async_smem();          // my rows before the bulk copies read them
-            __syncwarp();
-            if (lane == 0) {
-                bulk_store(static_cast<T *>(a.q_out) + at * a.hq * a.d, st, lay.q_bytes);
-                bulk_store(static_cast<T *>(a.k_cache) + slot * a.hkv * a.d, st + lay.q_bytes, lay.k_bytes);
-                bulk_store(static_cast<T *>(a.v_cache) + slot * a.hkv * a.dv, st + lay.q_bytes + lay.k_bytes, lay.v_bytes);
-                bulk_commit();
-            }
+            uint4 *vd = reinterpret_cast<uint4 *>(static_cast<T *>(a.v_cache) + slot * a.hkv * a.dv);
+            const uint32_t vs = stage + (uint32_t)(lay.q_bytes + lay.k_bytes);
+#pragma unroll 4
+            for (int c = lane; c < lay.v_bytes / 16; c += 32) vd[c] = lds16(vs + (uint32_t)(16 * c));
         } else if (lane == 0) {
             atomicCAS(a.status, 0, PA_DEVICE_RANGE);
         }
@@ -398,7 +499,6 @@ __global__ void __launch_bounds__(512, 1) norm_rope_tokens_kernel(NormRopeArgs a
             tc::mbar_wait(&full[k % kStages], (uint32_t)((k / kStages) & 1), 2000000ll);
     }
     griddep_launch();
-    if (lane == 0) bulk_wait_all();                // shared memory outlives the stores that read it
 }
 
 // Any head dim, stride and alignment: one warp per row, one element per lane

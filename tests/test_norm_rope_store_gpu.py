@@ -131,33 +131,33 @@ def test_prompt_chunk(cuda_device):
     (2, 1, 16, 16, 16, 16, False, dict(norms="", reset=False)), (6, 2, 128, 128, 16, 0, False, {})])
 def test_many_tokens(cuda_device, dt, hq, hkv, d, dv, ps, rot, inter, kw):
     """Prompts long enough for the streaming kernel: every shape it takes, its last tokens ragged over the warps."""
-    lens = [900, 401, 33]
+    lens = [1500, 801, 33]
     queries = [(s, i) for s, n in enumerate(lens) for i in range(n) if (s, i) != (0, 5)]
-    step(lens, queries, hq, hkv, d, dv, ps, dt, rot, inter, far=900, **kw)
+    step(lens, queries, hq, hkv, d, dv, ps, dt, rot, inter, far=1500, **kw)
 
 
 def test_many_tokens_with_positions_outside_the_table(cuda_device):
-    lens = [1500]
-    case = build_case("rope", 9, lens, [(0, i) for i in range(1500)], 4, 2, 64, 64, 16, torch.bfloat16, 0.1)
+    lens = [2500]
+    case = build_case("rope", 9, lens, [(0, i) for i in range(2500)], 4, 2, 64, 64, 16, torch.bfloat16, 0.1)
     dc, plan = case.to("cuda"), plan_for(case)
-    pos = torch.arange(1500, dtype=torch.int32, device="cuda")
-    bad = [0, 1, 700, 1499]
-    pos[bad] = torch.tensor([-5, 1500, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32, device="cuda")
-    good = torch.ones(1500, dtype=torch.bool, device="cuda")
+    pos = torch.arange(2500, dtype=torch.int32, device="cuda")
+    bad = [0, 1, 700, 2499]
+    pos[bad] = torch.tensor([-5, 2500, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32, device="cuda")
+    good = torch.ones(2500, dtype=torch.bool, device="cuda")
     good[bad] = False
     k0, v0 = dc.k_cache.clone(), dc.v_cache.clone()
     out = torch.full_like(dc.q, 7.0)
-    tab = table(1500, 64)
+    tab = table(2500, 64)
     pka.paged_qk_norm_rope_store(plan, dc.q, dc.new_k, dc.new_v, dc.k_cache, dc.v_cache, rope_table=tab.cuda(),
                                  positions=pos, q_out=out)
     torch.cuda.synchronize()
     assert pka.device_status() == 4
     t = tab.double().numpy()
-    ref, size = norm_rope(case.q, None, 0, t[np.arange(1500), :32], t[np.arange(1500), 32:], False)
+    ref, size = norm_rope(case.q, None, 0, t[np.arange(2500), :32], t[np.arange(2500), 32:], False)
     check(out[good], ref[good.cpu().numpy()], size[good.cpu().numpy()], torch.bfloat16, "q")
     assert torch.all(out[~good] == 7)
-    page = np.asarray(case.block_table)[0, np.arange(1500) // 16]
-    row = np.arange(1500) % 16
+    page = np.asarray(case.block_table)[0, np.arange(2500) // 16]
+    row = np.arange(2500) % 16
     assert bits_equal(dc.k_cache[page, row][~good], k0[page, row][~good])
     assert bits_equal(dc.v_cache[page, row][~good], v0[page, row][~good])
     assert bits_equal(dc.v_cache[page, row][good].cpu(), case.new_v[good.cpu()])
