@@ -49,8 +49,11 @@ MassLayout mass_layout(const pa_plan *plan, int32_t hq, int32_t dv, int32_t spli
     const size_t part = splits > 1 ? align256((size_t)splits * rows * dv * sizeof(float)) : 0;
     l.lse = part;
     l.lse_final = l.lse + align256((size_t)splits * rows * sizeof(float));
-    l.groups = l.lse_final + (splits > 1 && plan->n_tiles > 0 ? align256(rows * sizeof(float)) : 0);
-    l.scores = l.groups + align256((2 * ((size_t)plan->sequences + 1) + plan->queries) * sizeof(int32_t));
+    l.items = l.lse_final + (splits > 1 && plan->n_tiles > 0 ? align256(rows * sizeof(float)) : 0);
+    // work lists: [sequences + 1] starts and the records (the tiles' also the key blocks)
+    const size_t seqs = (size_t)plan->sequences + 1;
+    l.tiles = l.items + align256((seqs + plan->n_decode) * sizeof(int32_t));
+    l.scores = l.tiles + (plan->n_tiles > 0 ? align256((2 * seqs + plan->queries) * sizeof(int32_t)) : 0);
     int64_t keys = std::max<int64_t>(max_keys, plan->max_seq_len);
     if (window > 0) keys = std::min<int64_t>(keys, window);
     l.cap = plan->n_decode > 0 ? (keys + 31) / 32 * 32 : 0;
@@ -58,8 +61,9 @@ MassLayout mass_layout(const pa_plan *plan, int32_t hq, int32_t dv, int32_t spli
     return l;
 }
 
-cudaError_t add_mass(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass,
-                     cudaStream_t st) {
+namespace {
+
+MassArgs mass_args(const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass, size_t lists) {
     MassArgs m{};
     m.plan = a.plan;
     m.q = a.q; m.k = a.k;
@@ -68,29 +72,47 @@ cudaError_t add_mass(const pa_plan *plan, const AttnArgs &a, const MassLayout &l
     m.lse_final = a.splits > 1 ? reinterpret_cast<float *>(ws + lay.lse_final) : a.ws_lse;
     m.scores = a.scores;
     m.cap = a.score_cap;
-    m.group_start = reinterpret_cast<int32_t *>(ws + lay.groups);
-    m.unit_start = m.group_start + plan->sequences + 1;
-    m.group_list = m.unit_start + plan->sequences + 1;
+    m.group_start = reinterpret_cast<int32_t *>(ws + lists);
     m.hq = a.hq; m.hkv = a.hkv; m.d = a.d;
     m.splits = a.splits; m.causal = a.causal; m.window = a.window;
     m.scale = a.scale;
     m.dtype = a.dtype;
     m.status = a.status;
+    return m;
+}
+
+MassArgs tile_args(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass) {
+    MassArgs m = mass_args(a, lay, ws, key_mass, lay.tiles);
+    m.unit_start = m.group_start + plan->sequences + 1;
+    m.group_list = m.unit_start + plan->sequences + 1;
+    m.longest = (int32_t)std::max(longest_tile_seq(plan), plan->max_seq_len);
+    return m;
+}
+
+}  // namespace
+
+cudaError_t add_item_mass(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass, bool merge,
+                          bool use_list, cudaStream_t st) {
+    MassArgs m = mass_args(a, lay, ws, key_mass, lay.items);
+    m.group_list = m.group_start + plan->sequences + 1;
+    m.longest = (int32_t)plan->max_seq_len;
+    const bool repeated = (plan_facts(plan) & kFactRepeatedItems) != 0;
+    cudaError_t e = repeated ? launch_mass_index(m, kMassItems, st) : cudaSuccess;
+    if (e == cudaSuccess) e = launch_mass_items(m, repeated, merge ? &a : nullptr, use_list, st);
+    return e;
+}
+
+cudaError_t mass_tile_lists(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass,
+                            cudaStream_t st) {
+    return launch_mass_index(tile_args(plan, a, lay, ws, key_mass), prefill_supported(a) ? kMassTiles : kMassQueries, st);
+}
+
+cudaError_t add_tile_mass(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass,
+                          int tile_ctas_per_sm, cudaStream_t st) {
+    const MassArgs m = tile_args(plan, a, lay, ws, key_mass);
     cudaError_t e = cudaSuccess;
-    if (a.scores) {
-        const bool repeated = (plan_facts(plan) & kFactRepeatedItems) != 0;
-        m.longest = (int32_t)plan->max_seq_len;
-        if (repeated) e = launch_mass_index(m, kMassItems, st);
-        if (e == cudaSuccess) e = launch_mass_items(m, repeated, st);
-    }
-    if (e == cudaSuccess && plan->n_tiles > 0) {
-        // prefill tiles on the tensor-core kernel; otherwise every query of the plan
-        const bool tensor = prefill_supported(a);
-        m.longest = (int32_t)std::max(longest_tile_seq(plan), plan->max_seq_len);
-        e = launch_mass_index(m, tensor ? kMassTiles : kMassQueries, st);
-        if (e == cudaSuccess && a.splits > 1) e = launch_lse_final(m, reinterpret_cast<float *>(ws + lay.lse_final), st);
-        if (e == cudaSuccess) e = tensor ? launch_mass_tiles(m, st) : launch_mass_recompute(m, st);
-    }
+    if (a.splits > 1) e = launch_lse_final(m, reinterpret_cast<float *>(ws + lay.lse_final), st);
+    if (e == cudaSuccess) e = prefill_supported(a) ? launch_mass_tiles(m, tile_ctas_per_sm, st) : launch_mass_recompute(m, st);
     return e;
 }
 

@@ -17,6 +17,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "merge.cuh"
 #include "pa_internal.h"
 
 namespace pa {
@@ -76,9 +77,40 @@ __device__ __forceinline__ int block_prefix(int c, int *sums) {
 __global__ void __launch_bounds__(kIndexThreads) mass_index_kernel(MassArgs a, int kind, int n) {
     griddep_wait();
     griddep_launch();
-    __shared__ int seqs[kIndexThreads];
+    __shared__ __align__(16) int seqs[kIndexThreads];
     __shared__ int carry, sums[32];
     const int S = a.plan.sequences, tid = threadIdx.x;
+    if (n <= kIndexThreads && S < kIndexThreads) {
+        // the usual sizes: one pass in shared memory, a sequence and a record per thread
+        __shared__ int count[kIndexThreads];
+        count[tid] = 0;
+        const int mine = tid < n ? record_seq(a.plan, kind, tid) : -1;
+        const int len = kind == kMassTiles && tid < S ? a.plan.seq_lens[tid] : 0;
+        seqs[tid] = mine;
+        __syncthreads();
+        if (mine >= 0) atomicAdd(&count[mine], 1);
+        __syncthreads();
+        const int c = count[tid];
+        const int upto = block_prefix(c, sums);
+        if (tid <= S) a.group_start[tid] = upto - c;
+        count[tid] = upto - c;
+        __syncthreads();
+        if (mine >= 0) {
+            // records of the same sequence before mine
+            int before = 0, t = 0;
+            for (; t + 4 <= tid; t += 4) {
+                const int4 v = *reinterpret_cast<const int4 *>(seqs + t);
+                before += (v.x == mine) + (v.y == mine) + (v.z == mine) + (v.w == mine);
+            }
+            for (; t < tid; ++t) before += seqs[t] == mine;
+            a.group_list[count[mine] + before] = tid;
+        }
+        if (kind != kMassTiles) return;
+        const int blocks = c > 0 ? (len + 127) / 128 : 0;
+        const int to = block_prefix(blocks, sums);
+        if (tid <= S) a.unit_start[tid] = to - blocks;
+        return;
+    }
     for (int s = tid; s <= S; s += kIndexThreads) a.group_start[s] = 0;
     __syncthreads();
     for (int i = tid; i < n; i += kIndexThreads) atomicAdd(&a.group_start[record_seq(a.plan, kind, i)], 1);
@@ -140,22 +172,23 @@ __global__ void __launch_bounds__(kIndexThreads) mass_index_kernel(MassArgs a, i
 // ------------------------------------------------------------ decode items --
 constexpr int kItemThreads = 256, kItemWarps = kItemThreads / 32;
 constexpr int kItemKeys = 4 * kItemThreads;     // four keys a thread and step
+constexpr int kHeadsAtOnce = 4;                 // score rows in flight
 constexpr int kMaxStagedHeads = 64;
 
 // One CTA per (sequence or item, KV head, block of keys): four consecutive keys
 // per thread and step, the group's heads in turn.  The scores come from L2 when
 // they fit there (4 bytes a key and head), the totals are read and written once.
+// The pass is latency-bound (metadata, then scores, table and log-sum-exps, then
+// the totals): the first step's scores are asked for before the log-sum-exps are
+// merged.
 // Key j always falls to block (j / kItemKeys) % blocks and to one thread of it,
 // whatever an item's own range: the items of a sequence never meet on a key.
 // kQuads: pages hold whole aligned fours of keys and the totals are 16-byte
 // aligned.
 template <bool kQuads>
-__global__ void __launch_bounds__(kItemThreads) mass_items_kernel(MassArgs a, int repeated, int blocks, int ps_shift) {
-    griddep_wait();
-    griddep_launch();
-    __shared__ float lse[kMaxStagedHeads];
-    const int blk = blockIdx.x % blocks;
-    const int rest = blockIdx.x / blocks;
+__device__ __forceinline__ void add_items(const MassArgs &a, int repeated, int blocks, int ps_shift, int block, float *lse) {
+    const int blk = block % blocks;
+    const int rest = block / blocks;
     const int kvh = rest % a.hkv, unit = rest / a.hkv;
     const int G = a.hq / a.hkv, ps = a.plan.page_size;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -179,6 +212,16 @@ __global__ void __launch_bounds__(kItemThreads) mass_items_kernel(MassArgs a, in
         const int32_t *trow = a.plan.table + (int64_t)meta.x * a.plan.width;
         for (int g0 = 0; g0 < G; g0 += kMaxStagedHeads) {
             const int gn = min(G - g0, kMaxStagedHeads);
+            const float *head0 = a.scores + ((int64_t)item * a.hq + kvh * G + g0) * a.cap - lo;
+            float4 early[kHeadsAtOnce];
+            auto whole = [&](int64_t j) { return j >= lo && j + 4 <= hi && (lo & 3) == 0; };
+            auto ask = [&](int64_t j) {                 // the first heads' scores of four keys
+#pragma unroll
+                for (int g = 0; g < kHeadsAtOnce; ++g)
+                    if (whole(j) && g < gn) early[g] = *reinterpret_cast<const float4 *>(head0 + j + g * a.cap);
+            };
+            const int64_t j0 = start + 4 * (int)threadIdx.x;
+            ask(j0);
             __syncthreads();
             // a head per warp: its log-sum-exp over the splits (two a lane, at most 64), log2 units
             for (int g = warp; g < gn; g += kItemWarps) {
@@ -192,32 +235,47 @@ __global__ void __launch_bounds__(kItemThreads) mass_items_kernel(MassArgs a, in
                 if (lane == 0) lse[g] = a.splits == 1 ? l0 : m + log2f(t);
             }
             __syncthreads();
-            const float *head0 = a.scores + ((int64_t)item * a.hq + kvh * G + g0) * a.cap - lo;
-            for (int64_t base = start; base < hi; base += step) {
-                const int j = (int)base + 4 * (int)threadIdx.x;
-                if (j >= hi || j + 4 <= lo) continue;
+            for (int64_t j64 = j0; j64 < hi; j64 += step) {
+                if (j64 + 4 <= lo) {
+                    ask(j64 + step);
+                    continue;
+                }
+                const int j = (int)j64;
                 const float *sc = head0 + j;
                 const bool all = j >= lo && j + 4 <= hi;
+                float4 *m = nullptr;
+                float4 old;
+                if (kQuads && all) {
+                    const int pg = ps_shift >= 0 ? j >> ps_shift : j / ps;
+                    m = reinterpret_cast<float4 *>(a.key_mass + ((int64_t)trow[pg] * a.hkv + kvh) * ps + (j - pg * ps));
+                    old = *m;
+                }
                 float p[4] = {0.f, 0.f, 0.f, 0.f};
-                if (all && (lo & 3) == 0) {
+                if (whole(j)) {
+#pragma unroll
+                    for (int g = 0; g < kHeadsAtOnce; ++g)
+                        if (g < gn) {
+                            const float4 v = early[g];
+                            const float l = lse[g];
+                            p[0] += exp2f(v.x - l); p[1] += exp2f(v.y - l); p[2] += exp2f(v.z - l); p[3] += exp2f(v.w - l);
+                        }
+                    ask(j64 + step);
 #pragma unroll 4
-                    for (int g = 0; g < gn; ++g) {
+                    for (int g = kHeadsAtOnce; g < gn; ++g) {
                         const float4 v = *reinterpret_cast<const float4 *>(sc + g * a.cap);
                         const float l = lse[g];
                         p[0] += exp2f(v.x - l); p[1] += exp2f(v.y - l); p[2] += exp2f(v.z - l); p[3] += exp2f(v.w - l);
                     }
                 } else {
+                    ask(j64 + step);
                     for (int g = 0; g < gn; ++g)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             if (j + i >= lo && j + i < hi) p[i] += exp2f(sc[g * a.cap + i] - lse[g]);
                 }
                 if (kQuads && all) {
-                    const int pg = ps_shift >= 0 ? j >> ps_shift : j / ps;
-                    float4 *m = reinterpret_cast<float4 *>(a.key_mass + ((int64_t)trow[pg] * a.hkv + kvh) * ps + (j - pg * ps));
-                    float4 v = *m;
-                    v.x += p[0]; v.y += p[1]; v.z += p[2]; v.w += p[3];
-                    *m = v;
+                    old.x += p[0]; old.y += p[1]; old.z += p[2]; old.w += p[3];
+                    *m = old;
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -228,6 +286,34 @@ __global__ void __launch_bounds__(kItemThreads) mass_items_kernel(MassArgs a, in
                 }
             }
         }
+    }
+}
+
+template <bool kQuads>
+__global__ void __launch_bounds__(kItemThreads) mass_items_kernel(MassArgs a, int repeated, int blocks, int ps_shift) {
+    griddep_wait();
+    griddep_launch();
+    __shared__ float lse[kMaxStagedHeads];
+    add_items<kQuads>(a, repeated, blocks, ps_shift, blockIdx.x, lse);
+}
+
+// The merge of the split outputs and the totals in one launch: both follow the
+// decode kernel and neither needs the other.  The first merge_blocks CTAs merge.
+template <typename T, int VEC, bool kQuads>
+__global__ void __launch_bounds__(kItemThreads) merge_and_items_kernel(AttnArgs attn, MassArgs a, int use_list, int nrows,
+                                                                       int wide, int merge_blocks, int repeated, int blocks,
+                                                                       int ps_shift) {
+    griddep_wait();
+    griddep_launch();
+    extern __shared__ float part[];
+    __shared__ float lse[kMaxStagedHeads];
+    if ((int)blockIdx.x < merge_blocks) {
+        if (wide)
+            merge_row_wide<T, VEC>(attn, use_list, blockIdx.x, part);
+        else
+            merge_rows<T, VEC>(attn, use_list, nrows, blockIdx.x);
+    } else {
+        add_items<kQuads>(a, repeated, blocks, ps_shift, (int)blockIdx.x - merge_blocks, lse);
     }
 }
 
@@ -330,18 +416,48 @@ cudaError_t launch_lse_final(const MassArgs &a, float *out, cudaStream_t st) {
     return launch_pdl(lse_final_kernel, dim3((unsigned)((rows + 255) / 256)), dim3(256), 0, st, a, out);
 }
 
-cudaError_t launch_mass_items(const MassArgs &a, bool repeated, cudaStream_t st) {
+cudaError_t launch_mass_items(const MassArgs &a, bool repeated, const AttnArgs *merge, bool use_list, cudaStream_t st) {
     const int64_t units = (int64_t)(repeated ? a.plan.sequences : a.plan.n_decode) * a.hkv;
-    const int blocks = blocks_for(units, ((int64_t)a.longest + kItemKeys - 1) / kItemKeys);
+    // blocks a unit: one per 1024 keys of the longest history, but no more CTAs than
+    // about twice what the GPU holds (each strides over its keys)
+    const int64_t most = ((int64_t)a.longest + kItemKeys - 1) / kItemKeys, fill = (2 * 152 * 8 + units - 1) / units;
+    const int blocks = blocks_for(units, most < fill ? most : fill);
     const int ps = a.plan.page_size;
     int shift = -1;
     if ((ps & (ps - 1)) == 0)
         for (shift = 0; (1 << shift) < ps; ++shift) {}
     const bool quads = ps % 4 == 0 && reinterpret_cast<uintptr_t>(a.key_mass) % 16 == 0;
-    const dim3 grid((unsigned)(units * blocks)), block(kItemThreads);
+    const dim3 block(kItemThreads);
     const int rep = repeated ? 1 : 0;
-    cudaError_t e = quads ? launch_pdl(mass_items_kernel<true>, grid, block, 0, st, a, rep, blocks, shift)
-                          : launch_pdl(mass_items_kernel<false>, grid, block, 0, st, a, rep, blocks, shift);
+    cudaError_t e;
+    if (!merge) {
+        const dim3 grid((unsigned)(units * blocks));
+        e = quads ? launch_pdl(mass_items_kernel<true>, grid, block, 0, st, a, rep, blocks, shift)
+                  : launch_pdl(mass_items_kernel<false>, grid, block, 0, st, a, rep, blocks, shift);
+    } else {
+        const int nrows = (use_list ? a.plan.n_decode : a.plan.queries) * a.hq;
+        const bool wide = merge_is_wide(*merge, nrows);
+        const int64_t mb = wide ? nrows : (nrows + 7) / 8;
+        if (mb + units * blocks > INT32_MAX) return cudaErrorInvalidValue;
+        const dim3 grid((unsigned)(mb + units * blocks));
+        const size_t smem = wide ? (size_t)8 * merge->dv * sizeof(float) : 0;
+        auto launch = [&](auto kernel) {
+            return launch_pdl(kernel, grid, block, smem, st, *merge, a, use_list ? 1 : 0, nrows, wide ? 1 : 0, (int)mb, rep,
+                              blocks, shift);
+        };
+        auto by_vec = [&](auto t) {
+            using T = decltype(t);
+            const int vec = merge_vec(*merge);
+            if (quads)
+                return vec == 4   ? launch(merge_and_items_kernel<T, 4, true>)
+                       : vec == 2 ? launch(merge_and_items_kernel<T, 2, true>)
+                                  : launch(merge_and_items_kernel<T, 1, true>);
+            return vec == 4   ? launch(merge_and_items_kernel<T, 4, false>)
+                   : vec == 2 ? launch(merge_and_items_kernel<T, 2, false>)
+                              : launch(merge_and_items_kernel<T, 1, false>);
+        };
+        e = a.dtype == PA_F32 ? by_vec(float()) : (a.dtype == PA_F16 ? by_vec(__half()) : by_vec(__nv_bfloat16()));
+    }
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }

@@ -346,25 +346,20 @@ bool make_map(CUtensorMap *m, const void *base, int heads, int64_t rows, int box
 
 }  // namespace
 
-cudaError_t launch_mass_tiles(const MassArgs &a, cudaStream_t st) {
+cudaError_t launch_mass_tiles(const MassArgs &a, int ctas_per_sm, cudaStream_t st) {
     const bool bf16 = a.dtype == PA_BF16;
     CUtensorMap tq, tk;
     if (!make_map(&tq, a.q, a.hq, a.plan.queries, kQ, bf16) ||
         !make_map(&tk, a.k, a.hkv, (int64_t)a.plan.pages * a.plan.page_size, a.plan.page_size, bf16))
         return cudaErrorInvalidValue;
-    static int resident = 0;
-    if (resident == 0) {
+    static int sms = 0;
+    if (sms == 0) {
+        int dev = 0, n = 0;
         cudaError_t e = cudaFuncSetAttribute(mass_tiles_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+        if (e == cudaSuccess) e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return e;
-        int per_sm = 0, dev = 0, sms = 0;
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, mass_tiles_kernel, kThreads, sizeof(Smem));
-        if (e != cudaSuccess) return e;
-        e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return e;
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess) return e;
-        if (per_sm > 2) per_sm = 2;             // tensor memory: 256 columns each
-        resident = per_sm * sms > 0 ? per_sm * sms : 1;
+        sms = n;
     }
     TileParams prm{};
     prm.plan = a.plan;
@@ -378,7 +373,7 @@ cudaError_t launch_mass_tiles(const MassArgs &a, cudaStream_t st) {
     prm.bf16 = bf16 ? 1 : 0;
     prm.scale_log2 = a.scale * kLog2e;
     prm.status = a.status;
-    cudaError_t e = launch_pdl(mass_tiles_kernel, dim3((unsigned)resident), dim3(kThreads), sizeof(Smem), st, tq, tk, prm);
+    cudaError_t e = launch_pdl(mass_tiles_kernel, dim3((unsigned)(sms * ctas_per_sm)), dim3(kThreads), sizeof(Smem), st, tq, tk, prm);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }

@@ -32,6 +32,7 @@ namespace pa {
 constexpr int32_t kFactsKnown = 1;
 constexpr int32_t kFactSharedPages = 2;     // some page is held by two used block-table entries
 constexpr int32_t kFactRepeatedItems = 4;   // some sequence has more than one decode item
+constexpr int32_t kFactItemsAndTiles = 8;   // some sequence has decode items and prefill tiles
 
 // Facts about the plan's host copy (kFact* flags); std::bad_alloc when the host
 // has no memory for them.
@@ -59,15 +60,23 @@ pa_status spans_disjoint(const Span *written, int n_written, const Span *read, i
 
 // Workspace of paged_attn_forward_mass: byte offsets of its parts.
 struct MassLayout {
-    size_t lse, lse_final, groups, scores, bytes;   // the split partials start at 0
-    int64_t cap;                                     // keys of one score row
+    size_t lse, lse_final, items, tiles, scores, bytes;   // the split partials start at 0
+    int64_t cap;                                           // keys of one score row
 };
 // max_keys: keys the score rows hold at least; 0: the longest history of the host copy.
 // window: the call's, 0 when it is not causal (a causal query sees at most `window` keys).
 MassLayout mass_layout(const pa_plan *plan, int32_t hq, int32_t dv, int32_t splits, int32_t window, int64_t max_keys);
-// The kernels that follow the attention of `a` and add its weights to key_mass.
-cudaError_t add_mass(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass,
-                     cudaStream_t st);
+// The kernels that follow the attention of `a` and add its weights to key_mass:
+// the decode items with stored scores (merging the split outputs in the same
+// launch when `merge`), and the tiles -- or, where the tiles have no tensor-core
+// kernel, every query -- with recomputed ones.  The tiles' work list
+// (mass_tile_lists) depends on the plan alone.
+cudaError_t add_item_mass(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass, bool merge,
+                          bool use_list, cudaStream_t st);
+cudaError_t mass_tile_lists(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass,
+                            cudaStream_t st);
+cudaError_t add_tile_mass(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass,
+                          int tile_ctas_per_sm, cudaStream_t st);
 // Attention entry body with totals; key_mass is not null.
 pa_status attention_with_mass(const pa_plan *plan, const void *q, const void *k, const void *v, void *out,
                               float *key_mass, int32_t hq, int32_t hkv, int32_t d, int32_t dv, float scale,

@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "merge.cuh"
 #include "pa_internal.h"
 
 namespace pa {
@@ -71,163 +72,24 @@ cudaError_t launch_kv_store(const PlanView &plan, const void *new_k, const void 
     return cudaGetLastError();
 }
 
-template <typename T> __device__ __forceinline__ T from_float(float x);
-template <> __device__ __forceinline__ float from_float<float>(float x) { return x; }
-template <> __device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
-template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-
-// One warp per (query, head) row, eight rows per 256-thread block.  Every
-// lane derives the split weights e^(lse_s - M) itself (M = max over splits,
-// empty splits weigh 0) and holds VEC consecutive value columns of each
-// 32*VEC-column chunk, read as one vector per split.
-template <typename T, int VEC> struct OutVec;
-template <typename T> struct OutVec<T, 1> {
-    static __device__ __forceinline__ void store(T *p, const float *v) { p[0] = from_float<T>(v[0]); }
-};
-template <typename T> struct OutVec<T, 2> {
-    static __device__ __forceinline__ void store(T *p, const float *v) {
-        p[0] = from_float<T>(v[0]);
-        p[1] = from_float<T>(v[1]);
-    }
-};
-template <> struct OutVec<float, 4> {
-    static __device__ __forceinline__ void store(float *p, const float *v) {
-        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    }
-};
-template <typename T> struct OutVec<T, 4> {
-    static __device__ __forceinline__ void store(T *p, const float *v) {
-        union { T h[4]; uint2 u; } x;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x.h[i] = from_float<T>(v[i]);
-        *reinterpret_cast<uint2 *>(p) = x.u;
-    }
-};
-
-template <int VEC> __device__ __forceinline__ void load_vec(const float *p, float *v) {
-    if constexpr (VEC == 4) {
-        const float4 x = *reinterpret_cast<const float4 *>(p);
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-    } else if constexpr (VEC == 2) {
-        const float2 x = *reinterpret_cast<const float2 *>(p);
-        v[0] = x.x; v[1] = x.y;
-    } else {
-        v[0] = p[0];
-    }
-}
-
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) merge_kernel(AttnArgs a, int use_list, int nrows) {
     griddep_wait();
     griddep_launch();
-    const int wid = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
-    const int lane = threadIdx.x & 31;
-    if (wid >= nrows) return;
-    const int item = wid / a.hq, h = wid - item * a.hq;
-    const int qi = use_list ? a.plan.decode[item] : item;
-    const int S = a.splits;
-    const int64_t rows = (int64_t)a.plan.queries * a.hq;
-    const int64_t row = (int64_t)qi * a.hq + h;
-    // lane l holds the weights of splits l and l + 32 (at most PA_MAX_SPLITS = 64)
-    float m = -INFINITY;
-    for (int s = lane; s < S; s += 32) m = fmaxf(m, a.ws_lse[s * rows + row]);
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float wl[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int s = lane + 32 * k;
-        const float l = s < S ? a.ws_lse[s * rows + row] : -INFINITY;
-        wl[k] = l == -INFINITY ? 0.f : __expf(l - m);
-    }
-    float tot = wl[0] + wl[1];
-    for (int o = 16; o; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-    const float inv = 1.f / tot;
-    T *out = static_cast<T *>(a.out) + row * a.dv;
-    // every lane runs every chunk (the weights are shuffled in the loop); a lane
-    // past the last column reads column 0 and stores nothing
-    for (int c0 = 0; c0 < a.dv; c0 += 32 * VEC) {
-        const bool live = c0 + lane * VEC < a.dv;
-        const int c = live ? c0 + lane * VEC : 0;
-        float acc[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
-        // no branch on empty splits (their weight is 0 and their partial 0), so the
-        // loads of several splits are in flight at once
-#pragma unroll 8
-        for (int s = 0; s < S; ++s) {
-            const float ws = __shfl_sync(0xffffffffu, s < 32 ? wl[0] : wl[1], s & 31);
-            float v[VEC];
-            load_vec<VEC>(a.ws_o + (s * rows + row) * a.dv + c, v);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) acc[i] += ws * v[i];
-        }
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[i] *= inv;
-        if (live) OutVec<T, VEC>::store(out + c, acc);
-    }
+    merge_rows<T, VEC>(a, use_list, nrows, blockIdx.x);
 }
 
-// Few rows or many splits: one 8-warp block per (query, head) row, warp w
-// taking splits w, w + 8, ...; the eight partial sums meet in shared memory.
-// Rows spread over every SM and all splits of a row are in flight at once,
-// where one warp per row would walk its splits one after another.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) merge_wide_kernel(AttnArgs a, int use_list) {
     griddep_wait();
     griddep_launch();
-    extern __shared__ float part[];   // [8][dv]
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int item = blockIdx.x / a.hq, h = blockIdx.x - item * a.hq;
-    const int qi = use_list ? a.plan.decode[item] : item;
-    const int S = a.splits;
-    const int64_t rows = (int64_t)a.plan.queries * a.hq;
-    const int64_t row = (int64_t)qi * a.hq + h;
-    float m = -INFINITY;
-    for (int s = lane; s < S; s += 32) m = fmaxf(m, a.ws_lse[s * rows + row]);
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float wl[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int s = lane + 32 * k;
-        const float l = s < S ? a.ws_lse[s * rows + row] : -INFINITY;
-        wl[k] = l == -INFINITY ? 0.f : __expf(l - m);
-    }
-    float tot = wl[0] + wl[1];
-    for (int o = 16; o; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-    for (int c0 = 0; c0 < a.dv; c0 += 32 * VEC) {
-        const bool live = c0 + lane * VEC < a.dv;
-        const int c = live ? c0 + lane * VEC : 0;
-        float acc[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
-#pragma unroll 4
-        for (int s = warp; s < S; s += 8) {
-            const float ws = __shfl_sync(0xffffffffu, s < 32 ? wl[0] : wl[1], s & 31);
-            float v[VEC];
-            load_vec<VEC>(a.ws_o + (s * rows + row) * a.dv + c, v);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) acc[i] += ws * v[i];
-        }
-        if (live) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) part[warp * a.dv + c + i] = acc[i];
-        }
-    }
-    __syncthreads();
-    const float inv = 1.f / tot;
-    T *out = static_cast<T *>(a.out) + row * a.dv;
-    for (int c = threadIdx.x; c < a.dv; c += 256) {
-        float x = 0.f;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) x += part[w * a.dv + c];
-        out[c] = from_float<T>(x * inv);
-    }
+    extern __shared__ float part[];
+    merge_row_wide<T, VEC>(a, use_list, blockIdx.x, part);
 }
 
 template <int VEC> cudaError_t launch_merge_vec(const AttnArgs &a, bool use_list, int nrows, cudaStream_t st) {
     const int ul = use_list ? 1 : 0;
-    if (nrows < 1024 || a.splits >= 16) {
-        // fewer rows than fill the GPU at 8 per block, or long split chains
+    if (merge_is_wide(a, nrows)) {
         const dim3 grid((unsigned)nrows), block(256);
         const size_t smem = (size_t)8 * a.dv * sizeof(float);
         switch (a.dtype) {
@@ -248,17 +110,10 @@ cudaError_t launch_merge(const AttnArgs &a, bool use_list, cudaStream_t st) {
     const int items = use_list ? a.plan.n_decode : a.plan.queries;
     if (items == 0) return cudaSuccess;
     const int nrows = items * a.hq;
-    // the workspace is 16-byte aligned and rows are dv floats apart; the output
-    // takes 4-wide stores only when its base allows them
-    const uintptr_t ob = reinterpret_cast<uintptr_t>(a.out);
-    const uintptr_t esz = a.dtype == PA_F32 ? 4 : 2;
-    cudaError_t e;
-    if (a.dv % 4 == 0 && ob % (4 * esz) == 0)
-        e = launch_merge_vec<4>(a, use_list, nrows, st);
-    else if (a.dv % 2 == 0)
-        e = launch_merge_vec<2>(a, use_list, nrows, st);
-    else
-        e = launch_merge_vec<1>(a, use_list, nrows, st);
+    const int vec = merge_vec(a);
+    cudaError_t e = vec == 4   ? launch_merge_vec<4>(a, use_list, nrows, st)
+                    : vec == 2 ? launch_merge_vec<2>(a, use_list, nrows, st)
+                               : launch_merge_vec<1>(a, use_list, nrows, st);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }

@@ -71,7 +71,7 @@ def test_mass_workspace_bytes(built_lib):
     p = plan([300, 40], [list(range(19)), [19, 20, 21] + [-1] * 16], [(0, 299), (1, 39)], pages=30)
     up = lambda n: -(-n // 256) * 256                                          # noqa: E731
     rows = 2 * 8
-    lists = up((2 * (2 + 1) + 2) * 4)
+    lists = up((2 + 1 + 2) * 4)
     assert pka.mass_workspace_bytes(p, 8, 2, 128, 1) == up(rows * 4) + lists + up(rows * 320 * 4)
     assert pka.mass_workspace_bytes(p, 8, 2, 128, 3) == up(3 * rows * 128 * 4) + up(3 * rows * 4) + lists + up(rows * 320 * 4)
     assert pka.mass_workspace_bytes(p, 8, 2, 128, 1, window=50) == up(rows * 4) + lists + up(rows * 64 * 4)

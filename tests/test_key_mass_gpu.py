@@ -110,6 +110,64 @@ def test_prompt_chunks(cuda_device, hq, hkv, d, ps, dt, splits, window):
     verify(case, splits, True, window)
 
 
+def test_mixed_step_beside_and_in_turn(cuda_device):
+    """A step large enough to run its decode items on the thread's second stream, and the same step captured on a
+    thread that has none: the same bits, weights that add to one per query and head, and float64 sums for a sequence
+    of each kind.  Also with a sequence that has a chunk and an early query (its totals then wait for each other)."""
+    import threading
+    from workloads import mixed_prefill_decode_bf16
+    base = mixed_prefill_decode_bf16(n_prefill=8, chunk=512, off_hi=4096, n_decode=120)
+    for extra in ([], [(0, 0)]):
+        if extra and base.meta["prefill_offsets"][0] == 0:
+            continue
+        case = mixed_prefill_decode_bf16(n_prefill=8, chunk=512, off_hi=4096, n_decode=120)
+        if extra:
+            case.query_seq = np.append(case.query_seq, np.int32(0))
+            case.query_pos = np.append(case.query_pos, np.int32(0))
+            case.q = torch.cat([case.q, case.q[:1]])
+            case.new_k, case.new_v = torch.cat([case.new_k, case.new_k[:1]]), torch.cat([case.new_v, case.new_v[:1]])
+        dc, plan = case.to("cuda"), plan_for(case)
+        pka.paged_kv_store(plan, dc.new_k, dc.new_v, dc.k_cache, dc.v_cache)
+        assert pka.paged_attn_decode_sms_beside_prefill(plan, case.hq, case.hkv, 128, 128) > 0
+        mass = torch.zeros(case.num_pages, case.hkv, 16, device="cuda")
+        ws = pka.make_mass_workspace(plan, case.hq, case.hkv, 128, 1)
+        call = lambda m: pka.paged_attn_forward_mass(plan, dc.q, dc.k_cache, dc.v_cache, m, case.scale, splits=1,   # noqa: E731
+                                                     workspace=ws)
+        out = call(mass)
+        torch.cuda.synchronize()
+        assert pka.device_status() == 0
+        serial, box = torch.zeros_like(mass), {}
+
+        def captured():
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                box["out"] = call(serial)
+            g.replay()
+            torch.cuda.synchronize()
+            box["graph"] = g
+        t = threading.Thread(target=captured)
+        t.start()
+        t.join()
+        assert pka.device_status() == 0
+        assert torch.equal(out, box["out"]) and torch.equal(mass, serial)
+        got = mass.double().cpu().numpy()
+        k = dc.k_cache.double()
+        for s, n in enumerate(case.seq_lens):
+            used = np.asarray(case.block_table)[s][: -(-int(n) // 16)]
+            mine = np.nonzero(np.asarray(case.query_seq) == s)[0]
+            assert np.allclose(got[used].sum((0, 2)), 4.0 * len(mine), rtol=1e-4)
+            if s not in (0, 3, 8, 127):
+                continue
+            keys = k[torch.as_tensor(used).cuda().long()].reshape(-1, 8, 128)[:n]
+            q = dc.q[torch.as_tensor(mine).cuda()].double().view(len(mine), 8, 4, 128)
+            logit = torch.einsum("qhgd,nhd->hgqn", q, keys) * case.scale
+            pos = torch.as_tensor(np.asarray(case.query_pos)[mine]).cuda()[:, None]
+            logit.masked_fill_(torch.arange(int(n), device="cuda") > pos, -np.inf)
+            want = logit.softmax(-1).sum((1, 2)).cpu().numpy()            # [Hkv, n]
+            have = got[used].transpose(1, 0, 2).reshape(8, -1)[:, :n]
+            assert np.max(np.abs(have - want) / want) < weight_tolerance(case, torch.nan_to_num(dc.k_cache.cpu())) + len(mine) * 2.0 ** -23
+
+
 @pytest.mark.parametrize("window", [0, 40])
 def test_prompt_chunks_not_causal(cuda_device, window):
     queries = [(0, 100 + i) for i in range(60)] + [(1, 40)]
