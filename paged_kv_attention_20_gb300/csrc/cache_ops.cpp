@@ -108,11 +108,11 @@ cudaError_t mass_tile_lists(const pa_plan *plan, const AttnArgs &a, const MassLa
 }
 
 cudaError_t add_tile_mass(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass,
-                          int tile_ctas_per_sm, cudaStream_t st) {
+                          cudaStream_t st) {
     const MassArgs m = tile_args(plan, a, lay, ws, key_mass);
     cudaError_t e = cudaSuccess;
     if (a.splits > 1) e = launch_lse_final(m, reinterpret_cast<float *>(ws + lay.lse_final), st);
-    if (e == cudaSuccess) e = prefill_supported(a) ? launch_mass_tiles(m, tile_ctas_per_sm, st) : launch_mass_recompute(m, st);
+    if (e == cudaSuccess) e = prefill_supported(a) ? launch_mass_tiles(m, st) : launch_mass_recompute(m, st);
     return e;
 }
 
@@ -142,6 +142,7 @@ pa_status paged_attn_forward_mass(const pa_plan *plan, const void *q, const void
     if (!key_mass) return fail(PA_ERR_ARG, "paged_attn_forward_mass: key_mass is null");
     if (reinterpret_cast<uintptr_t>(key_mass) % sizeof(float))
         return fail(PA_ERR_ARG, "paged_attn_forward_mass: key_mass not 4-byte aligned");
+    if (plan->max_seq_len > (1 << 30)) return fail(PA_ERR_LIMIT, "paged_attn_forward_mass: history above 2^30 keys");
     try {
         if (pa::plan_facts(plan) & pa::kFactSharedPages)
             return fail(PA_ERR_WRITE_CONFLICT, "paged_attn_forward_mass: two sequences hold one page, its totals would have two owners");

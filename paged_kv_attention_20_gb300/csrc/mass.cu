@@ -197,61 +197,71 @@ __device__ __forceinline__ void add_items(const MassArgs &a, int repeated, int b
     for (int e = first; e < last; ++e) {
         const int item = repeated ? a.group_list[e] : e;
         const int qi = a.plan.decode[item];
+        // what hangs on the query alone is asked for at once: its metadata and the
+        // first of this warp's log-sum-exps (over the splits, two a lane)
+        const int64_t row0 = (int64_t)qi * a.hq + kvh * G;
+        const bool mine = warp < G;
+        float l0 = mine && lane < a.splits ? a.lse[lane * rows + row0 + warp] : -INFINITY;
+        float l1 = mine && lane + 32 < a.splits ? a.lse[(lane + 32) * rows + row0 + warp] : -INFINITY;
         const int4 meta = a.plan.qmeta[qi];
         int64_t lo64, hi64;
-        visible_range(meta.y, a.plan.seq_lens[meta.x], a.causal, a.window, lo64, hi64);
+        visible_range(meta.y, a.causal ? 0 : a.plan.seq_lens[meta.x], a.causal, a.window, lo64, hi64);
         const int lo = (int)lo64, hi = (int)hi64;       // positions fit 32 bits
-        if (hi - lo > a.cap) {
-            // the workspace holds no scores past cap: this item adds nothing
+        if (hi - lo > a.cap || hi > (1 << 30)) {
+            // the workspace holds no scores past cap: this item adds nothing (nor does
+            // one whose steps could leave 32 bits)
             if (threadIdx.x == 0) atomicCAS(a.status, 0, PA_DEVICE_RANGE);
             continue;
         }
-        const int64_t step = (int64_t)blocks * kItemKeys;
-        const int64_t start = lo / step * step + (int64_t)blk * kItemKeys;
+        const int step = blocks * kItemKeys;             // at most about the longest history
+        const int start = lo / step * step + blk * kItemKeys;
         if (start >= hi || (start + kItemKeys <= lo && start + step >= hi)) continue;   // nothing here (uniform)
         const int32_t *trow = a.plan.table + (int64_t)meta.x * a.plan.width;
+        const bool aligned = (lo & 3) == 0;
         for (int g0 = 0; g0 < G; g0 += kMaxStagedHeads) {
             const int gn = min(G - g0, kMaxStagedHeads);
             const float *head0 = a.scores + ((int64_t)item * a.hq + kvh * G + g0) * a.cap - lo;
             float4 early[kHeadsAtOnce];
-            auto whole = [&](int64_t j) { return j >= lo && j + 4 <= hi && (lo & 3) == 0; };
-            auto ask = [&](int64_t j) {                 // the first heads' scores of four keys
+            int page = 0;
+            auto ask = [&](int j) {                     // the page and the first heads' scores of four keys
+                if (j >= lo && j + 4 <= hi) {
+                    if (kQuads) page = trow[ps_shift >= 0 ? j >> ps_shift : j / ps];
 #pragma unroll
-                for (int g = 0; g < kHeadsAtOnce; ++g)
-                    if (whole(j) && g < gn) early[g] = *reinterpret_cast<const float4 *>(head0 + j + g * a.cap);
+                    for (int g = 0; g < kHeadsAtOnce; ++g)
+                        if (aligned && g < gn) early[g] = *reinterpret_cast<const float4 *>(head0 + j + g * a.cap);
+                }
             };
-            const int64_t j0 = start + 4 * (int)threadIdx.x;
-            ask(j0);
+            int j = start + 4 * (int)threadIdx.x;
+            ask(j);
             __syncthreads();
-            // a head per warp: its log-sum-exp over the splits (two a lane, at most 64), log2 units
             for (int g = warp; g < gn; g += kItemWarps) {
-                const int64_t row = (int64_t)qi * a.hq + kvh * G + g0 + g;
-                const float l0 = lane < a.splits ? a.lse[lane * rows + row] * kLog2e : -INFINITY;
-                const float l1 = lane + 32 < a.splits ? a.lse[(lane + 32) * rows + row] * kLog2e : -INFINITY;
+                if (g0 + g != warp) {
+                    l0 = lane < a.splits ? a.lse[lane * rows + row0 + g0 + g] : -INFINITY;
+                    l1 = lane + 32 < a.splits ? a.lse[(lane + 32) * rows + row0 + g0 + g] : -INFINITY;
+                }
                 float m = fmaxf(l0, l1);
                 for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                float t = (l0 == -INFINITY ? 0.f : exp2f(l0 - m)) + (l1 == -INFINITY ? 0.f : exp2f(l1 - m));
+                float t = (l0 == -INFINITY ? 0.f : exp2f((l0 - m) * kLog2e)) + (l1 == -INFINITY ? 0.f : exp2f((l1 - m) * kLog2e));
                 for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-                if (lane == 0) lse[g] = a.splits == 1 ? l0 : m + log2f(t);
+                if (lane == 0) lse[g] = a.splits == 1 ? l0 * kLog2e : m * kLog2e + log2f(t);
             }
             __syncthreads();
-            for (int64_t j64 = j0; j64 < hi; j64 += step) {
-                if (j64 + 4 <= lo) {
-                    ask(j64 + step);
+            for (; j < hi; j += step) {
+                if (j + 4 <= lo) {
+                    ask(j + step);
                     continue;
                 }
-                const int j = (int)j64;
                 const float *sc = head0 + j;
                 const bool all = j >= lo && j + 4 <= hi;
                 float4 *m = nullptr;
                 float4 old;
                 if (kQuads && all) {
-                    const int pg = ps_shift >= 0 ? j >> ps_shift : j / ps;
-                    m = reinterpret_cast<float4 *>(a.key_mass + ((int64_t)trow[pg] * a.hkv + kvh) * ps + (j - pg * ps));
+                    m = reinterpret_cast<float4 *>(a.key_mass + ((int64_t)page * a.hkv + kvh) * ps +
+                                                   (ps_shift >= 0 ? j & (ps - 1) : j % ps));
                     old = *m;
                 }
                 float p[4] = {0.f, 0.f, 0.f, 0.f};
-                if (whole(j)) {
+                if (all && aligned) {
 #pragma unroll
                     for (int g = 0; g < kHeadsAtOnce; ++g)
                         if (g < gn) {
@@ -259,7 +269,7 @@ __device__ __forceinline__ void add_items(const MassArgs &a, int repeated, int b
                             const float l = lse[g];
                             p[0] += exp2f(v.x - l); p[1] += exp2f(v.y - l); p[2] += exp2f(v.z - l); p[3] += exp2f(v.w - l);
                         }
-                    ask(j64 + step);
+                    ask(j + step);
 #pragma unroll 4
                     for (int g = kHeadsAtOnce; g < gn; ++g) {
                         const float4 v = *reinterpret_cast<const float4 *>(sc + g * a.cap);
@@ -267,7 +277,7 @@ __device__ __forceinline__ void add_items(const MassArgs &a, int repeated, int b
                         p[0] += exp2f(v.x - l); p[1] += exp2f(v.y - l); p[2] += exp2f(v.z - l); p[3] += exp2f(v.w - l);
                     }
                 } else {
-                    ask(j64 + step);
+                    ask(j + step);
                     for (int g = 0; g < gn; ++g)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
@@ -290,7 +300,7 @@ __device__ __forceinline__ void add_items(const MassArgs &a, int repeated, int b
 }
 
 template <bool kQuads>
-__global__ void __launch_bounds__(kItemThreads) mass_items_kernel(MassArgs a, int repeated, int blocks, int ps_shift) {
+__global__ void __launch_bounds__(kItemThreads, 4) mass_items_kernel(MassArgs a, int repeated, int blocks, int ps_shift) {
     griddep_wait();
     griddep_launch();
     __shared__ float lse[kMaxStagedHeads];
@@ -300,7 +310,7 @@ __global__ void __launch_bounds__(kItemThreads) mass_items_kernel(MassArgs a, in
 // The merge of the split outputs and the totals in one launch: both follow the
 // decode kernel and neither needs the other.  The first merge_blocks CTAs merge.
 template <typename T, int VEC, bool kQuads>
-__global__ void __launch_bounds__(kItemThreads) merge_and_items_kernel(AttnArgs attn, MassArgs a, int use_list, int nrows,
+__global__ void __launch_bounds__(kItemThreads, 4) merge_and_items_kernel(AttnArgs attn, MassArgs a, int use_list, int nrows,
                                                                        int wide, int merge_blocks, int repeated, int blocks,
                                                                        int ps_shift) {
     griddep_wait();
@@ -418,9 +428,9 @@ cudaError_t launch_lse_final(const MassArgs &a, float *out, cudaStream_t st) {
 
 cudaError_t launch_mass_items(const MassArgs &a, bool repeated, const AttnArgs *merge, bool use_list, cudaStream_t st) {
     const int64_t units = (int64_t)(repeated ? a.plan.sequences : a.plan.n_decode) * a.hkv;
-    // blocks a unit: one per 1024 keys of the longest history, but no more CTAs than
-    // about twice what the GPU holds (each strides over its keys)
-    const int64_t most = ((int64_t)a.longest + kItemKeys - 1) / kItemKeys, fill = (2 * 152 * 8 + units - 1) / units;
+    // blocks a unit: one per 1024 keys of the longest history, but no more than fill
+    // the GPU once (a CTA's start costs three dependent loads, its further keys one)
+    const int64_t most = ((int64_t)a.longest + kItemKeys - 1) / kItemKeys, fill = (152 * 4 + units - 1) / units;
     const int blocks = blocks_for(units, most < fill ? most : fill);
     const int ps = a.plan.page_size;
     int shift = -1;

@@ -54,7 +54,7 @@ struct Step {
 struct Smem {
     uint8_t k[kTile];
     uint8_t q[kStages][kTile];
-    float lse[kSlots][kQ];                    // log2 units
+    float lse[kSlots][kQ];                    // negated, log2 units
     Step step[kSlots];
     uint64_t k_full, k_empty;
     uint64_t q_full[kStages], q_empty[kStages];
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                     for (int i = 0; i < kQ / 32; ++i) {
                         const int c = lane + 32 * i;
-                        l[i] = c < st.nq ? prm.lse[(int64_t)(tile.y + c) * prm.hq + h] * kLog2e : 0.f;
+                        l[i] = c < st.nq ? prm.lse[(int64_t)(tile.y + c) * prm.hq + h] * -kLog2e : 0.f;
                     }
                     if (!open) {
                         if (u_open > 0 && !wait(&s.k_empty, (uint32_t)((u_open - 1) & 1))) { go = false; break; }
@@ -288,36 +288,43 @@ __global__ void __launch_bounds__(kThreads, 2)
             int n0 = prm.causal ? j - st.pos0 : 0, n1 = st.nq - 1;
             if (prm.window > 0) n1 = (int)min((int64_t)n1, (int64_t)j - st.pos0 + prm.window - 1);
             const bool edge = n0 > 0 || n1 < kQ - 1;
+            const uint32_t sb = tmem + lane_off + (uint32_t)(b * kQ);
             const float4 *ls = reinterpret_cast<const float4 *>(s.lse[sl]);
-            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            if (!__any_sync(0xffffffffu, edge)) {
+            float2 acc[4];
 #pragma unroll
-                for (int c = 0; c < kQ; c += 32) {
-                    float v[32];
-                    tmem_ld32f(tmem + lane_off + (uint32_t)(b * kQ + c), v);
-                    tmem_wait_ld();
+            for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.f, 0.f);
+            if (!__any_sync(0xffffffffu, edge)) {
+                // 32 columns at a time, the next ones on their way
+                float v[2][32];
+                tmem_ld32f(sb, v[0]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < kQ / 32; ++c) {
+                    if (c + 1 < kQ / 32) tmem_ld32f(sb + (uint32_t)(32 * (c + 1)), v[(c + 1) & 1]);
+                    const float *x = v[c & 1];
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
-                        const float4 l = ls[(c + i) / 4];
-                        const float2 x = ffma2(make_float2(v[i], v[i + 1]), sc2, make_float2(-l.x, -l.y));
-                        const float2 y = ffma2(make_float2(v[i + 2], v[i + 3]), sc2, make_float2(-l.z, -l.w));
-                        acc[0] = fadd2(acc[0], make_float2(ex2(x.x), ex2(x.y)));
-                        acc[1] = fadd2(acc[1], make_float2(ex2(y.x), ex2(y.y)));
+                        const float4 l = ls[8 * c + i / 4];
+                        const float2 p = ffma2(make_float2(x[i], x[i + 1]), sc2, make_float2(l.x, l.y));
+                        const float2 q = ffma2(make_float2(x[i + 2], x[i + 3]), sc2, make_float2(l.z, l.w));
+                        acc[(i / 4 * 2) & 3] = fadd2(acc[(i / 4 * 2) & 3], make_float2(ex2(p.x), ex2(p.y)));
+                        acc[(i / 4 * 2 + 1) & 3] = fadd2(acc[(i / 4 * 2 + 1) & 3], make_float2(ex2(q.x), ex2(q.y)));
                     }
+                    if (c + 1 < kQ / 32) tmem_wait_ld();
                 }
             } else {
 #pragma unroll
                 for (int c = 0; c < kQ; c += 32) {
                     float v[32];
-                    tmem_ld32f(tmem + lane_off + (uint32_t)(b * kQ + c), v);
+                    tmem_ld32f(sb + (uint32_t)c, v);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
                         const float2 x = ffma2(make_float2(v[i], v[i + 1]), sc2,
-                                               make_float2(-s.lse[sl][c + i], -s.lse[sl][c + i + 1]));
+                                               make_float2(s.lse[sl][c + i], s.lse[sl][c + i + 1]));
                         // columns outside the interval hold other queries' scores, NaN included
-                        acc[0] = fadd2(acc[0], make_float2(c + i >= n0 && c + i <= n1 ? ex2(x.x) : 0.f,
-                                                           c + i + 1 >= n0 && c + i + 1 <= n1 ? ex2(x.y) : 0.f));
+                        acc[i & 2] = fadd2(acc[i & 2], make_float2(c + i >= n0 && c + i <= n1 ? ex2(x.x) : 0.f,
+                                                                   c + i + 1 >= n0 && c + i + 1 <= n1 ? ex2(x.y) : 0.f));
                     }
                 }
             }
@@ -325,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             mbar_arrive(&s.s_empty[b]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.d_empty[sl]);
-            const float2 sum = fadd2(acc[0], acc[1]);
+            const float2 sum = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
             total += sum.x + sum.y;
         }
         if (!ok && lane == 0) atomicCAS(prm.status, 0, PA_DEVICE_TIMEOUT_SOFTMAX);
@@ -346,7 +353,7 @@ bool make_map(CUtensorMap *m, const void *base, int heads, int64_t rows, int box
 
 }  // namespace
 
-cudaError_t launch_mass_tiles(const MassArgs &a, int ctas_per_sm, cudaStream_t st) {
+cudaError_t launch_mass_tiles(const MassArgs &a, cudaStream_t st) {
     const bool bf16 = a.dtype == PA_BF16;
     CUtensorMap tq, tk;
     if (!make_map(&tq, a.q, a.hq, a.plan.queries, kQ, bf16) ||
@@ -373,7 +380,7 @@ cudaError_t launch_mass_tiles(const MassArgs &a, int ctas_per_sm, cudaStream_t s
     prm.bf16 = bf16 ? 1 : 0;
     prm.scale_log2 = a.scale * kLog2e;
     prm.status = a.status;
-    cudaError_t e = launch_pdl(mass_tiles_kernel, dim3((unsigned)(sms * ctas_per_sm)), dim3(kThreads), sizeof(Smem), st, tq, tk, prm);
+    cudaError_t e = launch_pdl(mass_tiles_kernel, dim3((unsigned)(2 * sms)), dim3(kThreads), sizeof(Smem), st, tq, tk, prm);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }

@@ -166,7 +166,7 @@ cudaError_t launch_lse_final(const MassArgs &a, float *out, cudaStream_t st);
 // merge (not null): the same launch merges the split outputs of these attention arguments.
 cudaError_t launch_mass_items(const MassArgs &a, bool repeated, const AttnArgs *merge, bool use_list, cudaStream_t st);
 // Grouped tiles, scores recomputed on the tensor cores (prefill_supported shapes).
-cudaError_t launch_mass_tiles(const MassArgs &a, int ctas_per_sm, cudaStream_t st);
+cudaError_t launch_mass_tiles(const MassArgs &a, cudaStream_t st);
 // Grouped queries of any shape, scores recomputed.
 cudaError_t launch_mass_recompute(const MassArgs &a, cudaStream_t st);
 

@@ -190,14 +190,12 @@ int32_t plan_facts(const pa_plan *plan) {
             word |= bit;
         }
     }
-    std::vector<uint8_t> seen((size_t)plan->sequences, 0);      // 1: has an item, 2: has a tile
+    std::vector<uint8_t> seen((size_t)plan->sequences, 0);
     for (int32_t i = 0; i < plan->n_decode; ++i) {
         uint8_t &s = seen[(size_t)w[plan->off_qmeta + 4 * (size_t)w[plan->off_decode + i]]];
         if (s) facts |= kFactRepeatedItems;
         s = 1;
     }
-    for (int32_t t = 0; t < plan->n_tiles; ++t)
-        if (seen[(size_t)w[plan->off_tiles + 4 * (size_t)t]] & 1) facts |= kFactItemsAndTiles;
     plan->facts.store(facts, std::memory_order_release);
     return facts;
 }
@@ -689,28 +687,7 @@ pa_status attention(const pa_plan *plan, const void *q, const void *k, const voi
             const int beside =
                 sms > 0 ? decode_sms_beside_prefill(plan, hq, hkv, d, dv, causal, window, dtype, sms) : 0;
             SideStream *side = beside > 0 ? side_stream(st) : nullptr;
-            if (side && mass) {
-                // With totals to add, the tiles' pass over their keys (tensor cores,
-                // exponentials) makes the better company for the decode items (HBM):
-                // the prefill takes every SM first, then one CTA of the tiles' pass
-                // per SM, launched before the prefill's end lets the decode start,
-                // leaves shared memory for the decode's CTAs.
-                const bool apart = !(pa::plan_facts(plan) & pa::kFactItemsAndTiles);
-                e = pa::mass_tile_lists(plan, a, lay, static_cast<char *>(ws), key_mass, st);
-                mark(t0);
-                if (e == cudaSuccess) e = pa::launch_prefill(a, st);
-                mark(t1);
-                if (e == cudaSuccess) e = cudaEventRecord(side->fork, st);
-                if (e == cudaSuccess) e = pa::add_tile_mass(plan, a, lay, static_cast<char *>(ws), key_mass, 1, st);
-                if (e == cudaSuccess) e = cudaStreamWaitEvent(side->stream, side->fork, 0);
-                if (e == cudaSuccess) e = pa::launch_decode(a, true, side->stream);
-                if (e == cudaSuccess && apart)
-                    e = pa::add_item_mass(plan, a, lay, static_cast<char *>(ws), key_mass, false, true, side->stream);
-                if (e == cudaSuccess) e = cudaEventRecord(side->join, side->stream);
-                if (e == cudaSuccess) e = cudaStreamWaitEvent(st, side->join, 0);
-                if (e == cudaSuccess && !apart)
-                    e = pa::add_item_mass(plan, a, lay, static_cast<char *>(ws), key_mass, false, true, st);
-            } else if (side) {
+            if (side) {
                 // prefill on sms - beside persistent CTAs, launched first so that they
                 // hold their SMs; the decode items fill the rest from the side stream
                 e = cudaEventRecord(side->fork, st);
@@ -729,15 +706,14 @@ pa_status attention(const pa_plan *plan, const void *q, const void *k, const voi
                 mark(t0);
                 e = pa::launch_prefill(a, st);
                 mark(t1);
-                if (mass) {
-                    if (e == cudaSuccess) e = pa::mass_tile_lists(plan, a, lay, static_cast<char *>(ws), key_mass, st);
-                    if (e == cudaSuccess) e = pa::add_tile_mass(plan, a, lay, static_cast<char *>(ws), key_mass, 2, st);
-                }
-                if (e == cudaSuccess && plan->n_decode > 0) {
-                    e = pa::launch_decode(a, true, st);
-                    if (e == cudaSuccess && mass)
-                        e = pa::add_item_mass(plan, a, lay, static_cast<char *>(ws), key_mass, false, true, st);
-                }
+                if (e == cudaSuccess && plan->n_decode > 0) e = pa::launch_decode(a, true, st);
+            }
+            if (mass) {
+                char *base = static_cast<char *>(ws);
+                if (e == cudaSuccess && plan->n_decode > 0)
+                    e = pa::add_item_mass(plan, a, lay, base, key_mass, false, true, st);
+                if (e == cudaSuccess) e = pa::mass_tile_lists(plan, a, lay, base, key_mass, st);
+                if (e == cudaSuccess) e = pa::add_tile_mass(plan, a, lay, base, key_mass, st);
             }
             if (e == cudaSuccess && splits > 1) e = pa::launch_merge(a, false, st);
         } else {
@@ -753,7 +729,7 @@ pa_status attention(const pa_plan *plan, const void *q, const void *k, const voi
                 if (e == cudaSuccess && splits > 1) e = pa::launch_merge(a, all_decode, st);
                 if (mass) {
                     if (e == cudaSuccess) e = pa::mass_tile_lists(plan, a, lay, static_cast<char *>(ws), key_mass, st);
-                    if (e == cudaSuccess) e = pa::add_tile_mass(plan, a, lay, static_cast<char *>(ws), key_mass, 2, st);
+                    if (e == cudaSuccess) e = pa::add_tile_mass(plan, a, lay, static_cast<char *>(ws), key_mass, st);
                 }
             }
         }

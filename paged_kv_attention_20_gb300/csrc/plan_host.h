@@ -32,7 +32,6 @@ namespace pa {
 constexpr int32_t kFactsKnown = 1;
 constexpr int32_t kFactSharedPages = 2;     // some page is held by two used block-table entries
 constexpr int32_t kFactRepeatedItems = 4;   // some sequence has more than one decode item
-constexpr int32_t kFactItemsAndTiles = 8;   // some sequence has decode items and prefill tiles
 
 // Facts about the plan's host copy (kFact* flags); std::bad_alloc when the host
 // has no memory for them.
@@ -76,7 +75,7 @@ cudaError_t add_item_mass(const pa_plan *plan, const AttnArgs &a, const MassLayo
 cudaError_t mass_tile_lists(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass,
                             cudaStream_t st);
 cudaError_t add_tile_mass(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass,
-                          int tile_ctas_per_sm, cudaStream_t st);
+                          cudaStream_t st);
 // Attention entry body with totals; key_mass is not null.
 pa_status attention_with_mass(const pa_plan *plan, const void *q, const void *k, const void *v, void *out,
                               float *key_mass, int32_t hq, int32_t hkv, int32_t d, int32_t dv, float scale,
