@@ -135,8 +135,18 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (lane == 0) mbar_arrive(&s.d_full[d % kSlots]);
             ++d;
         };
-        for (int u = blockIdx.x; go && u < units; u += gridDim.x) {
-            const int blk = u / prm.hkv, kvh = u - blk * prm.hkv;
+        // The walk over the steps runs one ahead of the loads, so that a step's
+        // metadata and log-sum-exps have a step's time to arrive (in turn, their
+        // latency made this warp the slowest role, ~2400 cycles a step).
+        struct Walk {
+            int u, e, e1, g;          // unit, entry of the tile list and its end, head of the group
+            int q0;                   // first query of the tile
+            int4 tile;                // the entry's tile
+            Step st;
+            bool live;
+        };
+        auto open_unit = [&](Walk &w) {                  // tile list and key block of unit w.u
+            const int blk = w.u / prm.hkv;
             // the sequence whose blocks hold blk: last one that starts at or before it
             int seq = 0;
             for (int n = S; n > 1;) {
@@ -146,66 +156,103 @@ __global__ void __launch_bounds__(kThreads, 2)
                 seq += k * step;
                 n = min(step, n - k * step);
             }
-            Step st{};
-            st.kvh = kvh;
-            st.key0 = (blk - prm.unit_start[seq]) * kKeys;
-            st.seq_len = prm.plan.seq_lens[seq];
-            const int32_t *trow = prm.plan.table + (int64_t)seq * prm.plan.width;
-            st.trow_lo = (int32_t)(uint32_t)reinterpret_cast<uint64_t>(trow);
-            st.trow_hi = (int32_t)(uint32_t)(reinterpret_cast<uint64_t>(trow) >> 32);
-            const int used_pages = (st.seq_len + ps - 1) / ps;
-            const int e1 = prm.group_start[seq + 1];
-            bool open = false;
-            for (int e = prm.group_start[seq]; go && e < e1; ++e) {
-                const int4 tile = prm.plan.tiles[prm.group_list[e]];
-                st.pos0 = tile.w;
-                st.nq = tile.z;
-                const int hi = prm.causal ? st.pos0 + st.nq : st.seq_len;
-                const int64_t lo = prm.window > 0 ? (int64_t)st.pos0 - prm.window + 1 : 0;
-                if (st.key0 >= hi || (int64_t)st.key0 + kKeys <= lo) continue;
-                for (int g = 0; go && g < G; ++g) {
-                    const int h = kvh * G + g;
-                    // log-sum-exps of the step's columns: loads first, they land during the waits
-                    float l[kQ / 32];
+            w.st.kvh = w.u - blk * prm.hkv;
+            w.st.key0 = (blk - prm.unit_start[seq]) * kKeys;
+            w.st.seq_len = prm.plan.seq_lens[seq];
+            const uint64_t trow = reinterpret_cast<uint64_t>(prm.plan.table + (int64_t)seq * prm.plan.width);
+            w.st.trow_lo = (int32_t)(uint32_t)trow;
+            w.st.trow_hi = (int32_t)(uint32_t)(trow >> 32);
+            w.e = prm.group_start[seq];
+            w.e1 = prm.group_start[seq + 1];
+            w.tile = prm.plan.tiles[prm.group_list[w.e]];   // a unit's sequence has tiles
+            w.st.first = 1;
+        };
+        // to the first tile from w.e on that sees the unit's keys; past the unit's
+        // tiles, to the next unit
+        auto settle = [&](Walk &w) {
+            while (true) {
+                while (w.e < w.e1) {
+                    const int hi = prm.causal ? w.tile.w + w.tile.z : w.st.seq_len;
+                    const int64_t lo = prm.window > 0 ? (int64_t)w.tile.w - prm.window + 1 : 0;
+                    if (w.st.key0 < hi && (int64_t)w.st.key0 + kKeys > lo) {
+                        w.q0 = w.tile.y;
+                        w.st.nq = w.tile.z;
+                        w.st.pos0 = w.tile.w;
+                        w.g = 0;
+                        ++w.e;
+                        if (w.e < w.e1) w.tile = prm.plan.tiles[prm.group_list[w.e]];
+                        return;
+                    }
+                    ++w.e;
+                    if (w.e < w.e1) w.tile = prm.plan.tiles[prm.group_list[w.e]];
+                }
+                w.u += (int)gridDim.x;
+                if (w.u >= units) {
+                    w.live = false;
+                    return;
+                }
+                open_unit(w);
+            }
+        };
+        auto ask = [&](const Walk &w, float (&l)[kQ / 32]) {   // log-sum-exps of the step's columns
 #pragma unroll
-                    for (int i = 0; i < kQ / 32; ++i) {
-                        const int c = lane + 32 * i;
-                        l[i] = c < st.nq ? prm.lse[(int64_t)(tile.y + c) * prm.hq + h] * -kLog2e : 0.f;
-                    }
-                    if (!open) {
-                        if (u_open > 0 && !wait(&s.k_empty, (uint32_t)((u_open - 1) & 1))) { go = false; break; }
-                        ++u_open;
-                        if (lane == 0) mbar_arrive_expect_tx(&s.k_full, kTile);
-                        __syncwarp();
-                        if (lane < boxes) {
-                            const int lp = st.key0 / ps + lane;
-                            const int row = lp < used_pages ? trow[lp] * ps : oob_row;
-                            tma_load_3d(s.k + lane * ps * 128, &tm_k, 0, kvh, row, &s.k_full);
-                            tma_load_3d(s.k + kHalf + lane * ps * 128, &tm_k, 64, kvh, row, &s.k_full);
-                        }
-                    }
-                    const int b = t % kStages;
-                    if (t >= kStages && !wait(&s.q_empty[b], (uint32_t)((t / kStages - 1) & 1))) { go = false; break; }
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&s.q_full[b], kTile);
-                        tma_load_3d(s.q[b], &tm_q, 0, h, tile.y, &s.q_full[b]);
-                        tma_load_3d(s.q[b] + kHalf, &tm_q, 64, h, tile.y, &s.q_full[b]);
-                    }
-                    ++t;
-                    if (!open_slot()) { go = false; break; }
-#pragma unroll
-                    for (int i = 0; i < kQ / 32; ++i) s.lse[d % kSlots][lane + 32 * i] = l[i];
-                    st.kind = kWork;
-                    st.first = open ? 0 : 1;
-                    open = true;
-                    publish(st);
+            for (int i = 0; i < kQ / 32; ++i) {
+                const int c = lane + 32 * i;
+                l[i] = w.live && c < w.st.nq ? prm.lse[(int64_t)(w.q0 + c) * prm.hq + w.st.kvh * G + w.g] : 0.f;
+            }
+        };
+        Walk cur{};
+        cur.u = (int)blockIdx.x;
+        cur.live = cur.u < units;
+        if (cur.live) {
+            open_unit(cur);
+            settle(cur);
+        }
+        float l[kQ / 32];
+        ask(cur, l);
+        while (go && cur.live) {
+            Walk next = cur;
+            next.st.first = 0;
+            if (++next.g == G) settle(next);
+            float nl[kQ / 32];
+            ask(next, nl);
+            Step &st = cur.st;
+            if (st.first) {
+                if (u_open > 0 && !wait(&s.k_empty, (uint32_t)((u_open - 1) & 1))) { go = false; break; }
+                ++u_open;
+                if (lane == 0) mbar_arrive_expect_tx(&s.k_full, kTile);
+                __syncwarp();
+                if (lane < boxes) {
+                    const int32_t *trow = reinterpret_cast<const int32_t *>((uint64_t)(uint32_t)st.trow_lo |
+                                                                            ((uint64_t)(uint32_t)st.trow_hi << 32));
+                    const int lp = st.key0 / ps + lane, used_pages = (st.seq_len + ps - 1) / ps;
+                    const int row = lp < used_pages ? trow[lp] * ps : oob_row;
+                    tma_load_3d(s.k + lane * ps * 128, &tm_k, 0, st.kvh, row, &s.k_full);
+                    tma_load_3d(s.k + kHalf + lane * ps * 128, &tm_k, 64, st.kvh, row, &s.k_full);
                 }
             }
-            if (go && open) {
-                st.kind = kUnitEnd;
-                go = open_slot();
-                if (go) publish(st);
+            const int b = t % kStages;
+            if (t >= kStages && !wait(&s.q_empty[b], (uint32_t)((t / kStages - 1) & 1))) { go = false; break; }
+            if (lane == 0) {
+                const int h = st.kvh * G + cur.g;
+                mbar_arrive_expect_tx(&s.q_full[b], kTile);
+                tma_load_3d(s.q[b], &tm_q, 0, h, cur.q0, &s.q_full[b]);
+                tma_load_3d(s.q[b] + kHalf, &tm_q, 64, h, cur.q0, &s.q_full[b]);
             }
+            ++t;
+            if (!open_slot()) { go = false; break; }
+#pragma unroll
+            for (int i = 0; i < kQ / 32; ++i) s.lse[d % kSlots][lane + 32 * i] = l[i] * -kLog2e;
+            st.kind = kWork;
+            publish(st);
+            if (!next.live || next.st.first) {           // that was the unit's last step
+                if (!open_slot()) { go = false; break; }
+                st.kind = kUnitEnd;
+                publish(st);
+            }
+            cur = next;
+#pragma unroll
+            for (int i = 0; i < kQ / 32; ++i) l[i] = nl[i];
         }
         if (go && open_slot()) {
             Step st{};
