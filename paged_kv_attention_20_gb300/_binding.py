@@ -304,7 +304,7 @@ def paged_kv_store(plan: Plan, new_k, new_v, k_cache, v_cache) -> None:
                                  v_cache.data_ptr(), heads, d, dv, _DTYPES[dt], _stream(dev)))
 
 
-def _attn_common(plan, q, k_cache, v_cache, out, disjoint=True):
+def _attn_common(plan, q, k_cache, v_cache, out):
     dev, dt = q.device, q.dtype
     if dt not in _DTYPES:
         raise TypeError("dtype must be float32, float16 or bfloat16")
@@ -324,8 +324,7 @@ def _attn_common(plan, q, k_cache, v_cache, out, disjoint=True):
         _tensor(out, "out", dt, dev, 3)
         if tuple(out.shape) != shape:
             raise ValueError(f"out must have shape {shape}")
-    if disjoint:                # else the library checks
-        _check_disjoint(out, q, k_cache, v_cache)
+    _check_disjoint(out, q, k_cache, v_cache)
     return out
 
 
@@ -395,28 +394,59 @@ def paged_mla_forward(plan: Plan, q, qp, latent_cache, pos_cache, scale: float, 
     return out
 
 
-def _key_mass(t, plan: Plan, heads: int, device) -> None:
-    _tensor(t, "key_mass", torch.float32, device, 3)
-    if tuple(t.shape) != (plan.pages, heads, plan.page_size):
+def _dense(t, name: str, dtype, device, index: int, rank: int):
+    """Shape of a dense operand.  The common case costs four attribute reads; anything else gets its message."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous()):
+        _tensor(t, name, dtype, device, rank)
+    shape = t.shape
+    if len(shape) != rank:
+        raise ValueError(f"{name} must have rank {rank}")
+    return shape
+
+
+def _cuda_index(device) -> int:
+    return device.index if device.type == "cuda" else -1
+
+
+def _key_mass(t, pages: int, heads: int, page_size: int, device, index: int) -> None:
+    if _dense(t, "key_mass", torch.float32, device, index, 3) != (pages, heads, page_size):
         raise ValueError("key_mass must be [pages, kv_heads, page_size]")
 
 
-def _rows(t, name: str, dtype, device, queries: int, dim: int) -> int:
-    """A [queries, heads, dim] operand whose rows may lie apart; returns the row stride in elements."""
+def _caches(plan: Plan, k_cache, v_cache):
+    """Checks of a K/V cache pair against the plan; (dtype, device, device index, K shape, value dim)."""
+    if not isinstance(k_cache, torch.Tensor):
+        raise TypeError("k_cache must be a torch.Tensor")
+    dev, dt = k_cache.device, k_cache.dtype
+    if dt not in _DTYPES:
+        raise TypeError("dtype must be float32, float16 or bfloat16")
+    index = _cuda_index(dev)
+    shape = _dense(k_cache, "k_cache", dt, dev, index, 4)
+    pages, ps, hkv, dv = _dense(v_cache, "v_cache", dt, dev, index, 4)
+    _plan_ready(plan, dev)
+    if shape[0] != pages or shape[1] != ps or shape[2] != hkv or pages != plan.pages or ps != plan.page_size:
+        raise ValueError("cache shapes do not match the plan")
+    return dt, dev, index, shape, dv
+
+
+def _rows(t, name: str, dtype, device, index: int, queries: int, dim: int):
+    """A [queries, heads, dim] operand whose rows may lie apart; returns (heads, row stride in elements)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.dim() != 3:
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{name} must have rank 3")
-    if t.shape[0] != queries or t.shape[2] != dim:
+    n, heads, d = shape
+    if n != queries or d != dim:
         raise ValueError(f"{name} must be [queries, heads, {dim}] matching the plan and cache")
     sq, sh, sd = t.stride()
-    if (dim > 1 and sd != 1) or (t.shape[1] > 1 and sh != dim):
+    if (sd != 1 and dim > 1) or (sh != dim and heads > 1):
         raise ValueError(f"{name}: each row's heads must be contiguous")
-    return sq if queries > 1 else t.shape[1] * dim
+    return heads, sq if queries > 1 else heads * dim
 
 
 def paged_qk_norm_rope_store(plan: Plan, q, new_k, new_v, k_cache, v_cache, rope_table=None, q_weight=None,
@@ -428,57 +458,46 @@ def paged_qk_norm_rope_store(plan: Plan, q, new_k, new_v, k_cache, v_cache, rope
     fp32 [max_positions, rope_dim], cosines then sines; `positions` (int32 [Q]) replaces the plan's positions for
     the rotation; key_mass, when given, is zeroed at the written keys.  Returns the queries, dense (`q_out` may be
     a dense q itself)."""
-    dev, dt = k_cache.device, k_cache.dtype
-    if dt not in _DTYPES:
-        raise TypeError("dtype must be float32, float16 or bfloat16")
-    _tensor(k_cache, "k_cache", dt, dev, 4)
-    _tensor(v_cache, "v_cache", dt, dev, 4)
-    _plan_ready(plan, dev)
-    pages, ps, hkv, d = k_cache.shape
-    dv, n = v_cache.shape[3], plan.queries
-    if tuple(v_cache.shape[:3]) != (pages, ps, hkv) or pages != plan.pages or ps != plan.page_size:
-        raise ValueError("cache shapes do not match the plan")
-    q_stride = _rows(q, "q", dt, dev, n, d)
-    k_stride = _rows(new_k, "new_k", dt, dev, n, d)
-    v_stride = _rows(new_v, "new_v", dt, dev, n, dv)
-    hq = q.shape[1]
-    if new_k.shape[1] != hkv or new_v.shape[1] != hkv:
+    dt, dev, index, (pages, ps, hkv, d), dv = _caches(plan, k_cache, v_cache)
+    n = plan.queries
+    hq, q_stride = _rows(q, "q", dt, dev, index, n, d)
+    hk, k_stride = _rows(new_k, "new_k", dt, dev, index, n, d)
+    hv, v_stride = _rows(new_v, "new_v", dt, dev, index, n, dv)
+    if hk != hkv or hv != hkv:
         raise ValueError("new rows must be [queries, kv_heads, d|dv]")
     table_ptr = pos_ptr = mass_ptr = qw_ptr = kw_ptr = None
     far = rot = 0
     if rope_table is not None:
-        _tensor(rope_table, "rope_table", torch.float32, dev, 2)
-        far, rot = rope_table.shape
+        far, rot = _dense(rope_table, "rope_table", torch.float32, dev, index, 2)
         if far == 0 or rot == 0:        # an empty tensor's null pointer would read as "no table"
             raise ValueError("the rope table is empty")
         table_ptr = rope_table.data_ptr()
     if positions is not None:
-        _tensor(positions, "positions", torch.int32, dev, 1)
-        if positions.shape[0] != n:
+        if _dense(positions, "positions", torch.int32, dev, index, 1)[0] != n:
             raise ValueError("positions must be [queries]")
         pos_ptr = positions.data_ptr()
     if q_weight is not None:
-        _tensor(q_weight, "q_weight", dt, dev, 1)
+        if _dense(q_weight, "q_weight", dt, dev, index, 1)[0] != d:
+            raise ValueError("norm weights must be [head_dim]")
         qw_ptr = q_weight.data_ptr()
     if k_weight is not None:
-        _tensor(k_weight, "k_weight", dt, dev, 1)
-        kw_ptr = k_weight.data_ptr()
-    for w in (q_weight, k_weight):
-        if w is not None and w.shape[0] != d:
+        if _dense(k_weight, "k_weight", dt, dev, index, 1)[0] != d:
             raise ValueError("norm weights must be [head_dim]")
+        kw_ptr = k_weight.data_ptr()
     if key_mass is not None:
-        _key_mass(key_mass, plan, hkv, dev)
+        _key_mass(key_mass, pages, hkv, ps, dev, index)
         mass_ptr = key_mass.data_ptr()
     if q_out is None:
         q_out = torch.empty((n, hq, d), dtype=dt, device=dev)
-    else:
-        _tensor(q_out, "q_out", dt, dev, 3)
-        if tuple(q_out.shape) != (n, hq, d):
-            raise ValueError(f"q_out must have shape {(n, hq, d)}")
-    _check(load().paged_qk_norm_rope_store(
-        plan.handle, q.data_ptr(), q_stride, new_k.data_ptr(), k_stride, new_v.data_ptr(), v_stride, q_out.data_ptr(),
+    elif _dense(q_out, "q_out", dt, dev, index, 3) != (n, hq, d):
+        raise ValueError(f"q_out must have shape {(n, hq, d)}")
+    lib = _LIB or load()
+    status = lib.paged_qk_norm_rope_store(
+        plan._handle, q.data_ptr(), q_stride, new_k.data_ptr(), k_stride, new_v.data_ptr(), v_stride, q_out.data_ptr(),
         k_cache.data_ptr(), v_cache.data_ptr(), mass_ptr, table_ptr, far, rot, 1 if interleaved else 0, pos_ptr, qw_ptr,
-        kw_ptr, float(eps), hq, hkv, d, dv, _DTYPES[dt], _stream(dev)))
+        kw_ptr, eps, hq, hkv, d, dv, _DTYPES[dt], _stream(dev))
+    if status:
+        _check(status)
     return q_out
 
 
@@ -501,17 +520,27 @@ def paged_attn_forward_mass(plan: Plan, q, k_cache, v_cache, key_mass, scale: fl
     """Paged attention that adds each key's softmax weights, over the plan's queries and a KV head's query heads, to
     key_mass [pages, kv_heads, page_size] (fp32).  splits defaults to the split heuristic; the workspace is allocated
     here when not given (make_mass_workspace)."""
-    out = _attn_common(plan, q, k_cache, v_cache, out, disjoint=False)
-    hq, hkv, dv = q.shape[1], k_cache.shape[2], v_cache.shape[3]
-    _key_mass(key_mass, plan, hkv, q.device)
+    dt, dev, index, (pages, ps, hkv, d), dv = _caches(plan, k_cache, v_cache)
+    n, hq, dq = _dense(q, "q", dt, dev, index, 3)
+    if n != plan.queries or dq != d:
+        raise ValueError("q must be [queries, num_heads, head_dim] matching the plan and cache")
+    if out is None:
+        out = torch.empty((n, hq, dv), dtype=dt, device=dev)
+    elif _dense(out, "out", dt, dev, index, 3) != (n, hq, dv):
+        raise ValueError(f"out must have shape {(n, hq, dv)}")
+    _key_mass(key_mass, pages, hkv, ps, dev, index)
     if splits is None:
         splits = paged_attn_split_heuristic(plan, hq, hkv, window=window)
     if workspace is None:
-        workspace = make_mass_workspace(plan, hq, hkv, dv, splits, window if causal else 0, device=q.device)
-    _check(load().paged_attn_forward_mass(
-        plan.handle, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), key_mass.data_ptr(), hq, hkv,
-        q.shape[2], dv, float(scale), 1 if causal else 0, int(window), _DTYPES[q.dtype], workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), int(splits), _stream(q.device)))
+        workspace = make_mass_workspace(plan, hq, hkv, dv, splits, window if causal else 0, device=dev)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    lib = _LIB or load()
+    status = lib.paged_attn_forward_mass(
+        plan._handle, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), key_mass.data_ptr(), hq, hkv, d,
+        dv, scale, 1 if causal else 0, window, _DTYPES[dt], workspace.data_ptr(), workspace.nbytes, splits, _stream(dev))
+    if status:
+        _check(status)
     return out
 
 
@@ -519,26 +548,21 @@ def paged_kv_evict(plan: Plan, kept_plan: Plan, key_mass, k_cache, v_cache, sink
     """Shrink every sequence of `plan` to its length in `kept_plan`: the first `sink`, the last `recent` and, between
     them, the keys with the largest key_mass stay and move to the kept schedule's rows.  Returns the kept keys' former
     indices, int32 [sequences, kv_heads, longest kept history], -1 past a sequence's kept length."""
-    dev, dt = k_cache.device, k_cache.dtype
-    if dt not in _DTYPES:
-        raise TypeError("dtype must be float32, float16 or bfloat16")
-    _tensor(k_cache, "k_cache", dt, dev, 4)
-    _tensor(v_cache, "v_cache", dt, dev, 4)
-    _plan_ready(plan, dev)
+    dt, dev, index, (pages, ps, hkv, d), dv = _caches(plan, k_cache, v_cache)
     _plan_ready(kept_plan, dev)
-    pages, ps, hkv, d = k_cache.shape
-    if tuple(v_cache.shape[:3]) != (pages, ps, hkv) or pages != plan.pages or ps != plan.page_size:
-        raise ValueError("cache shapes do not match the plan")
-    _key_mass(key_mass, plan, hkv, dev)
+    _key_mass(key_mass, pages, hkv, ps, dev, index)
     if kept is None:
         kept = torch.empty((plan.sequences, hkv, kept_plan.longest), dtype=torch.int32, device=dev)
+        stride = kept_plan.longest
     else:
-        _tensor(kept, "kept", torch.int32, dev, 3)
-        if tuple(kept.shape[:2]) != (plan.sequences, hkv):
+        sequences, heads, stride = _dense(kept, "kept", torch.int32, dev, index, 3)
+        if sequences != plan.sequences or heads != hkv:
             raise ValueError("kept must be [sequences, kv_heads, n]")
-    _check(load().paged_kv_evict(plan.handle, kept_plan.handle, key_mass.data_ptr(), k_cache.data_ptr(),
-                                 v_cache.data_ptr(), kept.data_ptr(), kept.shape[2], int(sink), int(recent), hkv, d,
-                                 v_cache.shape[3], _DTYPES[dt], _stream(dev)))
+    lib = _LIB or load()
+    status = lib.paged_kv_evict(plan._handle, kept_plan._handle, key_mass.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                kept.data_ptr(), stride, sink, recent, hkv, d, dv, _DTYPES[dt], _stream(dev))
+    if status:
+        _check(status)
     return kept
 
 
