@@ -97,7 +97,7 @@ cudaError_t add_item_mass(const pa_plan *plan, const AttnArgs &a, const MassLayo
     m.group_list = m.group_start + plan->sequences + 1;
     m.longest = (int32_t)plan->max_seq_len;
     const bool repeated = (plan_facts(plan) & kFactRepeatedItems) != 0;
-    cudaError_t e = repeated ? launch_mass_index(m, kMassItems, st) : cudaSuccess;
+    cudaError_t e = mass_items_grouped(m, repeated) ? launch_mass_index(m, kMassItems, st) : cudaSuccess;
     if (e == cudaSuccess) e = launch_mass_items(m, repeated, merge ? &a : nullptr, use_list, st);
     return e;
 }

@@ -17,6 +17,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "merge.cuh"
 #include "pa_internal.h"
 
@@ -175,155 +177,305 @@ constexpr int kItemKeys = 4 * kItemThreads;     // four keys a thread and step
 constexpr int kHeadsAtOnce = 4;                 // score rows in flight
 constexpr int kMaxStagedHeads = 64;
 
-// One CTA per (sequence or item, KV head, block of keys): four consecutive keys
-// per thread and step, the group's heads in turn.  The scores come from L2 when
+// Sequences of one item: a CTA per (item, KV head, block of keys), four consecutive
+// keys per thread and step, the group's heads in turn.  The scores come from L2 when
 // they fit there (4 bytes a key and head), the totals are read and written once.
 // The pass is latency-bound (metadata, then scores, table and log-sum-exps, then
 // the totals): the first step's scores are asked for before the log-sum-exps are
 // merged.
-// Key j always falls to block (j / kItemKeys) % blocks and to one thread of it,
-// whatever an item's own range: the items of a sequence never meet on a key.
 // kQuads: pages hold whole aligned fours of keys and the totals are 16-byte
 // aligned.
 template <bool kQuads>
-__device__ __forceinline__ void add_items(const MassArgs &a, int repeated, int blocks, int ps_shift, int block, float *lse) {
+__device__ __forceinline__ void add_item(const MassArgs &a, int blocks, int ps_shift, int block, float *lse) {
     const int blk = block % blocks;
     const int rest = block / blocks;
-    const int kvh = rest % a.hkv, unit = rest / a.hkv;
+    const int kvh = rest % a.hkv, item = rest / a.hkv;
     const int G = a.hq / a.hkv, ps = a.plan.page_size;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int first = repeated ? a.group_start[unit] : unit, last = repeated ? a.group_start[unit + 1] : unit + 1;
     const int64_t rows = (int64_t)a.plan.queries * a.hq;
-    for (int e = first; e < last; ++e) {
-        const int item = repeated ? a.group_list[e] : e;
-        const int qi = a.plan.decode[item];
-        // what hangs on the query alone is asked for at once: its metadata and the
-        // first of this warp's log-sum-exps (over the splits, two a lane)
-        const int64_t row0 = (int64_t)qi * a.hq + kvh * G;
-        const bool mine = warp < G;
-        float l0 = mine && lane < a.splits ? a.lse[lane * rows + row0 + warp] : -INFINITY;
-        float l1 = mine && lane + 32 < a.splits ? a.lse[(lane + 32) * rows + row0 + warp] : -INFINITY;
-        const int4 meta = a.plan.qmeta[qi];
-        int64_t lo64, hi64;
-        visible_range(meta.y, a.causal ? 0 : a.plan.seq_lens[meta.x], a.causal, a.window, lo64, hi64);
-        const int lo = (int)lo64, hi = (int)hi64;       // positions fit 32 bits
-        if (hi - lo > a.cap || hi > (1 << 30)) {
-            // the workspace holds no scores past cap: this item adds nothing (nor does
-            // one whose steps could leave 32 bits)
-            if (threadIdx.x == 0) atomicCAS(a.status, 0, PA_DEVICE_RANGE);
-            continue;
-        }
-        const int step = blocks * kItemKeys;             // at most about the longest history
-        const int start = lo / step * step + blk * kItemKeys;
-        if (start >= hi || (start + kItemKeys <= lo && start + step >= hi)) continue;   // nothing here (uniform)
-        const int32_t *trow = a.plan.table + (int64_t)meta.x * a.plan.width;
-        const bool aligned = (lo & 3) == 0;
-        for (int g0 = 0; g0 < G; g0 += kMaxStagedHeads) {
-            const int gn = min(G - g0, kMaxStagedHeads);
-            const float *head0 = a.scores + ((int64_t)item * a.hq + kvh * G + g0) * a.cap - lo;
-            float4 early[kHeadsAtOnce];
-            int page = 0;
-            auto ask = [&](int j) {                     // the page and the first heads' scores of four keys
-                if (j >= lo && j + 4 <= hi) {
-                    if (kQuads) page = trow[ps_shift >= 0 ? j >> ps_shift : j / ps];
+    const int qi = a.plan.decode[item];
+    // what hangs on the query alone is asked for at once: its metadata and the
+    // first of this warp's log-sum-exps (over the splits, two a lane)
+    const int64_t row0 = (int64_t)qi * a.hq + kvh * G;
+    const bool mine = warp < G;
+    float l0 = mine && lane < a.splits ? a.lse[lane * rows + row0 + warp] : -INFINITY;
+    float l1 = mine && lane + 32 < a.splits ? a.lse[(lane + 32) * rows + row0 + warp] : -INFINITY;
+    const int4 meta = a.plan.qmeta[qi];
+    int64_t lo64, hi64;
+    visible_range(meta.y, a.causal ? 0 : a.plan.seq_lens[meta.x], a.causal, a.window, lo64, hi64);
+    const int lo = (int)lo64, hi = (int)hi64;       // positions fit 32 bits
+    if (hi - lo > a.cap || hi > (1 << 30)) {
+        // the workspace holds no scores past cap: this item adds nothing (nor does
+        // one whose steps could leave 32 bits)
+        if (threadIdx.x == 0) atomicCAS(a.status, 0, PA_DEVICE_RANGE);
+        return;
+    }
+    const int step = blocks * kItemKeys;             // at most about the longest history
+    const int start = lo / step * step + blk * kItemKeys;
+    if (start >= hi || (start + kItemKeys <= lo && start + step >= hi)) return;   // nothing here (uniform)
+    const int32_t *trow = a.plan.table + (int64_t)meta.x * a.plan.width;
+    const bool aligned = (lo & 3) == 0;
+    for (int g0 = 0; g0 < G; g0 += kMaxStagedHeads) {
+        const int gn = min(G - g0, kMaxStagedHeads);
+        const float *head0 = a.scores + ((int64_t)item * a.hq + kvh * G + g0) * a.cap - lo;
+        float4 early[kHeadsAtOnce];
+        int page = 0;
+        auto ask = [&](int j) {                     // the page and the first heads' scores of four keys
+            if (j >= lo && j + 4 <= hi) {
+                if (kQuads) page = trow[ps_shift >= 0 ? j >> ps_shift : j / ps];
 #pragma unroll
-                    for (int g = 0; g < kHeadsAtOnce; ++g)
-                        if (aligned && g < gn) early[g] = *reinterpret_cast<const float4 *>(head0 + j + g * a.cap);
-                }
-            };
-            int j = start + 4 * (int)threadIdx.x;
-            ask(j);
-            __syncthreads();
-            for (int g = warp; g < gn; g += kItemWarps) {
-                if (g0 + g != warp) {
-                    l0 = lane < a.splits ? a.lse[lane * rows + row0 + g0 + g] : -INFINITY;
-                    l1 = lane + 32 < a.splits ? a.lse[(lane + 32) * rows + row0 + g0 + g] : -INFINITY;
-                }
-                float m = fmaxf(l0, l1);
-                for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                float t = (l0 == -INFINITY ? 0.f : exp2f((l0 - m) * kLog2e)) + (l1 == -INFINITY ? 0.f : exp2f((l1 - m) * kLog2e));
-                for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-                if (lane == 0) lse[g] = a.splits == 1 ? l0 * kLog2e : m * kLog2e + log2f(t);
+                for (int g = 0; g < kHeadsAtOnce; ++g)
+                    if (aligned && g < gn) early[g] = *reinterpret_cast<const float4 *>(head0 + j + g * a.cap);
             }
-            __syncthreads();
-            for (; j < hi; j += step) {
-                if (j + 4 <= lo) {
-                    ask(j + step);
-                    continue;
-                }
-                const float *sc = head0 + j;
-                const bool all = j >= lo && j + 4 <= hi;
-                float4 *m = nullptr;
-                float4 old;
-                if (kQuads && all) {
-                    m = reinterpret_cast<float4 *>(a.key_mass + ((int64_t)page * a.hkv + kvh) * ps +
-                                                   (ps_shift >= 0 ? j & (ps - 1) : j % ps));
-                    old = *m;
-                }
-                float p[4] = {0.f, 0.f, 0.f, 0.f};
-                if (all && aligned) {
+        };
+        int j = start + 4 * (int)threadIdx.x;
+        ask(j);
+        __syncthreads();
+        for (int g = warp; g < gn; g += kItemWarps) {
+            if (g0 + g != warp) {
+                l0 = lane < a.splits ? a.lse[lane * rows + row0 + g0 + g] : -INFINITY;
+                l1 = lane + 32 < a.splits ? a.lse[(lane + 32) * rows + row0 + g0 + g] : -INFINITY;
+            }
+            float m = fmaxf(l0, l1);
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            float t = (l0 == -INFINITY ? 0.f : exp2f((l0 - m) * kLog2e)) + (l1 == -INFINITY ? 0.f : exp2f((l1 - m) * kLog2e));
+            for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+            if (lane == 0) lse[g] = a.splits == 1 ? l0 * kLog2e : m * kLog2e + log2f(t);
+        }
+        __syncthreads();
+        for (; j < hi; j += step) {
+            if (j + 4 <= lo) {
+                ask(j + step);
+                continue;
+            }
+            const float *sc = head0 + j;
+            const bool all = j >= lo && j + 4 <= hi;
+            float4 *m = nullptr;
+            float4 old;
+            if (kQuads && all) {
+                m = reinterpret_cast<float4 *>(a.key_mass + ((int64_t)page * a.hkv + kvh) * ps +
+                                               (ps_shift >= 0 ? j & (ps - 1) : j % ps));
+                old = *m;
+            }
+            float p[4] = {0.f, 0.f, 0.f, 0.f};
+            if (all && aligned) {
 #pragma unroll
-                    for (int g = 0; g < kHeadsAtOnce; ++g)
-                        if (g < gn) {
-                            const float4 v = early[g];
-                            const float l = lse[g];
-                            p[0] += exp2f(v.x - l); p[1] += exp2f(v.y - l); p[2] += exp2f(v.z - l); p[3] += exp2f(v.w - l);
-                        }
-                    ask(j + step);
-#pragma unroll 4
-                    for (int g = kHeadsAtOnce; g < gn; ++g) {
-                        const float4 v = *reinterpret_cast<const float4 *>(sc + g * a.cap);
+                for (int g = 0; g < kHeadsAtOnce; ++g)
+                    if (g < gn) {
+                        const float4 v = early[g];
                         const float l = lse[g];
                         p[0] += exp2f(v.x - l); p[1] += exp2f(v.y - l); p[2] += exp2f(v.z - l); p[3] += exp2f(v.w - l);
                     }
-                } else {
-                    ask(j + step);
-                    for (int g = 0; g < gn; ++g)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (j + i >= lo && j + i < hi) p[i] += exp2f(sc[g * a.cap + i] - lse[g]);
+                ask(j + step);
+#pragma unroll 4
+                for (int g = kHeadsAtOnce; g < gn; ++g) {
+                    const float4 v = *reinterpret_cast<const float4 *>(sc + g * a.cap);
+                    const float l = lse[g];
+                    p[0] += exp2f(v.x - l); p[1] += exp2f(v.y - l); p[2] += exp2f(v.z - l); p[3] += exp2f(v.w - l);
                 }
-                if (kQuads && all) {
-                    old.x += p[0]; old.y += p[1]; old.z += p[2]; old.w += p[3];
-                    *m = old;
-                } else {
+            } else {
+                ask(j + step);
+                for (int g = 0; g < gn; ++g)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (j + i >= lo && j + i < hi) {
-                            const int pg = (j + i) / ps;
-                            a.key_mass[((int64_t)trow[pg] * a.hkv + kvh) * ps + (j + i - pg * ps)] += p[i];
+                        if (j + i >= lo && j + i < hi) p[i] += exp2f(sc[g * a.cap + i] - lse[g]);
+            }
+            if (kQuads && all) {
+                old.x += p[0]; old.y += p[1]; old.z += p[2]; old.w += p[3];
+                *m = old;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (j + i >= lo && j + i < hi) {
+                        const int pg = (j + i) / ps;
+                        a.key_mass[((int64_t)trow[pg] * a.hkv + kvh) * ps + (j + i - pg * ps)] += p[i];
+                    }
+            }
+        }
+    }
+}
+
+// Sequences of several items (drafted tokens, short runs): a CTA per (sequence,
+// KV head, block of keys).  It finds the sequence's items among the plan's (or
+// takes them from the grouped list when those are many), stages their ranges and
+// log-sum-exps, eight items at a time, and adds all their weights to a key before
+// it touches the key's total.  Key j always falls to block (j / kItemKeys) % blocks
+// and to one thread of it, whatever an item's own range: no two CTAs meet on a key.
+constexpr int kScanItems = 1024;               // more items in the plan: grouped list
+constexpr int kStagedItems = 8;
+
+struct RepeatedShared {
+    int item[kScanItems], lo[kScanItems], hi[kScanItems];
+    float lse[kStagedItems][kMaxStagedHeads];
+    int count[kItemWarps];
+};
+
+template <bool kQuads>
+__device__ __forceinline__ void add_repeated(const MassArgs &a, int grouped, int blocks, int ps_shift, int block,
+                                             RepeatedShared &sh) {
+    const int blk = block % blocks;
+    const int rest = block / blocks;
+    const int kvh = rest % a.hkv, seq = rest / a.hkv;
+    const int G = a.hq / a.hkv, ps = a.plan.page_size;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t rows = (int64_t)a.plan.queries * a.hq;
+    const int seq_len = a.plan.seq_lens[seq];
+    const int32_t *trow = a.plan.table + (int64_t)seq * a.plan.width;
+    const int step = blocks * kItemKeys;
+    auto stage = [&](int at, int item, int pos) {
+        int64_t lo, hi;
+        visible_range(pos, seq_len, a.causal, a.window, lo, hi);
+        if (hi - lo > a.cap || hi > (1 << 30)) {
+            atomicCAS(a.status, 0, PA_DEVICE_RANGE);    // no scores past cap: adds nothing
+            lo = hi = 0;
+        }
+        sh.item[at] = item;
+        sh.lo[at] = (int)lo;
+        sh.hi[at] = (int)hi;
+    };
+    const int g_first = grouped ? a.group_start[seq] : 0, g_last = grouped ? a.group_start[seq + 1] : 0;
+    for (int base = g_first; grouped ? base < g_last : base == 0; base += kScanItems) {
+        // this round's items, in the order of the plan's list
+        int cnt = 0;
+        __syncthreads();
+        if (grouped) {
+            cnt = min(kScanItems, g_last - base);
+            for (int i = tid; i < cnt; i += kItemThreads) {
+                const int item = a.group_list[base + i];
+                stage(i, item, a.plan.qmeta[a.plan.decode[item]].y);
+            }
+        } else {
+            for (int i0 = 0; i0 < a.plan.n_decode; i0 += kItemThreads) {
+                const int i = i0 + tid;
+                int4 meta = make_int4(-1, 0, 0, 0);
+                if (i < a.plan.n_decode) meta = a.plan.qmeta[a.plan.decode[i]];
+                const unsigned hit = __ballot_sync(0xffffffffu, meta.x == seq);
+                if (lane == 0) sh.count[warp] = __popc(hit);
+                __syncthreads();
+                int at = cnt + __popc(hit & ((1u << lane) - 1u));
+                for (int w = 0; w < kItemWarps; ++w) {
+                    at += w < warp ? sh.count[w] : 0;
+                    cnt += sh.count[w];
+                }
+                if (meta.x == seq) stage(at, i, meta.y);
+                __syncthreads();
+            }
+        }
+        __syncthreads();
+        for (int e0 = 0; e0 < cnt; e0 += kStagedItems) {
+            const int items = min(kStagedItems, cnt - e0);
+            int lo_all = 0x7fffffff, hi_all = 0;
+            for (int i = 0; i < items; ++i) {
+                lo_all = min(lo_all, sh.lo[e0 + i]);
+                hi_all = max(hi_all, sh.hi[e0 + i]);
+            }
+            const int start = lo_all / step * step + blk * kItemKeys;
+            if (start >= hi_all || (start + kItemKeys <= lo_all && start + step >= hi_all)) continue;   // uniform
+            for (int g0 = 0; g0 < G; g0 += kMaxStagedHeads) {
+                const int gn = min(G - g0, kMaxStagedHeads);
+                __syncthreads();
+                for (int k = warp; k < items * gn; k += kItemWarps) {
+                    const int i = k / gn, g = k - i * gn;
+                    const int64_t row = (int64_t)a.plan.decode[sh.item[e0 + i]] * a.hq + kvh * G + g0 + g;
+                    const float l0 = lane < a.splits ? a.lse[lane * rows + row] : -INFINITY;
+                    const float l1 = lane + 32 < a.splits ? a.lse[(lane + 32) * rows + row] : -INFINITY;
+                    float m = fmaxf(l0, l1);
+                    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    float t = (l0 == -INFINITY ? 0.f : exp2f((l0 - m) * kLog2e)) +
+                              (l1 == -INFINITY ? 0.f : exp2f((l1 - m) * kLog2e));
+                    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+                    if (lane == 0) sh.lse[i][g] = a.splits == 1 ? l0 * kLog2e : m * kLog2e + log2f(t);
+                }
+                __syncthreads();
+                for (int j = start + 4 * tid; j < hi_all; j += step) {
+                    float p[4] = {0.f, 0.f, 0.f, 0.f};
+                    bool any[4] = {false, false, false, false};
+#pragma unroll 2
+                    for (int i = 0; i < items; ++i) {
+                        const int lo = sh.lo[e0 + i], hi = sh.hi[e0 + i];
+                        if (j + 4 <= lo || j >= hi) continue;
+                        const float *sc = a.scores + ((int64_t)sh.item[e0 + i] * a.hq + kvh * G + g0) * a.cap + (j - lo);
+                        if (j >= lo && j + 4 <= hi) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) any[k] = true;
+                            const bool aligned = (lo & 3) == 0;
+#pragma unroll 4
+                            for (int g = 0; g < gn; ++g) {
+                                float4 v;
+                                if (aligned)
+                                    v = *reinterpret_cast<const float4 *>(sc + g * a.cap);
+                                else
+                                    v = make_float4(sc[g * a.cap], sc[g * a.cap + 1], sc[g * a.cap + 2], sc[g * a.cap + 3]);
+                                const float l = sh.lse[i][g];
+                                p[0] += exp2f(v.x - l); p[1] += exp2f(v.y - l); p[2] += exp2f(v.z - l); p[3] += exp2f(v.w - l);
+                            }
+                        } else {
+                            for (int g = 0; g < gn; ++g)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    if (j + k >= lo && j + k < hi) {
+                                        any[k] = true;
+                                        p[k] += exp2f(sc[g * a.cap + k] - sh.lse[i][g]);
+                                    }
                         }
+                    }
+                    if (kQuads && any[0] && any[1] && any[2] && any[3]) {
+                        const int pg = ps_shift >= 0 ? j >> ps_shift : j / ps;
+                        float4 *m = reinterpret_cast<float4 *>(a.key_mass + ((int64_t)trow[pg] * a.hkv + kvh) * ps + (j - pg * ps));
+                        float4 v = *m;
+                        v.x += p[0]; v.y += p[1]; v.z += p[2]; v.w += p[3];
+                        *m = v;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (any[k]) {
+                                const int pg = (j + k) / ps;
+                                a.key_mass[((int64_t)trow[pg] * a.hkv + kvh) * ps + (j + k - pg * ps)] += p[k];
+                            }
+                    }
                 }
             }
         }
     }
 }
 
-template <bool kQuads>
-__global__ void __launch_bounds__(kItemThreads, 4) mass_items_kernel(MassArgs a, int repeated, int blocks, int ps_shift) {
+// kRepeated: some sequence has several items (units are sequences, else items).
+template <bool kQuads, bool kRepeated>
+__global__ void __launch_bounds__(kItemThreads, 4) mass_items_kernel(MassArgs a, int grouped, int blocks, int ps_shift) {
     griddep_wait();
     griddep_launch();
-    __shared__ float lse[kMaxStagedHeads];
-    add_items<kQuads>(a, repeated, blocks, ps_shift, blockIdx.x, lse);
+    if constexpr (kRepeated) {
+        __shared__ RepeatedShared sh;
+        add_repeated<kQuads>(a, grouped, blocks, ps_shift, blockIdx.x, sh);
+    } else {
+        __shared__ float lse[kMaxStagedHeads];
+        add_item<kQuads>(a, blocks, ps_shift, blockIdx.x, lse);
+    }
 }
 
 // The merge of the split outputs and the totals in one launch: both follow the
 // decode kernel and neither needs the other.  The first merge_blocks CTAs merge.
-template <typename T, int VEC, bool kQuads>
+template <typename T, int VEC, bool kQuads, bool kRepeated>
 __global__ void __launch_bounds__(kItemThreads, 4) merge_and_items_kernel(AttnArgs attn, MassArgs a, int use_list, int nrows,
-                                                                       int wide, int merge_blocks, int repeated, int blocks,
-                                                                       int ps_shift) {
+                                                                          int wide, int merge_blocks, int grouped, int blocks,
+                                                                          int ps_shift) {
     griddep_wait();
     griddep_launch();
     extern __shared__ float part[];
-    __shared__ float lse[kMaxStagedHeads];
     if ((int)blockIdx.x < merge_blocks) {
         if (wide)
             merge_row_wide<T, VEC>(attn, use_list, blockIdx.x, part);
         else
             merge_rows<T, VEC>(attn, use_list, nrows, blockIdx.x);
+        return;
+    }
+    const int block = (int)blockIdx.x - merge_blocks;
+    if constexpr (kRepeated) {
+        __shared__ RepeatedShared sh;
+        add_repeated<kQuads>(a, grouped, blocks, ps_shift, block, sh);
     } else {
-        add_items<kQuads>(a, repeated, blocks, ps_shift, (int)blockIdx.x - merge_blocks, lse);
+        __shared__ float lse[kMaxStagedHeads];
+        add_item<kQuads>(a, blocks, ps_shift, block, lse);
     }
 }
 
@@ -426,6 +578,8 @@ cudaError_t launch_lse_final(const MassArgs &a, float *out, cudaStream_t st) {
     return launch_pdl(lse_final_kernel, dim3((unsigned)((rows + 255) / 256)), dim3(256), 0, st, a, out);
 }
 
+bool mass_items_grouped(const MassArgs &a, bool repeated) { return repeated && a.plan.n_decode > kScanItems; }
+
 cudaError_t launch_mass_items(const MassArgs &a, bool repeated, const AttnArgs *merge, bool use_list, cudaStream_t st) {
     const int64_t units = (int64_t)(repeated ? a.plan.sequences : a.plan.n_decode) * a.hkv;
     // blocks a unit: one per 1024 keys of the longest history, but no more than fill
@@ -438,12 +592,15 @@ cudaError_t launch_mass_items(const MassArgs &a, bool repeated, const AttnArgs *
         for (shift = 0; (1 << shift) < ps; ++shift) {}
     const bool quads = ps % 4 == 0 && reinterpret_cast<uintptr_t>(a.key_mass) % 16 == 0;
     const dim3 block(kItemThreads);
-    const int rep = repeated ? 1 : 0;
+    const int grouped = mass_items_grouped(a, repeated) ? 1 : 0;
     cudaError_t e;
     if (!merge) {
         const dim3 grid((unsigned)(units * blocks));
-        e = quads ? launch_pdl(mass_items_kernel<true>, grid, block, 0, st, a, rep, blocks, shift)
-                  : launch_pdl(mass_items_kernel<false>, grid, block, 0, st, a, rep, blocks, shift);
+        auto launch = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, st, a, grouped, blocks, shift); };
+        if (repeated)
+            e = quads ? launch(mass_items_kernel<true, true>) : launch(mass_items_kernel<false, true>);
+        else
+            e = quads ? launch(mass_items_kernel<true, false>) : launch(mass_items_kernel<false, false>);
     } else {
         const int nrows = (use_list ? a.plan.n_decode : a.plan.queries) * a.hq;
         const bool wide = merge_is_wide(*merge, nrows);
@@ -452,19 +609,23 @@ cudaError_t launch_mass_items(const MassArgs &a, bool repeated, const AttnArgs *
         const dim3 grid((unsigned)(mb + units * blocks));
         const size_t smem = wide ? (size_t)8 * merge->dv * sizeof(float) : 0;
         auto launch = [&](auto kernel) {
-            return launch_pdl(kernel, grid, block, smem, st, *merge, a, use_list ? 1 : 0, nrows, wide ? 1 : 0, (int)mb, rep,
-                              blocks, shift);
+            return launch_pdl(kernel, grid, block, smem, st, *merge, a, use_list ? 1 : 0, nrows, wide ? 1 : 0, (int)mb,
+                              grouped, blocks, shift);
+        };
+        auto by_kind = [&](auto t, auto vec) {
+            using T = decltype(t);
+            constexpr int VEC = decltype(vec)::value;
+            if (repeated)
+                return quads ? launch(merge_and_items_kernel<T, VEC, true, true>)
+                             : launch(merge_and_items_kernel<T, VEC, false, true>);
+            return quads ? launch(merge_and_items_kernel<T, VEC, true, false>)
+                         : launch(merge_and_items_kernel<T, VEC, false, false>);
         };
         auto by_vec = [&](auto t) {
-            using T = decltype(t);
             const int vec = merge_vec(*merge);
-            if (quads)
-                return vec == 4   ? launch(merge_and_items_kernel<T, 4, true>)
-                       : vec == 2 ? launch(merge_and_items_kernel<T, 2, true>)
-                                  : launch(merge_and_items_kernel<T, 1, true>);
-            return vec == 4   ? launch(merge_and_items_kernel<T, 4, false>)
-                   : vec == 2 ? launch(merge_and_items_kernel<T, 2, false>)
-                              : launch(merge_and_items_kernel<T, 1, false>);
+            return vec == 4   ? by_kind(t, std::integral_constant<int, 4>())
+                   : vec == 2 ? by_kind(t, std::integral_constant<int, 2>())
+                              : by_kind(t, std::integral_constant<int, 1>());
         };
         e = a.dtype == PA_F32 ? by_vec(float()) : (a.dtype == PA_F16 ? by_vec(__half()) : by_vec(__nv_bfloat16()));
     }

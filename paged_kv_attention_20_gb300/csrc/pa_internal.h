@@ -162,7 +162,9 @@ enum MassRecords { kMassItems = 0, kMassTiles = 1, kMassQueries = 2 };
 // Records of one kind (decode items, prefill tiles, single queries) grouped by sequence.
 cudaError_t launch_mass_index(const MassArgs &a, MassRecords kind, cudaStream_t st);
 cudaError_t launch_lse_final(const MassArgs &a, float *out, cudaStream_t st);
-// Decode items from their stored scores; `repeated`: sequences may have several items (grouped first).
+// Decode items from their stored scores; `repeated`: sequences may have several items
+// (grouped first by launch_mass_index where mass_items_grouped says so).
+bool mass_items_grouped(const MassArgs &a, bool repeated);
 // merge (not null): the same launch merges the split outputs of these attention arguments.
 cudaError_t launch_mass_items(const MassArgs &a, bool repeated, const AttnArgs *merge, bool use_list, cudaStream_t st);
 // Grouped tiles, scores recomputed on the tensor cores (prefill_supported shapes).

@@ -87,6 +87,16 @@ def test_several_queries_of_a_sequence(cuda_device, hq, hkv, d, ps, dt, window):
     verify(case, 4, True, window)
 
 
+def test_many_items_in_few_sequences(cuda_device):
+    """More decode items than a CTA scans for its sequence (they come from a grouped list), every second position."""
+    lens = [1500, 1300, 40]
+    queries = [(s, p) for s, n in enumerate(lens) for p in range(0, n, 2)]
+    case = build_case("mass", 17, lens, queries, 4, 2, 64, 64, 16, BF, 0.125)
+    assert case.num_queries > 1024
+    verify(case, 1)
+    verify(case, 2, True, 300)
+
+
 def test_drafted_tokens_under_a_window(cuda_device):
     """Queries a few positions apart see ranges a few keys apart: every key still has one owner."""
     lens = [2000, 1111, 700]
