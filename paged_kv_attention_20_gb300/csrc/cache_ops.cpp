@@ -50,10 +50,16 @@ MassLayout mass_layout(const pa_plan *plan, int32_t hq, int32_t dv, int32_t spli
     l.lse = part;
     l.lse_final = l.lse + align256((size_t)splits * rows * sizeof(float));
     l.items = l.lse_final + (splits > 1 && plan->n_tiles > 0 ? align256(rows * sizeof(float)) : 0);
-    // work lists: [sequences + 1] starts and the records (the tiles' also the key blocks)
+    // work lists: [sequences + 1] starts and the records; for tiles also the key
+    // blocks of as many sequences as can have some, and the laid out log-sum-exps
     const size_t seqs = (size_t)plan->sequences + 1;
     l.tiles = l.items + align256((seqs + plan->n_decode) * sizeof(int32_t));
-    l.scores = l.tiles + (plan->n_tiles > 0 ? align256((2 * seqs + plan->queries) * sizeof(int32_t)) : 0);
+    l.blocks = l.tiles + (plan->n_tiles > 0 ? align256((seqs + plan->queries) * sizeof(int32_t)) : 0);
+    const int64_t per_seq = ((int64_t)plan->width * plan->page_size + 127) / 128;
+    const int64_t blocks = std::min<int64_t>(std::min(plan->sequences, plan->n_tiles) * per_seq, INT32_MAX);
+    l.max_blocks = (int32_t)blocks;
+    l.tile_lse = l.blocks + (plan->n_tiles > 0 ? align256(((size_t)blocks + 1) * sizeof(int4)) : 0);
+    l.scores = l.tile_lse + align256((size_t)plan->n_tiles * hq * 128 * sizeof(float));
     int64_t keys = std::max<int64_t>(max_keys, plan->max_seq_len);
     if (window > 0) keys = std::min<int64_t>(keys, window);
     l.cap = plan->n_decode > 0 ? (keys + 31) / 32 * 32 : 0;
@@ -81,14 +87,6 @@ MassArgs mass_args(const AttnArgs &a, const MassLayout &lay, char *ws, float *ke
     return m;
 }
 
-MassArgs tile_args(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass) {
-    MassArgs m = mass_args(a, lay, ws, key_mass, lay.tiles);
-    m.unit_start = m.group_start + plan->sequences + 1;
-    m.group_list = m.unit_start + plan->sequences + 1;
-    m.longest = (int32_t)std::max(longest_tile_seq(plan), plan->max_seq_len);
-    return m;
-}
-
 }  // namespace
 
 cudaError_t add_item_mass(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass, bool merge,
@@ -102,18 +100,22 @@ cudaError_t add_item_mass(const pa_plan *plan, const AttnArgs &a, const MassLayo
     return e;
 }
 
-cudaError_t mass_tile_lists(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass,
-                            cudaStream_t st) {
-    return launch_mass_index(tile_args(plan, a, lay, ws, key_mass), prefill_supported(a) ? kMassTiles : kMassQueries, st);
-}
-
 cudaError_t add_tile_mass(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass,
                           cudaStream_t st) {
-    const MassArgs m = tile_args(plan, a, lay, ws, key_mass);
-    cudaError_t e = cudaSuccess;
-    if (a.splits > 1) e = launch_lse_final(m, reinterpret_cast<float *>(ws + lay.lse_final), st);
-    if (e == cudaSuccess) e = prefill_supported(a) ? launch_mass_tiles(m, st) : launch_mass_recompute(m, st);
-    return e;
+    MassArgs m = mass_args(a, lay, ws, key_mass, lay.tiles);
+    m.group_list = m.group_start + plan->sequences + 1;
+    m.longest = (int32_t)std::max(longest_tile_seq(plan), plan->max_seq_len);
+    if (prefill_supported(a)) {
+        m.n_blocks = reinterpret_cast<int32_t *>(ws + lay.blocks);           // its own 16 bytes, then the list
+        m.blocks = reinterpret_cast<int4 *>(ws + lay.blocks) + 1;
+        m.max_blocks = lay.max_blocks;
+        m.tile_lse = reinterpret_cast<float *>(ws + lay.tile_lse);
+        cudaError_t e = launch_mass_tiles_prepare(m, st);
+        return e == cudaSuccess ? launch_mass_tiles(m, st) : e;
+    }
+    cudaError_t e = launch_mass_index(m, kMassQueries, st);
+    if (e == cudaSuccess && a.splits > 1) e = launch_lse_final(m, reinterpret_cast<float *>(ws + lay.lse_final), st);
+    return e == cudaSuccess ? launch_mass_recompute(m, st) : e;
 }
 
 }  // namespace pa

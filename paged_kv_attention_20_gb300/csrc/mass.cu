@@ -74,11 +74,9 @@ __device__ __forceinline__ int block_prefix(int c, int *sums) {
     return before + x;
 }
 
-// One CTA: group_start[s] .. group_start[s+1] delimit the records of sequence s
+// One CTA of 1024 threads: group_start[s] .. group_start[s+1] delimit the records of sequence s
 // in group_list, in ascending record order (a stable counting sort).
-__global__ void __launch_bounds__(kIndexThreads) mass_index_kernel(MassArgs a, int kind, int n) {
-    griddep_wait();
-    griddep_launch();
+__device__ __forceinline__ void group_records(const MassArgs &a, int kind, int n) {
     __shared__ __align__(16) int seqs[kIndexThreads];
     __shared__ int carry, sums[32];
     const int S = a.plan.sequences, tid = threadIdx.x;
@@ -87,7 +85,6 @@ __global__ void __launch_bounds__(kIndexThreads) mass_index_kernel(MassArgs a, i
         __shared__ int count[kIndexThreads];
         count[tid] = 0;
         const int mine = tid < n ? record_seq(a.plan, kind, tid) : -1;
-        const int len = kind == kMassTiles && tid < S ? a.plan.seq_lens[tid] : 0;
         seqs[tid] = mine;
         __syncthreads();
         if (mine >= 0) atomicAdd(&count[mine], 1);
@@ -107,10 +104,6 @@ __global__ void __launch_bounds__(kIndexThreads) mass_index_kernel(MassArgs a, i
             for (; t < tid; ++t) before += seqs[t] == mine;
             a.group_list[count[mine] + before] = tid;
         }
-        if (kind != kMassTiles) return;
-        const int blocks = c > 0 ? (len + 127) / 128 : 0;
-        const int to = block_prefix(blocks, sums);
-        if (tid <= S) a.unit_start[tid] = to - blocks;
         return;
     }
     for (int s = tid; s <= S; s += kIndexThreads) a.group_start[s] = 0;
@@ -156,18 +149,73 @@ __global__ void __launch_bounds__(kIndexThreads) mass_index_kernel(MassArgs a, i
         if (s <= S) a.group_start[s] = v;
         __syncthreads();
     }
-    if (kind != kMassTiles) return;
-    // blocks of 128 keys of the sequences that have tiles, and their prefix sums
-    if (tid == 0) carry = 0;
-    __syncthreads();
-    for (int base = 0; base <= S; base += kIndexThreads) {
-        const int s = base + tid;
-        const int c = s < S && a.group_start[s + 1] > a.group_start[s] ? (a.plan.seq_lens[s] + 127) / 128 : 0;
-        const int x = block_prefix(c, sums);
-        if (s <= S) a.unit_start[s] = carry + x - c;
+}
+
+__global__ void __launch_bounds__(kIndexThreads) mass_index_kernel(MassArgs a, int kind, int n) {
+    griddep_wait();
+    griddep_launch();
+    group_records(a, kind, n);
+}
+
+// ------------------------------------------------------------------- tiles --
+// Block 0 groups the tiles by sequence and lists the key blocks of the sequences
+// that have some: blocks[i] = {sequence, first key, its tiles [z, w) in the
+// list}.  Every other block lays out one tile's log-sum-exps: [Hq][128], merged
+// over the splits, negated and in log2 units, 0 past the tile's queries.
+__global__ void __launch_bounds__(kIndexThreads) mass_tiles_prepare_kernel(MassArgs a) {
+    griddep_wait();
+    griddep_launch();
+    const int tid = threadIdx.x;
+    if (blockIdx.x == 0) {
+        group_records(a, kMassTiles, a.plan.n_tiles);
+        __syncthreads();                       // group_start is read below by other threads than wrote it
+        __shared__ int sums[32], upto[kIndexThreads];
+        int before = 0;                        // blocks of the sequences before this step's 1024
+        const int S = a.plan.sequences;
+        for (int base = 0; base < S; base += kIndexThreads) {
+            const int s = base + tid;
+            const int z = s < S ? a.group_start[s] : 0, w = s < S ? a.group_start[s + 1] : 0;
+            const int c = w > z ? (a.plan.seq_lens[s] + 127) / 128 : 0;
+            upto[tid] = block_prefix(c, sums);
+            __syncthreads();
+            const int total = upto[kIndexThreads - 1];
+            for (int i = tid; i < total; i += kIndexThreads) {
+                int lo = 0, hi = kIndexThreads - 1;    // first entry whose inclusive sum passes i
+                while (lo < hi) {
+                    const int mid = (lo + hi) / 2;
+                    if (upto[mid] > i)
+                        hi = mid;
+                    else
+                        lo = mid + 1;
+                }
+                const int first = lo ? upto[lo - 1] : 0, q = base + lo;
+                if (before + i < a.max_blocks)
+                    a.blocks[before + i] = make_int4(q, 128 * (i - first), a.group_start[q], a.group_start[q + 1]);
+            }
+            before += total;
+            __syncthreads();
+        }
+        if (tid == 0) {
+            if (before > a.max_blocks) atomicCAS(a.status, 0, PA_DEVICE_RANGE);
+            *a.n_blocks = min(before, a.max_blocks);
+        }
+        return;
+    }
+    const int tile_id = (int)blockIdx.x - 1;
+    const int4 tile = a.plan.tiles[tile_id];
+    __shared__ float part[128][33];
+    float *out = a.tile_lse + (int64_t)tile_id * a.hq * 128;
+    for (int h0 = 0; h0 < a.hq; h0 += 32) {
         __syncthreads();
-        if (tid == kIndexThreads - 1) carry += x;
+        for (int i = tid; i < 128 * 32; i += kIndexThreads) {
+            const int c = i >> 5, h = h0 + (i & 31);
+            part[c][i & 31] = c < tile.z && h < a.hq ? -merged_lse2(a, (int64_t)(tile.y + c) * a.hq + h) : 0.f;
+        }
         __syncthreads();
+        for (int i = tid; i < 128 * 32; i += kIndexThreads) {
+            const int h = h0 + (i >> 7), c = i & 127;
+            if (h < a.hq) out[(int64_t)h * 128 + c] = part[c][i >> 7];
+        }
     }
 }
 
@@ -571,6 +619,10 @@ template <typename T> cudaError_t launch_re(const MassArgs &a, cudaStream_t st) 
 cudaError_t launch_mass_index(const MassArgs &a, MassRecords kind, cudaStream_t st) {
     const int n = kind == kMassItems ? a.plan.n_decode : (kind == kMassTiles ? a.plan.n_tiles : a.plan.queries);
     return launch_pdl(mass_index_kernel, dim3(1), dim3(kIndexThreads), 0, st, a, (int)kind, n);
+}
+
+cudaError_t launch_mass_tiles_prepare(const MassArgs &a, cudaStream_t st) {
+    return launch_pdl(mass_tiles_prepare_kernel, dim3((unsigned)(1 + a.plan.n_tiles)), dim3(kIndexThreads), 0, st, a);
 }
 
 cudaError_t launch_lse_final(const MassArgs &a, float *out, cudaStream_t st) {

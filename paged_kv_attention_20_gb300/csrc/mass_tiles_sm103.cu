@@ -13,10 +13,15 @@
 // quarter rate) before the tensor core does; two CTAs of 96 KB per SM keep one's
 // exponentials running over the other's waits.
 //
-// Roles: warps 0-3 add up (thread r = key row r), warp 4 walks the CTA's units
-// and loads K (one box per page and 64-column half), Q and the log-sum-exps, warp 5
-// issues the MMAs.  A ring of step descriptors in shared memory tells warps 0-3
-// and 5 what each step is.  All waits are bounded (timeout -> device status word).
+// Before it, `mass_tiles_prepare_kernel` lists the key blocks of every sequence
+// with tiles and lays the log-sum-exps out tile by tile, negated and in log2
+// units, so that a step's 128 arrive with one bulk copy.
+//
+// Roles: warps 0-7 add up (row r of the keys is shared by warps r/32 and r/32 + 4,
+// 64 columns each), warp 8 walks the CTA's units and starts the loads of K (one
+// box per page and 64-column half), Q and the log-sum-exps, warp 9 issues the
+// MMAs.  A ring of step descriptors in shared memory tells warps 0-7 and 9 what
+// each step is.  All waits are bounded (timeout -> device status word).
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -38,7 +43,8 @@ constexpr int kHalf = 128 * 128;        // bytes of 128 rows x 64 columns
 constexpr int kTile = 2 * kHalf;
 constexpr int kStages = 2;              // Q ring and S buffers
 constexpr int kSlots = 4;               // step descriptors
-constexpr int kThreads = 192;
+constexpr int kAdders = 8;              // adding warps: two per TMEM lane quarter, 64 columns each
+constexpr int kThreads = 32 * (kAdders + 2);
 constexpr uint32_t kTmemCols = kStages * kQ;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -54,8 +60,10 @@ struct Step {
 struct Smem {
     uint8_t k[kTile];
     uint8_t q[kStages][kTile];
-    float lse[kSlots][kQ];                    // negated, log2 units
+    // 16-byte aligned: bulk copies land here
+    float lse[kSlots][kQ];                    // of the step's columns: negated, log2 units, 0 past the tile
     Step step[kSlots];
+    float part[4][kKeys];                     // second halves' sums at the end of a unit
     uint64_t k_full, k_empty;
     uint64_t q_full[kStages], q_empty[kStages];
     uint64_t s_full[kStages], s_empty[kStages];
@@ -66,13 +74,20 @@ struct Smem {
 struct TileParams {
     PlanView plan;
     float *key_mass;
-    const float *lse;                         // [queries, Hq], natural log
-    const int32_t *group_start, *group_list;  // tiles by sequence
-    const int32_t *unit_start;                // [sequences + 1] key blocks before a sequence
+    const float *lse;                         // [tiles, Hq, 128]
+    const int32_t *group_list;                // tiles by sequence
+    const int4 *blocks;                       // key blocks: {seq, first key, list entries [z, w)}
+    const int32_t *n_blocks;
     int hq, hkv, causal, window, bf16;
     float scale_log2;
     int32_t *status;
 };
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
 
 __global__ void __launch_bounds__(kThreads, 2)
     mass_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, TileParams prm) {
@@ -93,11 +108,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             mbar_init(&s.q_full[i], 1);
             mbar_init(&s.q_empty[i], 1);
             mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.s_empty[i], 128);
+            mbar_init(&s.s_empty[i], 32 * kAdders);
         }
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&s.d_full[i], 1);
-            mbar_init(&s.d_empty[i], 5);      // four adding warps and the MMA issuer
+            mbar_init(&s.d_empty[i], kAdders + 1);      // the adding warps and the MMA issuer
         }
         fence_mbar_init();
     }
@@ -110,16 +125,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     const uint32_t tmem = s.tmem_base;
 
-    if (warp == 4) {
+    if (warp == kAdders) {
         // ---------------------------------------------------- producer --
         if (lane == 0) {
             tma_prefetch_desc(&tm_q);
             tma_prefetch_desc(&tm_k);
         }
-        const int S = prm.plan.sequences;
-        const int units = prm.unit_start[S] * prm.hkv;
+        const int units = *prm.n_blocks * prm.hkv;
         const int oob_row = prm.plan.pages * ps;
-        const int boxes = kKeys / ps;
+        const int n_boxes = kKeys / ps;
         int t = 0, d = 0, u_open = 0;          // steps, descriptors and units (K loads) so far
         bool go = true;
         // lane 0 waits, the warp follows
@@ -128,146 +142,108 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (lane == 0) ok = mbar_wait(bar, parity) ? 1 : 0;
             return __shfl_sync(0xffffffffu, ok, 0) != 0;
         };
-        auto open_slot = [&]() -> bool { return d < kSlots || wait(&s.d_empty[d % kSlots], (uint32_t)((d / kSlots - 1) & 1)); };
-        auto publish = [&](const Step &st) {
-            if (lane == 0) s.step[d % kSlots] = st;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.d_full[d % kSlots]);
-            ++d;
-        };
-        // The walk over the steps runs one ahead of the loads, so that a step's
-        // metadata and log-sum-exps have a step's time to arrive (in turn, their
-        // latency made this warp the slowest role, ~2400 cycles a step).
-        struct Walk {
-            int u, e, e1, g;          // unit, entry of the tile list and its end, head of the group
-            int q0;                   // first query of the tile
-            int4 tile;                // the entry's tile
-            Step st;
-            bool live;
-        };
-        auto open_unit = [&](Walk &w) {                  // tile list and key block of unit w.u
-            const int blk = w.u / prm.hkv;
-            // the sequence whose blocks hold blk: last one that starts at or before it
-            int seq = 0;
-            for (int n = S; n > 1;) {
-                const int step = (n + 31) / 32, at = lane * step;
-                const bool le = at < n && prm.unit_start[seq + at] <= blk;
-                const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;
-                seq += k * step;
-                n = min(step, n - k * step);
-            }
-            w.st.kvh = w.u - blk * prm.hkv;
-            w.st.key0 = (blk - prm.unit_start[seq]) * kKeys;
-            w.st.seq_len = prm.plan.seq_lens[seq];
-            const uint64_t trow = reinterpret_cast<uint64_t>(prm.plan.table + (int64_t)seq * prm.plan.width);
-            w.st.trow_lo = (int32_t)(uint32_t)trow;
-            w.st.trow_hi = (int32_t)(uint32_t)(trow >> 32);
-            w.e = prm.group_start[seq];
-            w.e1 = prm.group_start[seq + 1];
-            w.tile = prm.plan.tiles[prm.group_list[w.e]];   // a unit's sequence has tiles
-            w.st.first = 1;
-        };
-        // to the first tile from w.e on that sees the unit's keys; past the unit's
-        // tiles, to the next unit
-        auto settle = [&](Walk &w) {
-            while (true) {
-                while (w.e < w.e1) {
-                    const int hi = prm.causal ? w.tile.w + w.tile.z : w.st.seq_len;
-                    const int64_t lo = prm.window > 0 ? (int64_t)w.tile.w - prm.window + 1 : 0;
-                    if (w.st.key0 < hi && (int64_t)w.st.key0 + kKeys > lo) {
-                        w.q0 = w.tile.y;
-                        w.st.nq = w.tile.z;
-                        w.st.pos0 = w.tile.w;
-                        w.g = 0;
-                        ++w.e;
-                        if (w.e < w.e1) w.tile = prm.plan.tiles[prm.group_list[w.e]];
-                        return;
-                    }
-                    ++w.e;
-                    if (w.e < w.e1) w.tile = prm.plan.tiles[prm.group_list[w.e]];
-                }
-                w.u += (int)gridDim.x;
-                if (w.u >= units) {
-                    w.live = false;
-                    return;
-                }
-                open_unit(w);
-            }
-        };
-        auto ask = [&](const Walk &w, float (&l)[kQ / 32]) {   // log-sum-exps of the step's columns
-#pragma unroll
-            for (int i = 0; i < kQ / 32; ++i) {
-                const int c = lane + 32 * i;
-                l[i] = w.live && c < w.st.nq ? prm.lse[(int64_t)(w.q0 + c) * prm.hq + w.st.kvh * G + w.g] : 0.f;
-            }
-        };
-        Walk cur{};
-        cur.u = (int)blockIdx.x;
-        cur.live = cur.u < units;
-        if (cur.live) {
-            open_unit(cur);
-            settle(cur);
-        }
-        float l[kQ / 32];
-        ask(cur, l);
-        while (go && cur.live) {
-            Walk next = cur;
-            next.st.first = 0;
-            if (++next.g == G) settle(next);
-            float nl[kQ / 32];
-            ask(next, nl);
-            Step &st = cur.st;
-            if (st.first) {
-                if (u_open > 0 && !wait(&s.k_empty, (uint32_t)((u_open - 1) & 1))) { go = false; break; }
-                ++u_open;
-                if (lane == 0) mbar_arrive_expect_tx(&s.k_full, kTile);
-                __syncwarp();
-                if (lane < boxes) {
-                    const int32_t *trow = reinterpret_cast<const int32_t *>((uint64_t)(uint32_t)st.trow_lo |
-                                                                            ((uint64_t)(uint32_t)st.trow_hi << 32));
-                    const int lp = st.key0 / ps + lane, used_pages = (st.seq_len + ps - 1) / ps;
-                    const int row = lp < used_pages ? trow[lp] * ps : oob_row;
-                    tma_load_3d(s.k + lane * ps * 128, &tm_k, 0, st.kvh, row, &s.k_full);
-                    tma_load_3d(s.k + kHalf + lane * ps * 128, &tm_k, 64, st.kvh, row, &s.k_full);
-                }
-            }
-            const int b = t % kStages;
-            if (t >= kStages && !wait(&s.q_empty[b], (uint32_t)((t / kStages - 1) & 1))) { go = false; break; }
+        auto slot_free = [&]() -> bool { return d < kSlots || wait(&s.d_empty[d % kSlots], (uint32_t)((d / kSlots - 1) & 1)); };
+        auto tell = [&](const Step &st) -> bool {          // a descriptor without log-sum-exps
+            if (!slot_free()) return false;
             if (lane == 0) {
-                const int h = st.kvh * G + cur.g;
-                mbar_arrive_expect_tx(&s.q_full[b], kTile);
-                tma_load_3d(s.q[b], &tm_q, 0, h, cur.q0, &s.q_full[b]);
-                tma_load_3d(s.q[b] + kHalf, &tm_q, 64, h, cur.q0, &s.q_full[b]);
+                s.step[d % kSlots] = st;
+                mbar_arrive(&s.d_full[d % kSlots]);
             }
-            ++t;
-            if (!open_slot()) { go = false; break; }
-#pragma unroll
-            for (int i = 0; i < kQ / 32; ++i) s.lse[d % kSlots][lane + 32 * i] = l[i] * -kLog2e;
+            ++d;
+            return true;
+        };
+        auto block_of = [&](int u) -> int4 { return u < units ? prm.blocks[u / prm.hkv] : make_int4(0, 0, 0, 0); };
+        // Walk over the CTA's units, their tiles and the group's heads.  Nothing the
+        // loop carries is a load still on its way, but for the next unit's record and
+        // the next tile's number.
+        int u = (int)blockIdx.x;
+        int4 rec = block_of(u);
+        while (go && u < units) {
+            const int4 blk = rec;
+            rec = block_of(u + (int)gridDim.x);
+            Step st{};
             st.kind = kWork;
-            publish(st);
-            if (!next.live || next.st.first) {           // that was the unit's last step
-                if (!open_slot()) { go = false; break; }
-                st.kind = kUnitEnd;
-                publish(st);
+            st.kvh = u % prm.hkv;
+            st.key0 = blk.y;
+            st.seq_len = prm.plan.seq_lens[blk.x];
+            const int32_t *trow = prm.plan.table + (int64_t)blk.x * prm.plan.width;
+            st.trow_lo = (int32_t)(uint32_t)reinterpret_cast<uint64_t>(trow);
+            st.trow_hi = (int32_t)(uint32_t)(reinterpret_cast<uint64_t>(trow) >> 32);
+            // first and one-past-last tile entry that sees the unit's keys, 32 entries at a time
+            auto sees = [&](const int4 &tile) {
+                const int hi = prm.causal ? tile.w + tile.z : st.seq_len;
+                const int64_t lo = prm.window > 0 ? (int64_t)tile.w - prm.window + 1 : 0;
+                return st.key0 < hi && (int64_t)st.key0 + kKeys > lo;
+            };
+            bool open = false;
+            for (int e0 = blk.z; go && e0 < blk.w; e0 += 32) {
+                // a lane looks at one entry; the warp then takes those that count, in order
+                const int id = e0 + lane < blk.w ? prm.group_list[e0 + lane] : -1;
+                const int4 mine = id >= 0 ? prm.plan.tiles[id] : make_int4(0, 0, 0, 0);
+                unsigned todo = __ballot_sync(0xffffffffu, id >= 0 && sees(mine));
+                if (!open && todo) {
+                    // the unit's keys
+                    if (u_open > 0 && !wait(&s.k_empty, (uint32_t)((u_open - 1) & 1))) { go = false; break; }
+                    ++u_open;
+                    if (lane == 0) mbar_arrive_expect_tx(&s.k_full, kTile);
+                    __syncwarp();
+                    if (lane < n_boxes) {
+                        const int lp = st.key0 / ps + lane, used_pages = (st.seq_len + ps - 1) / ps;
+                        const int row = lp < used_pages ? trow[lp] * ps : oob_row;
+                        tma_load_3d(s.k + lane * ps * 128, &tm_k, 0, st.kvh, row, &s.k_full);
+                        tma_load_3d(s.k + kHalf + lane * ps * 128, &tm_k, 64, st.kvh, row, &s.k_full);
+                    }
+                    open = true;
+                    st.first = 1;
+                }
+                while (go && todo) {
+                    const int from = __ffs(todo) - 1;
+                    todo &= todo - 1;
+                    const int tile_id = __shfl_sync(0xffffffffu, id, from);
+                    const int q0 = __shfl_sync(0xffffffffu, mine.y, from);
+                    st.nq = __shfl_sync(0xffffffffu, mine.z, from);
+                    st.pos0 = __shfl_sync(0xffffffffu, mine.w, from);
+                    for (int g = 0; g < G; ++g) {
+                        const int b = t % kStages, sl = d % kSlots, h = st.kvh * G + g;
+                        if (!slot_free()) { go = false; break; }
+                        if (lane == 0) {
+                            s.step[sl] = st;
+                            mbar_arrive_expect_tx(&s.d_full[sl], kQ * sizeof(float));
+                            bulk_load(s.lse[sl], prm.lse + ((int64_t)tile_id * prm.hq + h) * kQ, kQ * sizeof(float), &s.d_full[sl]);
+                        }
+                        ++d;
+                        st.first = 0;
+                        if (t >= kStages && !wait(&s.q_empty[b], (uint32_t)((t / kStages - 1) & 1))) { go = false; break; }
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&s.q_full[b], kTile);
+                            tma_load_3d(s.q[b], &tm_q, 0, h, q0, &s.q_full[b]);
+                            tma_load_3d(s.q[b] + kHalf, &tm_q, 64, h, q0, &s.q_full[b]);
+                        }
+                        ++t;
+                    }
+                }
             }
-            cur = next;
-#pragma unroll
-            for (int i = 0; i < kQ / 32; ++i) l[i] = nl[i];
+            if (go && open) {
+                st.kind = kUnitEnd;
+                go = tell(st);
+            }
+            u += (int)gridDim.x;
         }
-        if (go && open_slot()) {
+        {
             Step st{};
             st.kind = kExit;
-            publish(st);
-        } else if (lane == 0) {
-            atomicCAS(prm.status, 0, PA_DEVICE_TIMEOUT_TMA);
+            if (go) go = tell(st);
         }
+        if (!go && lane == 0) atomicCAS(prm.status, 0, PA_DEVICE_TIMEOUT_TMA);
         // leave only when the last loads have landed (on a timeout some may be unread)
         if (lane == 0) {
             for (int i = t > kStages ? t - kStages : 0; i < t; ++i)
                 mbar_wait(&s.q_full[i % kStages], (uint32_t)((i / kStages) & 1), 2000000ll);
             if (u_open > 0) mbar_wait(&s.k_full, (uint32_t)((u_open - 1) & 1), 2000000ll);
+            for (int i = d > kSlots ? d - kSlots : 0; i < d; ++i)
+                mbar_wait(&s.d_full[i % kSlots], (uint32_t)((i / kSlots) & 1), 2000000ll);
         }
-    } else if (warp == 5) {
+    } else if (warp == kAdders + 1) {
         // -------------------------------------------------- MMA issuer --
         if (lane == 0) {
             const uint32_t idesc = idesc_f16(kKeys, kQ, prm.bf16 != 0, false, false);
@@ -302,81 +278,82 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     } else {
         // ------------------------------------------------ adding warps --
-        const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
+        // Warps w and w + 4 share TMEM lanes 32 * (w % 4) ..: key rows, 64 columns each.
+        const int row = 32 * (warp & 3) + lane, half = warp >> 2, col0 = 64 * half;
+        const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
         const float2 sc2 = make_float2(prm.scale_log2, prm.scale_log2);
         float total = 0.f;
-        int t = 0;
+        int t = 0, unit = 0;
         bool ok = true;
         for (int d = 0;; ++d) {
             const int sl = d % kSlots;
             ok = __all_sync(0xffffffffu, mbar_wait(&s.d_full[sl], (uint32_t)((d / kSlots) & 1)));
             if (!ok) break;
-            const Step st = s.step[sl];
-            if (st.kind == kExit) break;
-            const int j = st.key0 + tid;               // my key
-            if (st.kind == kUnitEnd) {
-                __syncwarp();
+            const int kind = s.step[sl].kind;
+            if (kind == kExit) break;
+            const int j = s.step[sl].key0 + row;       // my key
+            if (kind == kUnitEnd) {
+                const Step st = s.step[sl];
+                // the halves meet; a slot is written again four units on, by when both
+                // have been through the steps between
+                if (half == 1) s.part[unit & 3][row] = total;
+                asm volatile("bar.sync 1, 256;\n" ::: "memory");
                 if (lane == 0) mbar_arrive(&s.d_empty[sl]);
-                if (j < st.seq_len && !(total == 0.f)) {
-                    const int32_t *trow = reinterpret_cast<const int32_t *>((uint64_t)(uint32_t)st.trow_lo |
-                                                                            ((uint64_t)(uint32_t)st.trow_hi << 32));
-                    const int64_t page = trow[j / ps];
-                    prm.key_mass[(page * prm.hkv + st.kvh) * ps + j % ps] += total;
+                if (half == 0) {
+                    total += s.part[unit & 3][row];
+                    if (j < st.seq_len && !(total == 0.f)) {
+                        const int32_t *trow = reinterpret_cast<const int32_t *>((uint64_t)(uint32_t)st.trow_lo |
+                                                                                ((uint64_t)(uint32_t)st.trow_hi << 32));
+                        const int64_t page = trow[j / ps];
+                        prm.key_mass[(page * prm.hkv + st.kvh) * ps + j % ps] += total;
+                    }
                 }
                 total = 0.f;
+                ++unit;
                 continue;
             }
+            const int pos0 = s.step[sl].pos0, nq = s.step[sl].nq;
             const int b = t % kStages;
             ok = __all_sync(0xffffffffu, mbar_wait(&s.s_full[b], (uint32_t)((t / kStages) & 1)));
             if (!ok) break;
             ++t;
             tc_fence_after();
             // columns (queries) that see my key: an interval
-            int n0 = prm.causal ? j - st.pos0 : 0, n1 = st.nq - 1;
-            if (prm.window > 0) n1 = (int)min((int64_t)n1, (int64_t)j - st.pos0 + prm.window - 1);
-            const bool edge = n0 > 0 || n1 < kQ - 1;
-            const uint32_t sb = tmem + lane_off + (uint32_t)(b * kQ);
-            const float4 *ls = reinterpret_cast<const float4 *>(s.lse[sl]);
+            int n0 = prm.causal ? j - pos0 : 0, n1 = nq - 1;
+            if (prm.window > 0) n1 = (int)min((int64_t)n1, (int64_t)j - pos0 + prm.window - 1);
+            const bool edge = n0 > col0 || n1 < col0 + 63;
+            const uint32_t sb = tmem + lane_off + (uint32_t)(b * kQ + col0);
+            const float4 *ls = reinterpret_cast<const float4 *>(s.lse[sl] + col0);
             float2 acc[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.f, 0.f);
+            float v[64];
+            tmem_ld32f(sb, v);
+            tmem_ld32f(sb + 32, v + 32);
+            tmem_wait_ld();
+            // S is in registers: the next MMA may have the buffer
+            tc_fence_before();
+            mbar_arrive(&s.s_empty[b]);
             if (!__any_sync(0xffffffffu, edge)) {
-                // 32 columns at a time, the next ones on their way
-                float v[2][32];
-                tmem_ld32f(sb, v[0]);
-                tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < kQ / 32; ++c) {
-                    if (c + 1 < kQ / 32) tmem_ld32f(sb + (uint32_t)(32 * (c + 1)), v[(c + 1) & 1]);
-                    const float *x = v[c & 1];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 l = ls[8 * c + i / 4];
-                        const float2 p = ffma2(make_float2(x[i], x[i + 1]), sc2, make_float2(l.x, l.y));
-                        const float2 q = ffma2(make_float2(x[i + 2], x[i + 3]), sc2, make_float2(l.z, l.w));
-                        acc[(i / 4 * 2) & 3] = fadd2(acc[(i / 4 * 2) & 3], make_float2(ex2(p.x), ex2(p.y)));
-                        acc[(i / 4 * 2 + 1) & 3] = fadd2(acc[(i / 4 * 2 + 1) & 3], make_float2(ex2(q.x), ex2(q.y)));
-                    }
-                    if (c + 1 < kQ / 32) tmem_wait_ld();
+                for (int i = 0; i < 64; i += 4) {
+                    const float4 l = ls[i / 4];
+                    const float2 p = ffma2(make_float2(v[i], v[i + 1]), sc2, make_float2(l.x, l.y));
+                    const float2 q = ffma2(make_float2(v[i + 2], v[i + 3]), sc2, make_float2(l.z, l.w));
+                    acc[(i / 2) & 3] = fadd2(acc[(i / 2) & 3], make_float2(ex2(p.x), ex2(p.y)));
+                    acc[(i / 2 + 1) & 3] = fadd2(acc[(i / 2 + 1) & 3], make_float2(ex2(q.x), ex2(q.y)));
                 }
             } else {
 #pragma unroll
-                for (int c = 0; c < kQ; c += 32) {
-                    float v[32];
-                    tmem_ld32f(sb + (uint32_t)c, v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float2 x = ffma2(make_float2(v[i], v[i + 1]), sc2,
-                                               make_float2(s.lse[sl][c + i], s.lse[sl][c + i + 1]));
-                        // columns outside the interval hold other queries' scores, NaN included
-                        acc[i & 2] = fadd2(acc[i & 2], make_float2(c + i >= n0 && c + i <= n1 ? ex2(x.x) : 0.f,
-                                                                   c + i + 1 >= n0 && c + i + 1 <= n1 ? ex2(x.y) : 0.f));
-                    }
+                for (int i = 0; i < 64; i += 2) {
+                    const float2 x = ffma2(make_float2(v[i], v[i + 1]), sc2,
+                                           make_float2(s.lse[sl][col0 + i], s.lse[sl][col0 + i + 1]));
+                    // columns outside the interval hold other queries' scores, NaN included
+                    const int c = col0 + i;
+                    acc[i & 2] = fadd2(acc[i & 2], make_float2(c >= n0 && c <= n1 ? ex2(x.x) : 0.f,
+                                                               c + 1 >= n0 && c + 1 <= n1 ? ex2(x.y) : 0.f));
                 }
             }
-            tc_fence_before();
-            mbar_arrive(&s.s_empty[b]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.d_empty[sl]);
             const float2 sum = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
@@ -418,10 +395,10 @@ cudaError_t launch_mass_tiles(const MassArgs &a, cudaStream_t st) {
     TileParams prm{};
     prm.plan = a.plan;
     prm.key_mass = a.key_mass;
-    prm.lse = a.lse_final;
-    prm.group_start = a.group_start;
+    prm.lse = a.tile_lse;
     prm.group_list = a.group_list;
-    prm.unit_start = a.unit_start;
+    prm.blocks = a.blocks;
+    prm.n_blocks = a.n_blocks;
     prm.hq = a.hq; prm.hkv = a.hkv;
     prm.causal = a.causal; prm.window = a.window;
     prm.bf16 = bf16 ? 1 : 0;

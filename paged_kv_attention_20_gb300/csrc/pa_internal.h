@@ -151,7 +151,10 @@ struct MassArgs {
     int64_t cap;
     int32_t *group_start;     // [sequences + 1] records grouped by sequence (launch_mass_index)
     int32_t *group_list;      // [records]
-    int32_t *unit_start;      // [sequences + 1] blocks of 128 keys before a sequence that has tiles
+    int4 *blocks;             // key blocks of the sequences with tiles, at most max_blocks
+    int32_t *n_blocks;
+    int32_t max_blocks;
+    float *tile_lse;          // [tiles, Hq, 128]
     int32_t hq, hkv, d, splits, causal, window;
     float scale;
     pa_dtype dtype;
@@ -168,6 +171,7 @@ bool mass_items_grouped(const MassArgs &a, bool repeated);
 // merge (not null): the same launch merges the split outputs of these attention arguments.
 cudaError_t launch_mass_items(const MassArgs &a, bool repeated, const AttnArgs *merge, bool use_list, cudaStream_t st);
 // Grouped tiles, scores recomputed on the tensor cores (prefill_supported shapes).
+cudaError_t launch_mass_tiles_prepare(const MassArgs &a, cudaStream_t st);
 cudaError_t launch_mass_tiles(const MassArgs &a, cudaStream_t st);
 // Grouped queries of any shape, scores recomputed.
 cudaError_t launch_mass_recompute(const MassArgs &a, cudaStream_t st);

@@ -712,7 +712,6 @@ pa_status attention(const pa_plan *plan, const void *q, const void *k, const voi
                 char *base = static_cast<char *>(ws);
                 if (e == cudaSuccess && plan->n_decode > 0)
                     e = pa::add_item_mass(plan, a, lay, base, key_mass, false, true, st);
-                if (e == cudaSuccess) e = pa::mass_tile_lists(plan, a, lay, base, key_mass, st);
                 if (e == cudaSuccess) e = pa::add_tile_mass(plan, a, lay, base, key_mass, st);
             }
             if (e == cudaSuccess && splits > 1) e = pa::launch_merge(a, false, st);
@@ -727,10 +726,8 @@ pa_status attention(const pa_plan *plan, const void *q, const void *k, const voi
                     e = pa::add_item_mass(plan, a, lay, static_cast<char *>(ws), key_mass, splits > 1, all_decode, st);
             } else {
                 if (e == cudaSuccess && splits > 1) e = pa::launch_merge(a, all_decode, st);
-                if (mass) {
-                    if (e == cudaSuccess) e = pa::mass_tile_lists(plan, a, lay, static_cast<char *>(ws), key_mass, st);
-                    if (e == cudaSuccess) e = pa::add_tile_mass(plan, a, lay, static_cast<char *>(ws), key_mass, st);
-                }
+                if (e == cudaSuccess && mass)
+                    e = pa::add_tile_mass(plan, a, lay, static_cast<char *>(ws), key_mass, st);
             }
         }
     }

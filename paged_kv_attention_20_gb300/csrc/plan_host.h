@@ -59,7 +59,8 @@ pa_status spans_disjoint(const Span *written, int n_written, const Span *read, i
 
 // Workspace of paged_attn_forward_mass: byte offsets of its parts.
 struct MassLayout {
-    size_t lse, lse_final, items, tiles, scores, bytes;   // the split partials start at 0
+    size_t lse, lse_final, items, tiles, blocks, tile_lse, scores, bytes;   // the split partials start at 0
+    int32_t max_blocks;                                    // key blocks of sequences with tiles
     int64_t cap;                                           // keys of one score row
 };
 // max_keys: keys the score rows hold at least; 0: the longest history of the host copy.
@@ -68,12 +69,9 @@ MassLayout mass_layout(const pa_plan *plan, int32_t hq, int32_t dv, int32_t spli
 // The kernels that follow the attention of `a` and add its weights to key_mass:
 // the decode items with stored scores (merging the split outputs in the same
 // launch when `merge`), and the tiles -- or, where the tiles have no tensor-core
-// kernel, every query -- with recomputed ones.  The tiles' work list
-// (mass_tile_lists) depends on the plan alone.
+// kernel, every query -- with recomputed ones.
 cudaError_t add_item_mass(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass, bool merge,
                           bool use_list, cudaStream_t st);
-cudaError_t mass_tile_lists(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass,
-                            cudaStream_t st);
 cudaError_t add_tile_mass(const pa_plan *plan, const AttnArgs &a, const MassLayout &lay, char *ws, float *key_mass,
                           cudaStream_t st);
 // Attention entry body with totals; key_mass is not null.
