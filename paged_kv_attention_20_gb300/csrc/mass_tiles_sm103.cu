@@ -6,22 +6,27 @@
 //   total_j += sum over (query n, head h of the group) of 2^(scale_log2 * k_j . q_n - lse_n)
 // The keys are the M rows of the MMA (S^T = K Q^T: K stays in shared memory, Q
 // tiles of 128 queries of one head stream past), so a key is a TMEM lane and its
-// sum lives in one thread's register: no exchange between threads, no atomics,
-// one fixed order, one add to memory per key.  A step (128 keys x 128 queries)
-// costs 2 * 128^3 flops on the tensor core and 128^2 exponentials; P is never
-// written and V never read.  The exponentials bound it (16384 per step and SM
-// quarter rate) before the tensor core does; two CTAs of 96 KB per SM keep one's
-// exponentials running over the other's waits.
+// sum lives in registers of one or two threads: no atomics, one fixed order, one
+// add to memory per key.  A step (128 keys x 128 queries of one head) costs 2 * 128^3
+// flops on the tensor core (512 cycles at its rate) and 128^2 exponentials (512 cycles
+// at 32 a cycle and SM); P is never written and V never read.
 //
-// Before it, `mass_tiles_prepare_kernel` lists the key blocks of every sequence
-// with tiles and lays the log-sum-exps out tile by tile, negated and in log2
-// units, so that a step's 128 arrive with one bulk copy.
+// `mass_tiles_prepare_kernel` runs before it: it lists the key blocks of every
+// sequence with tiles and lays the log-sum-exps out tile by tile, negated and in
+// log2 units, so that a step's 128 arrive with one bulk copy.
 //
-// Roles: warps 0-7 add up (row r of the keys is shared by warps r/32 and r/32 + 4,
-// 64 columns each), warp 8 walks the CTA's units and starts the loads of K (one
-// box per page and 64-column half), Q and the log-sum-exps, warp 9 issues the
-// MMAs.  A ring of step descriptors in shared memory tells warps 0-7 and 9 what
-// each step is.  All waits are bounded (timeout -> device status word).
+// Roles, two CTAs per SM: warps 0-7 add up, in two groups that take every second
+// step each; warp 8 walks the CTA's units and starts the loads of K (one box per
+// page and 64-column half), Q (two stages) and the log-sum-exps; warp 9 issues the
+// MMAs into two S buffers.  A ring of step descriptors in shared memory tells warps
+// 0-7 and 9 what each step is.  All waits are bounded (timeout -> device status word).
+//
+// Eight chunks of 512 queries over 0.5-4.6K keys, 32 heads (18,900 steps, 65 GFLOP):
+// one thread a key, log-sum-exps gathered by the producer 85 us; producer a step
+// ahead 85 us; log-sum-exps by bulk copy, 64 columns a thread 78 us; two groups on
+// alternate steps 71 us (0.92 PFLOP/s).  What is left is latency: a Q tile arrives
+// ~1500 cycles after its stage is free, and two stages a CTA are all the shared
+// memory holds.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -42,18 +47,20 @@ constexpr int kD = 128;                 // head dim
 constexpr int kHalf = 128 * 128;        // bytes of 128 rows x 64 columns
 constexpr int kTile = 2 * kHalf;
 constexpr int kStages = 2;              // Q ring and S buffers
-constexpr int kSlots = 4;               // step descriptors
-constexpr int kAdders = 8;              // adding warps: two per TMEM lane quarter, 64 columns each
+constexpr int kSlots = 8;               // step descriptors
+constexpr int kAdders = 8;              // adding warps: two groups of four
 constexpr int kThreads = 32 * (kAdders + 2);
 constexpr uint32_t kTmemCols = kStages * kQ;
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum StepKind { kWork = 0, kUnitEnd = 1, kExit = 2 };
 
-struct Step {
+struct alignas(16) Step {
     int kind, first;        // first: this step opens a unit (its K tile is new)
+    int buf;                // S buffer, and so the group of warps, that takes it
+    int key0;
     int pos0, nq;           // position of column 0, live columns
-    int key0, seq_len, kvh;
+    int seq_len, kvh;
     int trow_lo, trow_hi;   // block-table row
 };
 
@@ -63,7 +70,7 @@ struct Smem {
     // 16-byte aligned: bulk copies land here
     float lse[kSlots][kQ];                    // of the step's columns: negated, log2 units, 0 past the tile
     Step step[kSlots];
-    float part[4][kKeys];                     // second halves' sums at the end of a unit
+    float part[2][kKeys];                     // the second group's sums at the end of a unit
     uint64_t k_full, k_empty;
     uint64_t q_full[kStages], q_empty[kStages];
     uint64_t s_full[kStages], s_empty[kStages];
@@ -108,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             mbar_init(&s.q_full[i], 1);
             mbar_init(&s.q_empty[i], 1);
             mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.s_empty[i], 32 * kAdders);
+            mbar_init(&s.s_empty[i], 128);       // one group
         }
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&s.d_full[i], 1);
@@ -176,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 return st.key0 < hi && (int64_t)st.key0 + kKeys > lo;
             };
             bool open = false;
+            st.buf = 0;
             for (int e0 = blk.z; go && e0 < blk.w; e0 += 32) {
                 // a lane looks at one entry; the warp then takes those that count, in order
                 const int id = e0 + lane < blk.w ? prm.group_list[e0 + lane] : -1;
@@ -213,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                         ++d;
                         st.first = 0;
+                        st.buf ^= 1;
                         if (t >= kStages && !wait(&s.q_empty[b], (uint32_t)((t / kStages - 1) & 1))) { go = false; break; }
                         if (lane == 0) {
                             mbar_arrive_expect_tx(&s.q_full[b], kTile);
@@ -248,11 +257,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0) {
             const uint32_t idesc = idesc_f16(kKeys, kQ, prm.bf16 != 0, false, false);
             const uint64_t k_desc = smem_desc(smem_u32(s.k), 16, 1024, kLayoutSwizzle128B);
-            int t = 0, units = 0;
+            int t = 0, units = 0, used[2] = {0, 0};      // used: steps of an S buffer so far
             bool ok = true;
             for (int d = 0;; ++d) {
                 if (!mbar_wait(&s.d_full[d % kSlots], (uint32_t)((d / kSlots) & 1))) { ok = false; break; }
-                const int kind = s.step[d % kSlots].kind, first = s.step[d % kSlots].first;
+                const int4 st = *reinterpret_cast<const int4 *>(&s.step[d % kSlots]);
+                const int kind = st.x, first = st.y, sb = st.z;
                 mbar_arrive(&s.d_empty[d % kSlots]);
                 if (kind == kExit) break;
                 if (kind == kUnitEnd) {
@@ -262,15 +272,16 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const int b = t % kStages;
                 if (first && !mbar_wait(&s.k_full, (uint32_t)(units++ & 1))) { ok = false; break; }
                 if (!mbar_wait(&s.q_full[b], (uint32_t)((t / kStages) & 1))) { ok = false; break; }
-                if (t >= kStages && !mbar_wait(&s.s_empty[b], (uint32_t)((t / kStages - 1) & 1))) { ok = false; break; }
+                const int n = sb ? used[1]++ : used[0]++;
+                if (n > 0 && !mbar_wait(&s.s_empty[sb], (uint32_t)((n - 1) & 1))) { ok = false; break; }
                 tc_fence_after();
                 const uint64_t q_desc = smem_desc(smem_u32(s.q[b]), 16, 1024, kLayoutSwizzle128B);
 #pragma unroll
                 for (int ks = 0; ks < kD / 16; ++ks) {
                     const uint64_t o = (uint64_t)(((ks / 4) * kHalf + (ks % 4) * 32) >> 4);
-                    mma_f16_ss(tmem + (uint32_t)(b * kQ), k_desc + o, q_desc + o, idesc, ks > 0 ? 1u : 0u);
+                    mma_f16_ss(tmem + (uint32_t)(sb * kQ), k_desc + o, q_desc + o, idesc, ks > 0 ? 1u : 0u);
                 }
-                mma_commit(&s.s_full[b]);
+                mma_commit(&s.s_full[sb]);
                 mma_commit(&s.q_empty[b]);
                 ++t;
             }
@@ -278,29 +289,31 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     } else {
         // ------------------------------------------------ adding warps --
-        // Warps w and w + 4 share TMEM lanes 32 * (w % 4) ..: key rows, 64 columns each.
-        const int row = 32 * (warp & 3) + lane, half = warp >> 2, col0 = 64 * half;
-        const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+        // Group g = warps 4g .. 4g + 3 takes the steps of S buffer g, every second one
+        // of a unit, so that one group's waits and start of a step lie under the
+        // other's exponentials.  A thread is a key row (TMEM lane 32 * (warp % 4) + lane).
+        const int row = 32 * (warp & 3) + lane, group = warp >> 2;
+        const uint32_t sb = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)(group * kQ);
         const float2 sc2 = make_float2(prm.scale_log2, prm.scale_log2);
         float total = 0.f;
-        int t = 0, unit = 0;
+        int n = 0, unit = 0;                            // my steps and units so far
         bool ok = true;
         for (int d = 0;; ++d) {
             const int sl = d % kSlots;
             ok = __all_sync(0xffffffffu, mbar_wait(&s.d_full[sl], (uint32_t)((d / kSlots) & 1)));
             if (!ok) break;
-            const int kind = s.step[sl].kind;
-            if (kind == kExit) break;
-            const int j = s.step[sl].key0 + row;       // my key
-            if (kind == kUnitEnd) {
+            const int4 what = *reinterpret_cast<const int4 *>(&s.step[sl]);
+            if (what.x == kExit) break;
+            const int j = what.w + row;                // my key
+            if (what.x == kUnitEnd) {
                 const Step st = s.step[sl];
-                // the halves meet; a slot is written again four units on, by when both
-                // have been through the steps between
-                if (half == 1) s.part[unit & 3][row] = total;
+                // the groups meet; a slot of `part` is written again two units on, past the
+                // next unit's barrier, which the first group joins after it has read
+                if (group == 1) s.part[unit & 1][row] = total;
                 asm volatile("bar.sync 1, 256;\n" ::: "memory");
                 if (lane == 0) mbar_arrive(&s.d_empty[sl]);
-                if (half == 0) {
-                    total += s.part[unit & 3][row];
+                if (group == 0) {
+                    total += s.part[unit & 1][row];
                     if (j < st.seq_len && !(total == 0.f)) {
                         const int32_t *trow = reinterpret_cast<const int32_t *>((uint64_t)(uint32_t)st.trow_lo |
                                                                                 ((uint64_t)(uint32_t)st.trow_hi << 32));
@@ -312,46 +325,56 @@ __global__ void __launch_bounds__(kThreads, 2)
                 ++unit;
                 continue;
             }
-            const int pos0 = s.step[sl].pos0, nq = s.step[sl].nq;
-            const int b = t % kStages;
-            ok = __all_sync(0xffffffffu, mbar_wait(&s.s_full[b], (uint32_t)((t / kStages) & 1)));
+            if (what.z != group) {                     // the other group's step
+                if (lane == 0) mbar_arrive(&s.d_empty[sl]);
+                continue;
+            }
+            const int2 cols = *reinterpret_cast<const int2 *>(&s.step[sl].pos0);    // pos0, nq
+            ok = __all_sync(0xffffffffu, mbar_wait(&s.s_full[group], (uint32_t)(n & 1)));
             if (!ok) break;
-            ++t;
+            ++n;
             tc_fence_after();
+            float v[2][32];
+            tmem_ld32f(sb, v[0]);
             // columns (queries) that see my key: an interval
-            int n0 = prm.causal ? j - pos0 : 0, n1 = nq - 1;
-            if (prm.window > 0) n1 = (int)min((int64_t)n1, (int64_t)j - pos0 + prm.window - 1);
-            const bool edge = n0 > col0 || n1 < col0 + 63;
-            const uint32_t sb = tmem + lane_off + (uint32_t)(b * kQ + col0);
-            const float4 *ls = reinterpret_cast<const float4 *>(s.lse[sl] + col0);
+            int n0 = prm.causal ? j - cols.x : 0, n1 = cols.y - 1;
+            if (prm.window > 0) n1 = (int)min((int64_t)n1, (int64_t)j - cols.x + prm.window - 1);
+            const bool edge = __any_sync(0xffffffffu, n0 > 0 || n1 < kQ - 1);
+            const float4 *ls = reinterpret_cast<const float4 *>(s.lse[sl]);
             float2 acc[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.f, 0.f);
-            float v[64];
-            tmem_ld32f(sb, v);
-            tmem_ld32f(sb + 32, v + 32);
-            tmem_wait_ld();
-            // S is in registers: the next MMA may have the buffer
-            tc_fence_before();
-            mbar_arrive(&s.s_empty[b]);
-            if (!__any_sync(0xffffffffu, edge)) {
+            // 32 columns at a time, the next ones on their way
 #pragma unroll
-                for (int i = 0; i < 64; i += 4) {
-                    const float4 l = ls[i / 4];
-                    const float2 p = ffma2(make_float2(v[i], v[i + 1]), sc2, make_float2(l.x, l.y));
-                    const float2 q = ffma2(make_float2(v[i + 2], v[i + 3]), sc2, make_float2(l.z, l.w));
-                    acc[(i / 2) & 3] = fadd2(acc[(i / 2) & 3], make_float2(ex2(p.x), ex2(p.y)));
-                    acc[(i / 2 + 1) & 3] = fadd2(acc[(i / 2 + 1) & 3], make_float2(ex2(q.x), ex2(q.y)));
+            for (int c = 0; c < kQ / 32; ++c) {
+                tmem_wait_ld();
+                if (c + 1 < kQ / 32) {
+                    tmem_ld32f(sb + (uint32_t)(32 * (c + 1)), v[(c + 1) & 1]);
+                } else {
+                    // all of S is in registers: the next MMA may have the buffer
+                    tc_fence_before();
+                    mbar_arrive(&s.s_empty[group]);
                 }
-            } else {
+                const float *x = v[c & 1];
+                if (!edge) {
 #pragma unroll
-                for (int i = 0; i < 64; i += 2) {
-                    const float2 x = ffma2(make_float2(v[i], v[i + 1]), sc2,
-                                           make_float2(s.lse[sl][col0 + i], s.lse[sl][col0 + i + 1]));
-                    // columns outside the interval hold other queries' scores, NaN included
-                    const int c = col0 + i;
-                    acc[i & 2] = fadd2(acc[i & 2], make_float2(c >= n0 && c <= n1 ? ex2(x.x) : 0.f,
-                                                               c + 1 >= n0 && c + 1 <= n1 ? ex2(x.y) : 0.f));
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 l = ls[8 * c + i / 4];
+                        const float2 p = ffma2(make_float2(x[i], x[i + 1]), sc2, make_float2(l.x, l.y));
+                        const float2 q = ffma2(make_float2(x[i + 2], x[i + 3]), sc2, make_float2(l.z, l.w));
+                        acc[(i / 2) & 3] = fadd2(acc[(i / 2) & 3], make_float2(ex2(p.x), ex2(p.y)));
+                        acc[(i / 2 + 1) & 3] = fadd2(acc[(i / 2 + 1) & 3], make_float2(ex2(q.x), ex2(q.y)));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const int col = 32 * c + i;
+                        const float2 l = reinterpret_cast<const float2 *>(ls)[col / 2];
+                        const float2 p = ffma2(make_float2(x[i], x[i + 1]), sc2, l);
+                        // columns outside the interval hold other queries' scores, NaN included
+                        acc[(i / 2) & 3] = fadd2(acc[(i / 2) & 3], make_float2(col >= n0 && col <= n1 ? ex2(p.x) : 0.f,
+                                                                               col + 1 >= n0 && col + 1 <= n1 ? ex2(p.y) : 0.f));
+                    }
                 }
             }
             __syncwarp();
