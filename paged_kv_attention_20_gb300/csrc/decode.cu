@@ -390,6 +390,7 @@ __global__ void __launch_bounds__(128) decode_generic_kernel(AttnArgs a, int use
     const T *vg = static_cast<const T *>(a.v);
     const T *kpg = static_cast<const T *>(a.kp);
     const float qs = a.scale * kLog2e;
+    const bool wide_k = a.d % (16 / (int)sizeof(T)) == 0 && (reinterpret_cast<uintptr_t>(a.k) & 15u) == 0;
     {
         const T *qrow = static_cast<const T *>(a.q) + ((int64_t)qi * a.hq + h) * a.d;
         for (int i = tid; i < a.d; i += 128) qf[i] = to_f<T>(qrow[i]) * qs;
@@ -413,7 +414,19 @@ __global__ void __launch_bounds__(128) decode_generic_kernel(AttnArgs a, int use
             rows_sm[tid] = row;
             const T *kr = kg + (row * a.hkv + kvh) * a.d;
             float dot = 0.f;
-            for (int e = 0; e < a.d; ++e) dot = fmaf(qf[e], to_f<T>(kr[e]), dot);
+            int e = 0;
+            if (wide_k) {
+                // 16 bytes a load; the products still add up in element order
+                constexpr int V = 16 / sizeof(T);
+                union { uint4 u; T t[V]; } x;
+#pragma unroll 4
+                for (; e < a.d; e += V) {
+                    x.u = *reinterpret_cast<const uint4 *>(kr + e);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) dot = fmaf(qf[e + i], to_f<T>(x.t[i]), dot);
+                }
+            }
+            for (; e < a.d; ++e) dot = fmaf(qf[e], to_f<T>(kr[e]), dot);
             if (a.p) {
                 const T *kpr = kpg + row * a.p;
                 for (int e = 0; e < a.p; ++e) dot = fmaf(qpf[e], to_f<T>(kpr[e]), dot);
@@ -436,6 +449,7 @@ __global__ void __launch_bounds__(128) decode_generic_kernel(AttnArgs a, int use
             const int c = tid + 128 * i;
             if (c < a.dv) {
                 float x = acc[i] * alpha;
+#pragma unroll 8
                 for (int t = 0; t < cnt; ++t)
                     x = fmaf(p_sm[t], to_f<T>(vg[(rows_sm[t] * a.hkv + kvh) * a.dv + c]), x);
                 acc[i] = x;
