@@ -88,6 +88,20 @@ def test_ties_and_odd_totals(cuda_device, name):
     verify([700, 90], [333, 20], sink=2, recent=5, totals=totals)
 
 
+@pytest.mark.parametrize("n,m", [(3000, 1500), (200000, 60000)])
+@pytest.mark.parametrize("spread", [1e-6, 1.0, 30.0])
+@pytest.mark.parametrize("levels", [0, 3, 900, 5000])
+def test_crowded_and_wide_totals(cuda_device, n, m, spread, levels):
+    """Totals that crowd into a sliver, or span most of the exponents, with up to thousands of equal values around the
+    threshold: the choice takes from one to three rounds."""
+    def totals(rng, k, hkv):
+        x = np.exp(np.clip(spread * rng.standard_normal((k, hkv)), -80, 80))
+        if levels:
+            x = np.round(x / x.max() * levels) / levels if spread < 5 else np.exp(np.round(np.log(x) * levels / 900) * 900 / levels)
+        return np.clip(x, 0, 3e38).astype(np.float32)
+    verify([n], [m], hkv=2, d=8, dv=8, sink=4, recent=7, totals=totals)
+
+
 def test_many_sequences(cuda_device):
     rng = np.random.default_rng(5)
     lens = [int(x) for x in rng.integers(30, 900, size=70)]
