@@ -21,7 +21,7 @@
 // MMAs into two S buffers.  A ring of step descriptors in shared memory tells warps
 // 0-7 and 9 what each step is.  All waits are bounded (timeout -> device status word).
 //
-// Eight chunks of 512 queries over 0.5-4.6K keys, 32 heads (18,900 steps, 65 GFLOP):
+// Eight chunks of 512 queries over 0.5-4.6K keys, 32 heads (15,600 steps, 65 GFLOP):
 // one thread a key, log-sum-exps gathered by the producer 85 us; producer a step
 // ahead 85 us; log-sum-exps by bulk copy, 64 columns a thread 78 us; two groups on
 // alternate steps 71 us (0.92 PFLOP/s).  What is left is latency: a Q tile arrives
