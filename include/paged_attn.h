@@ -408,8 +408,8 @@ size_t pa_mass_workspace_bytes(const pa_plan *plan, int32_t num_heads, int32_t n
  * graph replays) still gets its output, but adds nothing to the totals and sets
  * PA_DEVICE_RANGE.  A captured call stays valid for plan images with the same
  * counts whose sequences have one decode item each (or several, when captured so)
- * and share no pages.  splits in 1..PA_MAX_SPLITS; other arguments, shapes and
- * checks as paged_attn_forward.
+ * and share no pages.  Histories hold at most 2^30 keys (PA_ERR_LIMIT).  splits in
+ * 1..PA_MAX_SPLITS; other arguments, shapes and checks as paged_attn_forward.
  */
 pa_status paged_attn_forward_mass(const pa_plan *plan, const void *q, const void *k_cache, const void *v_cache, void *out,
                                   float *key_mass, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,

@@ -75,6 +75,7 @@ struct Smem {
     uint64_t q_full[kStages], q_empty[kStages];
     uint64_t s_full[kStages], s_empty[kStages];
     uint64_t d_full[kSlots], d_empty[kSlots];
+    uint64_t part_full[2], part_empty[2];
     uint32_t tmem_base;
 };
 
@@ -120,6 +121,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&s.d_full[i], 1);
             mbar_init(&s.d_empty[i], kAdders + 1);      // the adding warps and the MMA issuer
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.part_full[i], 128);
+            mbar_init(&s.part_empty[i], 128);
         }
         fence_mbar_init();
     }
@@ -307,19 +312,28 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int j = what.w + row;                // my key
             if (what.x == kUnitEnd) {
                 const Step st = s.step[sl];
-                // the groups meet; a slot of `part` is written again two units on, past the
-                // next unit's barrier, which the first group joins after it has read
-                if (group == 1) s.part[unit & 1][row] = total;
-                asm volatile("bar.sync 1, 256;\n" ::: "memory");
+                // the second group hands its sums to the first (bounded waits: a named
+                // barrier would hold the others if one warp had given up)
+                const int slot = unit & 1;
+                if (group == 1) {
+                    if (unit >= 2)
+                        ok = __all_sync(0xffffffffu, mbar_wait(&s.part_empty[slot], (uint32_t)((unit / 2 - 1) & 1)));
+                    if (!ok) break;
+                    s.part[slot][row] = total;
+                    mbar_arrive(&s.part_full[slot]);
+                } else {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&s.part_full[slot], (uint32_t)((unit / 2) & 1)));
+                    if (!ok) break;
+                    total += s.part[slot][row];
+                    mbar_arrive(&s.part_empty[slot]);
+                }
+                __syncwarp();
                 if (lane == 0) mbar_arrive(&s.d_empty[sl]);
-                if (group == 0) {
-                    total += s.part[unit & 1][row];
-                    if (j < st.seq_len && !(total == 0.f)) {
-                        const int32_t *trow = reinterpret_cast<const int32_t *>((uint64_t)(uint32_t)st.trow_lo |
-                                                                                ((uint64_t)(uint32_t)st.trow_hi << 32));
-                        const int64_t page = trow[j / ps];
-                        prm.key_mass[(page * prm.hkv + st.kvh) * ps + j % ps] += total;
-                    }
+                if (group == 0 && j < st.seq_len && !(total == 0.f)) {
+                    const int32_t *trow = reinterpret_cast<const int32_t *>((uint64_t)(uint32_t)st.trow_lo |
+                                                                            ((uint64_t)(uint32_t)st.trow_hi << 32));
+                    const int64_t page = trow[j / ps];
+                    prm.key_mass[(page * prm.hkv + st.kvh) * ps + j % ps] += total;
                 }
                 total = 0.f;
                 ++unit;

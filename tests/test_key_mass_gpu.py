@@ -268,6 +268,33 @@ def test_captured_decode_loop(cuda_device):
     assert torch.equal(mass[4:], total[4:]) and not torch.equal(mass[:4], total[:4])
 
 
+def test_two_streams_at_once(cuda_device):
+    """Calls on two streams with a workspace and totals each, on one plan and cache: the bits of calls in turn."""
+    lens = [700, 350, 300]
+    queries = [(0, i) for i in range(300, 700)] + [(1, 349), (2, 298), (2, 299)]
+    case = build_case("mass", 12, lens, queries, 8, 2, 128, 128, 16, BF, 0.088)
+    dc, plan = case.to("cuda"), plan_for(case)
+    pka.paged_kv_store(plan, dc.new_k, dc.new_v, dc.k_cache, dc.v_cache)
+    call = lambda m, ws: pka.paged_attn_forward_mass(plan, dc.q, dc.k_cache, dc.v_cache, m, case.scale, splits=2,   # noqa: E731
+                                                     workspace=ws)
+    new = lambda: (torch.zeros(case.num_pages, 2, 16, device="cuda"), pka.make_mass_workspace(plan, 8, 2, 128, 2))   # noqa: E731
+    want, (m0, ws) = None, new()
+    for _ in range(3):
+        want = call(m0, ws)
+    torch.cuda.synchronize()
+    both = [(torch.cuda.Stream(), *new()) for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [None, None]
+    for _ in range(3):
+        for i, (st, m, w) in enumerate(both):
+            with torch.cuda.stream(st):
+                outs[i] = call(m, w)
+    torch.cuda.synchronize()
+    assert pka.device_status() == 0
+    for i, (_, m, _) in enumerate(both):
+        assert torch.equal(outs[i], want) and torch.equal(m, m0)
+
+
 def test_refusals(cuda_device):
     case = decode_case(4, 2, 64, 64, 16, BF, lens=(20, 20))
     dc, plan = case.to("cuda"), plan_for(case)
