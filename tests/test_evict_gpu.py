@@ -138,6 +138,38 @@ def test_shared_prefix_inside_the_sink(cuda_device):
     assert e.value.status == 5
 
 
+def test_pages_partly_in_place(cuda_device):
+    """Each kept page is the source's own or a fresh one, entry by entry; a third sequence only moves house."""
+    ps, hkv, d = 16, 2, 64
+    lens, kept_lens = [100, 64, 40], [50, 40, 40]
+    src = np.array([[0, 1, 2, 3, 4, 5, 6], [7, 8, 9, 10, -1, -1, -1], [11, 12, 13, -1, -1, -1, -1]])
+    dst = np.array([[0, 20, 2, 21], [22, 8, 9, -1], [23, 24, 25, -1]])
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    k = torch.randn(26, ps, hkv, d, generator=gen, device="cuda").half()
+    v, mass = torch.randn_like(k), torch.rand(26, hkv, ps, generator=gen, device="cuda")
+    plan = pka.paged_attn_plan(lens, src, [], [], ps, 26, device="cuda")
+    kept_plan = pka.paged_attn_plan(kept_lens, dst, [], [], ps, 26, device="cuda")
+    rows = lambda t: t.view(-1, hkv, d)                                     # noqa: E731
+    want_k, want_v = rows(k.clone()), rows(v.clone())
+    host = mass.cpu().numpy().transpose(0, 2, 1).reshape(-1, hkv)
+    want_m = host.copy()
+    ids = [[kept_keys(host[slots(src, ps, s, n), h], m, 3, 9) for h in range(hkv)]
+           for s, (n, m) in enumerate(zip(lens, kept_lens))]
+    for s, (n, m) in enumerate(zip(lens, kept_lens)):
+        for h in range(hkv):
+            at, to = slots(src, ps, s, n)[ids[s][h]], slots(dst, ps, s, m)
+            want_k[torch.from_numpy(to).cuda(), h] = rows(k)[torch.from_numpy(at).cuda(), h]
+            want_v[torch.from_numpy(to).cuda(), h] = rows(v)[torch.from_numpy(at).cuda(), h]
+            want_m[to, h] = host[at, h]
+    kept = pka.paged_kv_evict(plan, kept_plan, mass, k, v, sink=3, recent=9).cpu().numpy()
+    assert pka.device_status() == 0
+    for s in range(3):
+        for h in range(hkv):
+            assert np.array_equal(kept[s, h, :kept_lens[s]], ids[s][h])
+    assert torch.equal(bits(rows(k)), bits(want_k)) and torch.equal(bits(rows(v)), bits(want_v))
+    assert np.array_equal(mass.cpu().numpy().transpose(0, 2, 1).reshape(-1, hkv), want_m)
+
+
 def test_source_advanced_on_the_device(cuda_device):
     """Lengths are the device copy's: a plan advanced by graph replays is evicted at its true length."""
     ps, hkv, d = 16, 1, 16

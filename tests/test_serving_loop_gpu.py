@@ -116,3 +116,34 @@ def test_loop(cuda_device, dt, in_place):
 def kept_plan_table(pages):
     w = max(map(len, pages))
     return np.array([p + [-1] * (w - len(p)) for p in pages])
+
+
+def test_offsets_past_32_bits(cuda_device):
+    """The same step on a pool of 12 pages and on the last pages of one with 4.6 G elements a cache: the same bits."""
+    hq, hkv, d, ps, dt = 8, 8, 256, 16, torch.bfloat16
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=dt)        # noqa: E731
+    k0, v0, m0 = rnd(12, ps, hkv, d), rnd(12, ps, hkv, d), torch.rand(12, hkv, ps, generator=gen, device="cuda")
+    q, nk, nv, w = rnd(3, hq, d), rnd(3, hkv, d), rnd(3, hkv, d), rnd(d)
+    table = torch.rand(200, 128, generator=gen, device="cuda")
+    lens, rows = [100, 50], np.array([[0, 1, 2, 3, 4, 5, 6], [7, 8, 9, 10, -1, -1, -1]])
+
+    def step(pool, first):
+        k, v = torch.empty(pool, ps, hkv, d, dtype=dt, device="cuda"), torch.empty(pool, ps, hkv, d, dtype=dt, device="cuda")
+        mass = torch.empty(pool, hkv, ps, device="cuda")
+        here = slice(first, first + 12)
+        k[here], v[here], mass[here] = k0, v0, m0
+        bt = np.where(rows >= 0, rows + first, -1)
+        plan = pka.paged_attn_plan(lens, bt, [0, 0, 1], [98, 99, 49], ps, pool, device="cuda")
+        kept_plan = pka.paged_attn_plan([40, 20], bt, [], [], ps, pool, device="cuda")
+        got = [pka.paged_qk_norm_rope_store(plan, q, nk, nv, k, v, rope_table=table, q_weight=w, k_weight=w, key_mass=mass)]
+        got.append(pka.paged_attn_forward_mass(plan, got[0], k, v, mass, d ** -0.5, splits=2))
+        got.append(mass[here].clone())
+        got.append(pka.paged_kv_evict(plan, kept_plan, mass, k, v, sink=2, recent=4))
+        torch.cuda.synchronize()
+        assert pka.device_status() == 0
+        return got + [k[here].clone(), v[here].clone(), mass[here].clone()]
+
+    small, large = step(12, 0), step(140_012, 140_000)
+    for a, b in zip(small, large):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
