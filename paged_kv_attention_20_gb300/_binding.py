@@ -129,9 +129,13 @@ def _i32_array(a) -> np.ndarray:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+def _current_stream(index: int) -> int:
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _stream(device) -> int:
-    if _raw_stream is not None and device.index is not None:
-        return _raw_stream(device.index)
+    if device.index is not None:
+        return _current_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -145,6 +149,7 @@ class Plan:
         self.longest = 0    # keys of the longest sequence the plan was built with
         self.words = None
         self.device = None
+        self._index = -1    # CUDA index of the device copy, -1 before the upload
 
     @property
     def handle(self) -> ctypes.c_void_p:
@@ -159,6 +164,7 @@ class Plan:
         n = self.device_bytes()
         self.words = torch.empty(max(16, n), dtype=torch.uint8, device=device)
         self.device = self.words.device
+        self._index = self.words.get_device()
         _check(load().pa_plan_upload(self._handle, self.words.data_ptr(), self.words.numel(),
                                      _stream(self.device)))
         return self
@@ -167,6 +173,7 @@ class Plan:
         """Upload into a caller-provided device byte buffer (reused across steps)."""
         self.words = words
         self.device = words.device
+        self._index = words.get_device()
         _check(load().pa_plan_upload(self._handle, words.data_ptr(), words.numel(), _stream(words.device)))
         return self
 
@@ -184,6 +191,7 @@ class Plan:
                                     device_words.data_ptr(), device_words.numel()))
         self.words = device_words
         self.device = device_words.device
+        self._index = device_words.get_device()
         return self
 
     def __del__(self):
@@ -394,49 +402,49 @@ def paged_mla_forward(plan: Plan, q, qp, latent_cache, pos_cache, scale: float, 
     return out
 
 
-def _dense(t, name: str, dtype, device, index: int, rank: int):
-    """Shape of a dense operand.  The common case costs four attribute reads; anything else gets its message."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous()):
-        _tensor(t, name, dtype, device, rank)
-    shape = t.shape
-    if len(shape) != rank:
-        raise ValueError(f"{name} must have rank {rank}")
-    return shape
+def _dense(t, name: str, dtype, index: int, rank: int):
+    """Shape of a dense operand on CUDA device `index` (-1: the host)."""
+    try:
+        if t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+            shape = t.shape
+            if len(shape) == rank:
+                return shape
+    except AttributeError:
+        pass
+    _tensor(t, name, dtype, torch.device("cuda", index) if index >= 0 else torch.device("cpu"), rank)
+    return t.shape
 
 
-def _cuda_index(device) -> int:
-    return device.index if device.type == "cuda" else -1
-
-
-def _key_mass(t, pages: int, heads: int, page_size: int, device, index: int) -> None:
-    if _dense(t, "key_mass", torch.float32, device, index, 3) != (pages, heads, page_size):
+def _key_mass(t, pages: int, heads: int, page_size: int, index: int) -> None:
+    if _dense(t, "key_mass", torch.float32, index, 3) != (pages, heads, page_size):
         raise ValueError("key_mass must be [pages, kv_heads, page_size]")
 
 
 def _caches(plan: Plan, k_cache, v_cache):
-    """Checks of a K/V cache pair against the plan; (dtype, device, device index, K shape, value dim)."""
+    """Checks of a K/V cache pair against the plan; (dtype, its code, device index, K shape, value dim)."""
     if not isinstance(k_cache, torch.Tensor):
         raise TypeError("k_cache must be a torch.Tensor")
-    dev, dt = k_cache.device, k_cache.dtype
-    if dt not in _DTYPES:
+    dt, index = k_cache.dtype, k_cache.get_device()
+    code = _DTYPES.get(dt)
+    if code is None:
         raise TypeError("dtype must be float32, float16 or bfloat16")
-    index = _cuda_index(dev)
-    shape = _dense(k_cache, "k_cache", dt, dev, index, 4)
-    pages, ps, hkv, dv = _dense(v_cache, "v_cache", dt, dev, index, 4)
-    _plan_ready(plan, dev)
+    shape = _dense(k_cache, "k_cache", dt, index, 4)
+    pages, ps, hkv, dv = _dense(v_cache, "v_cache", dt, index, 4)
+    if plan._index != index or index < 0:
+        _plan_ready(plan, k_cache.device)
     if shape[0] != pages or shape[1] != ps or shape[2] != hkv or pages != plan.pages or ps != plan.page_size:
         raise ValueError("cache shapes do not match the plan")
-    return dt, dev, index, shape, dv
+    return dt, code, index, shape, dv
 
 
-def _rows(t, name: str, dtype, device, index: int, queries: int, dim: int):
+def _rows(t, name: str, dtype, index: int, queries: int, dim: int):
     """A [queries, heads, dim] operand whose rows may lie apart; returns (heads, row stride in elements)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+        raise ValueError(f"{name} is on {t.device}, expected CUDA device {index}")
     shape = t.shape
     if len(shape) != 3:
         raise ValueError(f"{name} must have rank 3")
@@ -458,44 +466,44 @@ def paged_qk_norm_rope_store(plan: Plan, q, new_k, new_v, k_cache, v_cache, rope
     fp32 [max_positions, rope_dim], cosines then sines; `positions` (int32 [Q]) replaces the plan's positions for
     the rotation; key_mass, when given, is zeroed at the written keys.  Returns the queries, dense (`q_out` may be
     a dense q itself)."""
-    dt, dev, index, (pages, ps, hkv, d), dv = _caches(plan, k_cache, v_cache)
+    dt, code, index, (pages, ps, hkv, d), dv = _caches(plan, k_cache, v_cache)
     n = plan.queries
-    hq, q_stride = _rows(q, "q", dt, dev, index, n, d)
-    hk, k_stride = _rows(new_k, "new_k", dt, dev, index, n, d)
-    hv, v_stride = _rows(new_v, "new_v", dt, dev, index, n, dv)
+    hq, q_stride = _rows(q, "q", dt, index, n, d)
+    hk, k_stride = _rows(new_k, "new_k", dt, index, n, d)
+    hv, v_stride = _rows(new_v, "new_v", dt, index, n, dv)
     if hk != hkv or hv != hkv:
         raise ValueError("new rows must be [queries, kv_heads, d|dv]")
     table_ptr = pos_ptr = mass_ptr = qw_ptr = kw_ptr = None
     far = rot = 0
     if rope_table is not None:
-        far, rot = _dense(rope_table, "rope_table", torch.float32, dev, index, 2)
+        far, rot = _dense(rope_table, "rope_table", torch.float32, index, 2)
         if far == 0 or rot == 0:        # an empty tensor's null pointer would read as "no table"
             raise ValueError("the rope table is empty")
         table_ptr = rope_table.data_ptr()
     if positions is not None:
-        if _dense(positions, "positions", torch.int32, dev, index, 1)[0] != n:
+        if _dense(positions, "positions", torch.int32, index, 1)[0] != n:
             raise ValueError("positions must be [queries]")
         pos_ptr = positions.data_ptr()
     if q_weight is not None:
-        if _dense(q_weight, "q_weight", dt, dev, index, 1)[0] != d:
+        if _dense(q_weight, "q_weight", dt, index, 1)[0] != d:
             raise ValueError("norm weights must be [head_dim]")
         qw_ptr = q_weight.data_ptr()
     if k_weight is not None:
-        if _dense(k_weight, "k_weight", dt, dev, index, 1)[0] != d:
+        if _dense(k_weight, "k_weight", dt, index, 1)[0] != d:
             raise ValueError("norm weights must be [head_dim]")
         kw_ptr = k_weight.data_ptr()
     if key_mass is not None:
-        _key_mass(key_mass, pages, hkv, ps, dev, index)
+        _key_mass(key_mass, pages, hkv, ps, index)
         mass_ptr = key_mass.data_ptr()
     if q_out is None:
-        q_out = torch.empty((n, hq, d), dtype=dt, device=dev)
-    elif _dense(q_out, "q_out", dt, dev, index, 3) != (n, hq, d):
+        q_out = torch.empty((n, hq, d), dtype=dt, device=k_cache.device)
+    elif _dense(q_out, "q_out", dt, index, 3) != (n, hq, d):
         raise ValueError(f"q_out must have shape {(n, hq, d)}")
     lib = _LIB or load()
     status = lib.paged_qk_norm_rope_store(
         plan._handle, q.data_ptr(), q_stride, new_k.data_ptr(), k_stride, new_v.data_ptr(), v_stride, q_out.data_ptr(),
         k_cache.data_ptr(), v_cache.data_ptr(), mass_ptr, table_ptr, far, rot, 1 if interleaved else 0, pos_ptr, qw_ptr,
-        kw_ptr, eps, hq, hkv, d, dv, _DTYPES[dt], _stream(dev))
+        kw_ptr, eps, hq, hkv, d, dv, code, _current_stream(index))
     if status:
         _check(status)
     return q_out
@@ -520,25 +528,25 @@ def paged_attn_forward_mass(plan: Plan, q, k_cache, v_cache, key_mass, scale: fl
     """Paged attention that adds each key's softmax weights, over the plan's queries and a KV head's query heads, to
     key_mass [pages, kv_heads, page_size] (fp32).  splits defaults to the split heuristic; the workspace is allocated
     here when not given (make_mass_workspace)."""
-    dt, dev, index, (pages, ps, hkv, d), dv = _caches(plan, k_cache, v_cache)
-    n, hq, dq = _dense(q, "q", dt, dev, index, 3)
+    dt, code, index, (pages, ps, hkv, d), dv = _caches(plan, k_cache, v_cache)
+    n, hq, dq = _dense(q, "q", dt, index, 3)
     if n != plan.queries or dq != d:
         raise ValueError("q must be [queries, num_heads, head_dim] matching the plan and cache")
     if out is None:
-        out = torch.empty((n, hq, dv), dtype=dt, device=dev)
-    elif _dense(out, "out", dt, dev, index, 3) != (n, hq, dv):
+        out = torch.empty((n, hq, dv), dtype=dt, device=k_cache.device)
+    elif _dense(out, "out", dt, index, 3) != (n, hq, dv):
         raise ValueError(f"out must have shape {(n, hq, dv)}")
-    _key_mass(key_mass, pages, hkv, ps, dev, index)
+    _key_mass(key_mass, pages, hkv, ps, index)
     if splits is None:
         splits = paged_attn_split_heuristic(plan, hq, hkv, window=window)
     if workspace is None:
-        workspace = make_mass_workspace(plan, hq, hkv, dv, splits, window if causal else 0, device=dev)
+        workspace = make_mass_workspace(plan, hq, hkv, dv, splits, window if causal else 0, device=k_cache.device)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     lib = _LIB or load()
     status = lib.paged_attn_forward_mass(
         plan._handle, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), key_mass.data_ptr(), hq, hkv, d,
-        dv, scale, 1 if causal else 0, window, _DTYPES[dt], workspace.data_ptr(), workspace.nbytes, splits, _stream(dev))
+        dv, scale, 1 if causal else 0, window, code, workspace.data_ptr(), workspace.nbytes, splits, _current_stream(index))
     if status:
         _check(status)
     return out
@@ -548,19 +556,20 @@ def paged_kv_evict(plan: Plan, kept_plan: Plan, key_mass, k_cache, v_cache, sink
     """Shrink every sequence of `plan` to its length in `kept_plan`: the first `sink`, the last `recent` and, between
     them, the keys with the largest key_mass stay and move to the kept schedule's rows.  Returns the kept keys' former
     indices, int32 [sequences, kv_heads, longest kept history], -1 past a sequence's kept length."""
-    dt, dev, index, (pages, ps, hkv, d), dv = _caches(plan, k_cache, v_cache)
-    _plan_ready(kept_plan, dev)
-    _key_mass(key_mass, pages, hkv, ps, dev, index)
+    dt, code, index, (pages, ps, hkv, d), dv = _caches(plan, k_cache, v_cache)
+    if kept_plan._index != index:
+        _plan_ready(kept_plan, k_cache.device)
+    _key_mass(key_mass, pages, hkv, ps, index)
     if kept is None:
-        kept = torch.empty((plan.sequences, hkv, kept_plan.longest), dtype=torch.int32, device=dev)
+        kept = torch.empty((plan.sequences, hkv, kept_plan.longest), dtype=torch.int32, device=k_cache.device)
         stride = kept_plan.longest
     else:
-        sequences, heads, stride = _dense(kept, "kept", torch.int32, dev, index, 3)
+        sequences, heads, stride = _dense(kept, "kept", torch.int32, index, 3)
         if sequences != plan.sequences or heads != hkv:
             raise ValueError("kept must be [sequences, kv_heads, n]")
     lib = _LIB or load()
     status = lib.paged_kv_evict(plan._handle, kept_plan._handle, key_mass.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                kept.data_ptr(), stride, sink, recent, hkv, d, dv, _DTYPES[dt], _stream(dev))
+                                kept.data_ptr(), stride, sink, recent, hkv, d, dv, code, _current_stream(index))
     if status:
         _check(status)
     return kept
