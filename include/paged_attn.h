@@ -384,8 +384,8 @@ pa_status paged_qk_norm_rope_store(const pa_plan *plan, const void *q, int64_t q
  * Workspace bytes for paged_attn_forward_mass: the split partials and
  * log-sum-exp values, the score rows of the decode items (fp32 [decode items,
  * num_heads, keys]) and the work lists.  `keys` is the longest history of the
- * plan's decode items, or max_keys when that is more, at most `window` when
- * window > 0 (pass 0 for a call that is not causal).  A larger max_keys lets a
+ * plan's decode items, or max_keys when that is more, at most `window` + 3
+ * when window > 0 (pass 0 for a call that is not causal).  A larger max_keys lets a
  * captured decode loop (pa_plan_advance, staged plans) grow past the histories
  * it was captured with.  0 for invalid arguments.
  */

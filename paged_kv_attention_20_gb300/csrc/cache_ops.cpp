@@ -61,7 +61,7 @@ MassLayout mass_layout(const pa_plan *plan, int32_t hq, int32_t dv, int32_t spli
     l.tile_lse = l.blocks + (plan->n_tiles > 0 ? align256(((size_t)blocks + 1) * sizeof(int4)) : 0);
     l.scores = l.tile_lse + align256((size_t)plan->n_tiles * hq * 128 * sizeof(float));
     int64_t keys = std::max<int64_t>(max_keys, plan->max_seq_len);
-    if (window > 0) keys = std::min<int64_t>(keys, window);
+    if (window > 0 && keys > window) keys = (int64_t)window + 3;      // a row starts up to three keys early
     l.cap = plan->n_decode > 0 ? (keys + 31) / 32 * 32 : 0;
     l.bytes = l.scores + align256((size_t)plan->n_decode * hq * (size_t)l.cap * sizeof(float));
     return l;

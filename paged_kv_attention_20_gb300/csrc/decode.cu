@@ -259,8 +259,8 @@ __global__ void __launch_bounds__(128) decode_fast_kernel(AttnArgs a, int use_li
         // Online softmax update, one warp per head.
         for (int g = warp; g < GH; g += 4) {
             const float s = lane < C::TK ? sp[lane * GH + g] : -INFINITY;
-            if (a.scores && lane < C::TK && tb + lane < j1 && tb + lane - lo < a.score_cap)
-                a.scores[((int64_t)item * a.hq + h0 + g) * a.score_cap + (tb + lane - lo)] = s;
+            if (a.scores && lane < C::TK && tb + lane < j1 && tb + lane - score_origin(lo) < a.score_cap)
+                a.scores[((int64_t)item * a.hq + h0 + g) * a.score_cap + (tb + lane - score_origin(lo))] = s;
             float mt = s;
 #pragma unroll
             for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
@@ -432,8 +432,8 @@ __global__ void __launch_bounds__(128) decode_generic_kernel(AttnArgs a, int use
                 for (int e = 0; e < a.p; ++e) dot = fmaf(qpf[e], to_f<T>(kpr[e]), dot);
             }
             s = dot;
-            if (a.scores && j - lo < a.score_cap)
-                a.scores[((int64_t)item * a.hq + h) * a.score_cap + (j - lo)] = s;
+            if (a.scores && j - score_origin(lo) < a.score_cap)
+                a.scores[((int64_t)item * a.hq + h) * a.score_cap + (j - score_origin(lo))] = s;
         }
         const float mt = block_max128(s, scratch);
         const float nm = fmaxf(m, mt);

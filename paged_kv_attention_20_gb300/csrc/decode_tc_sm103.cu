@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 if constexpr (kMass) {
                     // my columns of the head's score row: whole 16-byte pieces where the
                     // tile is whole and the row's offset allows
-                    const int64_t at = kbase + c0 - x.lo;
+                    const int64_t at = kbase + c0 - score_origin(x.lo);
                     if (a.scores && h < G) {
                         float *dst = a.scores + ((int64_t)x.item * a.hq + (int64_t)x.kvh * G + h) * a.score_cap + at;
                         if (valid == kN && first == 0 && (at & 3) == 0 && at + CW <= a.score_cap) {

@@ -266,8 +266,8 @@ __global__ void __launch_bounds__(128) decode_tma_kernel(const __grid_constant__
             const bool vis = gv && t16 < valid && t16 >= first;
             const float s = vis ? sp[2 * C::TT * GH + t16 * GH + g] : -INFINITY;
             if constexpr (kMass) {
-                if (a.scores && vis && jt + t16 - lo < a.score_cap)
-                    a.scores[((int64_t)item * a.hq + h0 + g) * a.score_cap + (jt + t16 - lo)] = s;
+                if (a.scores && vis && jt + t16 - score_origin(lo) < a.score_cap)
+                    a.scores[((int64_t)item * a.hq + h0 + g) * a.score_cap + (jt + t16 - score_origin(lo))] = s;
             }
             float alpha = 1.f;
             if (__any_sync(0xffffffffu, s > m_ref[k] + kSlack)) {

@@ -225,12 +225,48 @@ constexpr int kItemKeys = 4 * kItemThreads;     // four keys a thread and step
 constexpr int kHeadsAtOnce = 4;                 // score rows in flight
 constexpr int kMaxStagedHeads = 64;
 
+// A quad at the ends of the visible range loads its four scores all the same
+// (score_origin keeps them inside the row; entries no key has may hold anything and are
+// not added) and its totals before any is written: an end costs no chain of loads
+// (24 sequences of four drafted tokens, window 1000: the pass 14.8 us, so 12.4, and
+// 10.8 with as many blocks as the window touches).
+template <bool kQuads>
+__device__ __forceinline__ void add_to_part(const MassArgs &a, const int32_t *trow, int kvh, int ps_shift, int j, int in,
+                                            const float (&p)[4]) {
+    const int ps = a.plan.page_size;
+    if constexpr (kQuads) {
+        const int pg = ps_shift >= 0 ? j >> ps_shift : j / ps;
+        float *at = a.key_mass + ((int64_t)trow[pg] * a.hkv + kvh) * ps + (j - pg * ps), old[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) old[k] = in >> k & 1 ? at[k] : 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (in >> k & 1) at[k] = old[k] + p[k];
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (in >> k & 1) {
+                const int pg = (j + k) / ps;
+                a.key_mass[((int64_t)trow[pg] * a.hkv + kvh) * ps + (j + k - pg * ps)] += p[k];
+            }
+    }
+}
+
+// The keys of [lo, hi) among j .. j + 3, a bit each.
+__device__ __forceinline__ int quad_mask(int j, int lo, int hi) {
+    const int below = min(max(lo - j, 0), 4), past = min(max(j + 4 - hi, 0), 4);
+    return (15 << below) & (15 >> past);
+}
+
 // Sequences of one item: a CTA per (item, KV head, block of keys), four consecutive
 // keys per thread and step, the group's heads in turn.  The scores come from L2 when
 // they fit there (4 bytes a key and head), the totals are read and written once.
 // The pass is latency-bound (metadata, then scores, table and log-sum-exps, then
 // the totals): the first step's scores are asked for before the log-sum-exps are
 // merged.
+// Four CTAs of 64 registers an SM, or three of 80 where the merge rides along: four
+// histories of 32-128K keys at G = 8 take 254 us a call so and 260 at four, 64 of
+// 0.5-8K at G = 4 the same 215; without the merge 18 us at four and 23 at three.
 // kQuads: pages hold whole aligned fours of keys and the totals are 16-byte
 // aligned.
 template <bool kQuads>
@@ -252,7 +288,8 @@ __device__ __forceinline__ void add_item(const MassArgs &a, int blocks, int ps_s
     int64_t lo64, hi64;
     visible_range(meta.y, a.causal ? 0 : a.plan.seq_lens[meta.x], a.causal, a.window, lo64, hi64);
     const int lo = (int)lo64, hi = (int)hi64;       // positions fit 32 bits
-    if (hi - lo > a.cap || hi > (1 << 30)) {
+    const int origin = (int)score_origin(lo);
+    if (hi - origin > a.cap || hi > (1 << 30)) {
         // the workspace holds no scores past cap: this item adds nothing (nor does
         // one whose steps could leave 32 bits)
         if (threadIdx.x == 0) atomicCAS(a.status, 0, PA_DEVICE_RANGE);
@@ -262,18 +299,17 @@ __device__ __forceinline__ void add_item(const MassArgs &a, int blocks, int ps_s
     const int start = lo / step * step + blk * kItemKeys;
     if (start >= hi || (start + kItemKeys <= lo && start + step >= hi)) return;   // nothing here (uniform)
     const int32_t *trow = a.plan.table + (int64_t)meta.x * a.plan.width;
-    const bool aligned = (lo & 3) == 0;
     for (int g0 = 0; g0 < G; g0 += kMaxStagedHeads) {
         const int gn = min(G - g0, kMaxStagedHeads);
-        const float *head0 = a.scores + ((int64_t)item * a.hq + kvh * G + g0) * a.cap - lo;
+        const float *head0 = a.scores + ((int64_t)item * a.hq + kvh * G + g0) * a.cap - origin;
         float4 early[kHeadsAtOnce];
         int page = 0;
         auto ask = [&](int j) {                     // the page and the first heads' scores of four keys
-            if (j >= lo && j + 4 <= hi) {
+            if (j + 4 > lo && j < hi) {
                 if (kQuads) page = trow[ps_shift >= 0 ? j >> ps_shift : j / ps];
 #pragma unroll
                 for (int g = 0; g < kHeadsAtOnce; ++g)
-                    if (aligned && g < gn) early[g] = *reinterpret_cast<const float4 *>(head0 + j + g * a.cap);
+                    if (g < gn) early[g] = *reinterpret_cast<const float4 *>(head0 + j + g * a.cap);
             }
         };
         int j = start + 4 * (int)threadIdx.x;
@@ -306,38 +342,25 @@ __device__ __forceinline__ void add_item(const MassArgs &a, int blocks, int ps_s
                 old = *m;
             }
             float p[4] = {0.f, 0.f, 0.f, 0.f};
-            if (all && aligned) {
 #pragma unroll
-                for (int g = 0; g < kHeadsAtOnce; ++g)
-                    if (g < gn) {
-                        const float4 v = early[g];
-                        const float l = lse[g];
-                        p[0] += exp2f(v.x - l); p[1] += exp2f(v.y - l); p[2] += exp2f(v.z - l); p[3] += exp2f(v.w - l);
-                    }
-                ask(j + step);
-#pragma unroll 4
-                for (int g = kHeadsAtOnce; g < gn; ++g) {
-                    const float4 v = *reinterpret_cast<const float4 *>(sc + g * a.cap);
+            for (int g = 0; g < kHeadsAtOnce; ++g)
+                if (g < gn) {
+                    const float4 v = early[g];
                     const float l = lse[g];
                     p[0] += exp2f(v.x - l); p[1] += exp2f(v.y - l); p[2] += exp2f(v.z - l); p[3] += exp2f(v.w - l);
                 }
-            } else {
-                ask(j + step);
-                for (int g = 0; g < gn; ++g)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (j + i >= lo && j + i < hi) p[i] += exp2f(sc[g * a.cap + i] - lse[g]);
+            ask(j + step);
+#pragma unroll 4
+            for (int g = kHeadsAtOnce; g < gn; ++g) {
+                const float4 v = *reinterpret_cast<const float4 *>(sc + g * a.cap);
+                const float l = lse[g];
+                p[0] += exp2f(v.x - l); p[1] += exp2f(v.y - l); p[2] += exp2f(v.z - l); p[3] += exp2f(v.w - l);
             }
             if (kQuads && all) {
                 old.x += p[0]; old.y += p[1]; old.z += p[2]; old.w += p[3];
                 *m = old;
             } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (j + i >= lo && j + i < hi) {
-                        const int pg = (j + i) / ps;
-                        a.key_mass[((int64_t)trow[pg] * a.hkv + kvh) * ps + (j + i - pg * ps)] += p[i];
-                    }
+                add_to_part<kQuads>(a, trow, kvh, ps_shift, j, quad_mask(j, lo, hi), p);
             }
         }
     }
@@ -373,7 +396,7 @@ __device__ __forceinline__ void add_repeated(const MassArgs &a, int grouped, int
     auto stage = [&](int at, int item, int pos) {
         int64_t lo, hi;
         visible_range(pos, seq_len, a.causal, a.window, lo, hi);
-        if (hi - lo > a.cap || hi > (1 << 30)) {
+        if (hi - score_origin(lo) > a.cap || hi > (1 << 30)) {
             atomicCAS(a.status, 0, PA_DEVICE_RANGE);    // no scores past cap: adds nothing
             lo = hi = 0;
         }
@@ -437,49 +460,33 @@ __device__ __forceinline__ void add_repeated(const MassArgs &a, int grouped, int
                 __syncthreads();
                 for (int j = start + 4 * tid; j < hi_all; j += step) {
                     float p[4] = {0.f, 0.f, 0.f, 0.f};
-                    bool any[4] = {false, false, false, false};
+                    int any = 0;
 #pragma unroll 2
                     for (int i = 0; i < items; ++i) {
                         const int lo = sh.lo[e0 + i], hi = sh.hi[e0 + i];
                         if (j + 4 <= lo || j >= hi) continue;
-                        const float *sc = a.scores + ((int64_t)sh.item[e0 + i] * a.hq + kvh * G + g0) * a.cap + (j - lo);
-                        if (j >= lo && j + 4 <= hi) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) any[k] = true;
-                            const bool aligned = (lo & 3) == 0;
+                        const float *sc = a.scores + ((int64_t)sh.item[e0 + i] * a.hq + kvh * G + g0) * a.cap + (j - (int)score_origin(lo));
+                        const int in = quad_mask(j, lo, hi);
+                        float w[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-                            for (int g = 0; g < gn; ++g) {
-                                float4 v;
-                                if (aligned)
-                                    v = *reinterpret_cast<const float4 *>(sc + g * a.cap);
-                                else
-                                    v = make_float4(sc[g * a.cap], sc[g * a.cap + 1], sc[g * a.cap + 2], sc[g * a.cap + 3]);
-                                const float l = sh.lse[i][g];
-                                p[0] += exp2f(v.x - l); p[1] += exp2f(v.y - l); p[2] += exp2f(v.z - l); p[3] += exp2f(v.w - l);
-                            }
-                        } else {
-                            for (int g = 0; g < gn; ++g)
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    if (j + k >= lo && j + k < hi) {
-                                        any[k] = true;
-                                        p[k] += exp2f(sc[g * a.cap + k] - sh.lse[i][g]);
-                                    }
+                        for (int g = 0; g < gn; ++g) {
+                            const float4 v = *reinterpret_cast<const float4 *>(sc + g * a.cap);
+                            const float l = sh.lse[i][g];
+                            w[0] += exp2f(v.x - l); w[1] += exp2f(v.y - l); w[2] += exp2f(v.z - l); w[3] += exp2f(v.w - l);
                         }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (in >> k & 1) p[k] += w[k];
+                        any |= in;
                     }
-                    if (kQuads && any[0] && any[1] && any[2] && any[3]) {
+                    if (kQuads && any == 15) {
                         const int pg = ps_shift >= 0 ? j >> ps_shift : j / ps;
                         float4 *m = reinterpret_cast<float4 *>(a.key_mass + ((int64_t)trow[pg] * a.hkv + kvh) * ps + (j - pg * ps));
                         float4 v = *m;
                         v.x += p[0]; v.y += p[1]; v.z += p[2]; v.w += p[3];
                         *m = v;
                     } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (any[k]) {
-                                const int pg = (j + k) / ps;
-                                a.key_mass[((int64_t)trow[pg] * a.hkv + kvh) * ps + (j + k - pg * ps)] += p[k];
-                            }
+                        add_to_part<kQuads>(a, trow, kvh, ps_shift, j, any, p);
                     }
                 }
             }
@@ -504,7 +511,7 @@ __global__ void __launch_bounds__(kItemThreads, 4) mass_items_kernel(MassArgs a,
 // The merge of the split outputs and the totals in one launch: both follow the
 // decode kernel and neither needs the other.  The first merge_blocks CTAs merge.
 template <typename T, int VEC, bool kQuads, bool kRepeated>
-__global__ void __launch_bounds__(kItemThreads, 4) merge_and_items_kernel(AttnArgs attn, MassArgs a, int use_list, int nrows,
+__global__ void __launch_bounds__(kItemThreads, 3) merge_and_items_kernel(AttnArgs attn, MassArgs a, int use_list, int nrows,
                                                                           int wide, int merge_blocks, int grouped, int blocks,
                                                                           int ps_shift) {
     griddep_wait();
@@ -634,9 +641,12 @@ bool mass_items_grouped(const MassArgs &a, bool repeated) { return repeated && a
 
 cudaError_t launch_mass_items(const MassArgs &a, bool repeated, const AttnArgs *merge, bool use_list, cudaStream_t st) {
     const int64_t units = (int64_t)(repeated ? a.plan.sequences : a.plan.n_decode) * a.hkv;
-    // blocks a unit: one per 1024 keys of the longest history, but no more than fill
-    // the GPU once (a CTA's start costs three dependent loads, its further keys one)
-    const int64_t most = ((int64_t)a.longest + kItemKeys - 1) / kItemKeys, fill = (152 * 4 + units - 1) / units;
+    // blocks a unit: one per 1024 keys of the longest history, or of what a window can
+    // touch, but no more than fill the GPU once (a CTA's start costs three dependent
+    // loads, its further keys one)
+    int64_t keys = a.longest;
+    if (a.causal && a.window > 0 && (int64_t)a.window + kItemKeys < keys) keys = (int64_t)a.window + kItemKeys;
+    const int64_t most = (keys + kItemKeys - 1) / kItemKeys, fill = (152 * 4 + units - 1) / units;
     const int blocks = blocks_for(units, most < fill ? most : fill);
     const int ps = a.plan.page_size;
     int shift = -1;

@@ -50,7 +50,7 @@ struct AttnArgs {
     pa_dtype dtype;
     int32_t *status;      // device status word (bounded waits record timeouts here)
     float *scores;        // per-key totals wanted: log2-domain scores [item, Hq, score_cap] (else null)
-    int64_t score_cap;    // keys a score row holds (key j of an item at j - lo)
+    int64_t score_cap;    // entries of a score row; key j of an item at j - score_origin(lo)
     int32_t max_ctas;     // persistent kernels: at most this many CTAs (0: as many as are resident at once)
 };
 
@@ -64,6 +64,10 @@ __host__ __device__ inline void visible_range(int pos, int seq_len, int causal, 
     lo = window > 0 ? (int64_t)pos - window + 1 : 0;
     if (lo < 0) lo = 0;
 }
+
+// The key a decode item's score row starts with: its first visible one, rounded
+// down so that fours of keys lie on 16-byte boundaries under any window.
+__host__ __device__ inline int64_t score_origin(int64_t lo) { return lo & ~(int64_t)3; }
 
 // Split s of `splits` over the visible keys [lo, hi): with base = lo rounded
 // down to a page boundary and chunk = ceil((hi - base) / splits) rounded up to

@@ -75,6 +75,8 @@ def test_mass_workspace_bytes(built_lib):
     assert pka.mass_workspace_bytes(p, 8, 2, 128, 1) == up(rows * 4) + lists + up(rows * 320 * 4)
     assert pka.mass_workspace_bytes(p, 8, 2, 128, 3) == up(3 * rows * 128 * 4) + up(3 * rows * 4) + lists + up(rows * 320 * 4)
     assert pka.mass_workspace_bytes(p, 8, 2, 128, 1, window=50) == up(rows * 4) + lists + up(rows * 64 * 4)
+    assert pka.mass_workspace_bytes(p, 8, 2, 128, 1, window=64) == up(rows * 4) + lists + up(rows * 96 * 4)   # + 3 keys
+    assert pka.mass_workspace_bytes(p, 8, 2, 128, 1, window=300) == pka.mass_workspace_bytes(p, 8, 2, 128, 1)
     assert pka.mass_workspace_bytes(p, 8, 2, 128, 1, max_keys=1000) == up(rows * 4) + lists + up(rows * 1024 * 4)
     for bad in (dict(heads=0), dict(heads=7), dict(kv_heads=0), dict(value_dim=0), dict(splits=0), dict(splits=65),
                 dict(window=-1), dict(max_keys=-1)):

@@ -105,6 +105,18 @@ def test_drafted_tokens_under_a_window(cuda_device):
     verify(case, 3, True, 1000)
 
 
+@pytest.mark.parametrize("hq,hkv,d,ps,dt", [(8, 2, 128, 16, BF), (16, 2, 128, 16, BF), (4, 2, 64, 24, HF), (4, 2, 40, 5, SF)])
+@pytest.mark.parametrize("window", [32, 64])
+def test_window_starts_at_any_key(cuda_device, hq, hkv, d, ps, dt, window):
+    """Score rows start up to three keys before a window that fills them, and both of its ends fall inside a four of
+    keys; sequences of one item, and of four items a key apart.  The last item's row ends with the workspace."""
+    lens = [200, 201, 202, 203]
+    for queries in (decode_queries(lens), [(s, n - 4 + i) for s, n in enumerate(lens) for i in range(4)]):
+        case = build_case("mass", 21, lens, queries, hq, hkv, d, d, ps, dt, 1 / np.sqrt(d))
+        verify(case, 1, True, window)
+        verify(case, 2, True, window)
+
+
 @pytest.mark.parametrize("window", [0, 70])
 @pytest.mark.parametrize("splits", [1, 3])
 @pytest.mark.parametrize("hq,hkv,d,ps,dt", [
