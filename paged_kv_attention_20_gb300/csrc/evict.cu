@@ -16,6 +16,7 @@
 // barrier between the reads and the writes of a chunk is all it takes.
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "pa_internal.h"
@@ -461,32 +462,98 @@ template <typename U> cudaError_t launch_move(const EvictArgs &a, bool in_place,
                     : launch_pdl(move_kernel<U, false>, grid, block, 0, st, a, sh, uk, uv, w_shift, nk, (int)parts);
 }
 
-// Fours of keys a CTA holds in shared memory at most (half of an SM's).
-constexpr int kStagedFours = 6144;
+// Fours of keys a CTA holds in shared memory at most (half of an SM's; the CTAs of
+// clusters have an SM each).
+constexpr int kStagedFours = 6144, kClusterStagedFours = 12288;
+// What the CTA of a cluster asks for at least: more than half of an SM's shared memory.
+constexpr size_t kAlone = 120 * 1024;
 
-cudaError_t launch_select(const EvictArgs &a, int cluster, int room, cudaStream_t st) {
-    size_t smem = (size_t)room * sizeof(uint4);
-    // a few clusters land on a few SMs, several CTAs to each, unless a CTA asks for
-    // more than half of an SM's shared memory
-    const size_t alone = 120 * 1024;
-    if (cluster > 1 && (int64_t)a.src.sequences * a.hkv * cluster <= 152 && smem < alone) smem = alone;
-    auto kernel = cluster > 1 ? select_kernel<true> : select_kernel<false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)std::max(alone, kStagedFours * sizeof(uint4)));
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.src.sequences * a.hkv * cluster));
-    cfg.blockDim = dim3(cluster > 1 ? 1024 : 512);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
+cudaLaunchConfig_t cluster_config(cudaLaunchAttribute (&attr)[2], unsigned grid, int cluster, size_t smem) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = (unsigned)cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(cluster > 1 ? 1024 : 512);
+    cfg.dynamicSmemBytes = smem;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cfg;
+}
+
+// Clusters of a size that the current device runs at once, an SM a CTA: fewer than
+// its SMs over the size, since a cluster stays in one group of SMs and the groups'
+// sizes differ (of eight CTAs a GB300 holds 15, not 19).  0 when unknown.
+int clusters_at_once(int cluster) {
+    static std::atomic<int> known[64][kMaxCluster + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = known[dev][cluster].load(std::memory_order_relaxed);
+    if (n) return n;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = cluster_config(attr, (unsigned)cluster, cluster, kAlone);
+    if (cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(kClusterStagedFours * sizeof(uint4))) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, select_kernel<true>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    known[dev][cluster].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// Fours of keys a CTA of `cluster` stages, whatever the sink's alignment; 0: more than
+// it holds, they are re-read.
+int staged_fours(int cluster, int longest) {
+    const int span = (longest / 4 + 2 + cluster - 1) / cluster;
+    return span <= (cluster > 1 ? kClusterStagedFours : kStagedFours) ? span : 0;
+}
+
+// CTAs per (sequence, head).  A round of clusters of c takes about 10 + c + 0.8 k / c
+// microseconds for k thousand keys (barriers, then the passes over a CTA's part), a
+// lone CTA 10 + 1.1 k and about twice the passes where its keys do not fit; the
+// rounds are what decides, so that more CTAs to a list are no gain once they cost one.
+// Measured, microseconds by cluster size 1, 2, 4, 6, 8:
+//   16 lists of 131K keys   -, -, 39, 34, 50      32 lists of 32K   73, 21, 19, 37, 55
+//   64 lists of 16K        28, 19, 33, 53, 88     128 lists of 16K  28, 34, 59, 95, 158
+// No part is below 2048 keys.
+int select_ctas(int64_t pairs, int longest) {
+    int best_c = 1;
+    double best = 0.;
+    for (int c = 1; c <= (int)kMaxCluster && (c == 1 || longest / c >= 2048); ++c) {
+        const int room = staged_fours(c, longest);
+        const double k = 1e-3 * longest * (room ? 1. : 2.);
+        double rounds, each;
+        if (c == 1) {
+            const int per_sm = std::min(3, 227 * 1024 / (room * 16 + 9 * 1024));
+            rounds = std::max(1., (double)pairs / (152 * per_sm));
+            each = 10. + 1.1 * k;
+        } else {
+            const int at_once = clusters_at_once(c);
+            if (!at_once) continue;
+            rounds = (double)((pairs + at_once - 1) / at_once);
+            each = 10. + c + 0.8 * k / c;
+        }
+        if (c == 1 || rounds * each < best) {
+            best = rounds * each;
+            best_c = c;
+        }
+    }
+    return best_c;
+}
+
+cudaError_t launch_select(const EvictArgs &a, int cluster, int room, cudaStream_t st) {
+    size_t smem = (size_t)room * sizeof(uint4);
+    if (cluster > 1 && smem < kAlone) smem = kAlone;
+    auto kernel = cluster > 1 ? select_kernel<true> : select_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)((cluster > 1 ? kClusterStagedFours : kStagedFours) * sizeof(uint4)));
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = cluster_config(attr, (unsigned)(a.src.sequences * a.hkv * cluster), cluster, smem);
+    cfg.stream = st;
     const int quads = a.src.page_size % 4 == 0 && reinterpret_cast<uintptr_t>(a.key_mass) % 16 == 0;
     return cudaLaunchKernelEx(&cfg, kernel, a, ps_shift_of(a.src.page_size), room, quads);
 }
@@ -496,14 +563,8 @@ cudaError_t launch_select(const EvictArgs &a, int cluster, int room, cudaStream_
 cudaError_t launch_evict(const EvictArgs &a, int longest, int longest_kept, bool in_place, cudaStream_t st) {
     const int64_t pairs = (int64_t)a.src.sequences * a.hkv;
     if (pairs > INT32_MAX / 8) return cudaErrorInvalidValue;
-    // CTAs per (sequence, head): enough that the pairs cover the SMs and a part
-    // fits in shared memory, but no part below 2048 keys
-    int cluster = 1;
-    while (cluster < (int)kMaxCluster && longest / (2 * cluster) >= 2048 &&
-           (pairs * cluster < 152 || longest / cluster > 4 * kStagedFours))
-        cluster *= 2;
-    const int span = (longest / 4 + 2 + cluster - 1) / cluster;    // fours a CTA, whatever the sink's alignment
-    cudaError_t e = launch_select(a, cluster, span <= kStagedFours ? span : 0, st);
+    const int cluster = select_ctas(pairs, longest);
+    cudaError_t e = launch_select(a, cluster, staged_fours(cluster, longest), st);
     if (e != cudaSuccess) return e;
     auto al = [](const void *p, int n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; };
     const int64_t kb = (int64_t)a.d * a.elem, vb = (int64_t)a.dv * a.elem;

@@ -102,6 +102,19 @@ def test_crowded_and_wide_totals(cuda_device, n, m, spread, levels):
     verify([n], [m], hkv=2, d=8, dv=8, sink=4, recent=7, totals=totals)
 
 
+@pytest.mark.parametrize("seqs,hkv,n", [(1, 1, 4500), (2, 4, 12000), (4, 8, 32768), (3, 8, 60000), (2, 8, 100001), (1, 8, 60000),
+                                        (1, 2, 200000), (16, 8, 9000)])
+@pytest.mark.parametrize("ties", [False, True])
+def test_lists_over_any_number_of_ctas(cuda_device, seqs, hkv, n, ties):
+    """Lists so many and so long that one to eight CTAs share one, some much shorter than the longest; with few
+    different totals the threshold's equals lie in every CTA's part."""
+    def totals(rng, k, heads):
+        x = rng.random((k, heads)).astype(np.float32)
+        return np.round(x * 7) / 7 if ties else x
+    lens = [n // (1 + 2 * (s % 3)) + s for s in range(seqs)]
+    verify(lens, [m // 4 + 7 for m in lens], hkv=hkv, d=8, dv=8, in_place=False, sink=3, recent=10, totals=totals)
+
+
 def test_many_sequences(cuda_device):
     rng = np.random.default_rng(5)
     lens = [int(x) for x in rng.integers(30, 900, size=70)]
