@@ -24,9 +24,11 @@
 // Eight chunks of 512 queries over 0.5-4.6K keys, 32 heads (15,600 steps, 65 GFLOP):
 // one thread a key, log-sum-exps gathered by the producer 85 us; producer a step
 // ahead 85 us; log-sum-exps by bulk copy, 64 columns a thread 78 us; two groups on
-// alternate steps 71 us (0.92 PFLOP/s).  What is left is latency: a Q tile arrives
-// ~1500 cycles after its stage is free, and two stages a CTA are all the shared
-// memory holds.
+// alternate steps 71 us (0.92 PFLOP/s).  Units of 256 keys, each Q tile serving two
+// MMAs, four Q stages in one CTA per SM: 80 us, as no second CTA then covers the load
+// of a unit's keys.  What is left is latency (a Q tile arrives ~1500 cycles after its
+// stage is free; two stages a CTA are all the shared memory holds) and the last round
+// of units, which fills half of the GPU.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
