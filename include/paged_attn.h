@@ -429,7 +429,11 @@ pa_status paged_attn_forward_mass(const pa_plan *plan, const void *q, const void
  *        indices, ascending, then -1 (kept_stride >= the longest kept history)
  *
  * kept_plan's block table names, entry by entry, either the source's own page
- * (in place) or a page that no used entry of the source schedule names.  A page
+ * (in place) or a page that no entry of the source schedule holds.  Held are the
+ * pages in use and, where pa_plan_advance can move the source (queries, no prefill
+ * tiles), those its rows reserve: the entries after a queried sequence's pages, up to
+ * the first that names no page of the pool or a page in use -- the device copy may be
+ * ahead of the host's.  A page
  * that rows move into has one holder (PA_ERR_WRITE_CONFLICT); pages that lie
  * within the sink and stay in place may be shared by several sequences.  A
  * sequence with equal lengths keeps every key (and is copied where the pages

@@ -260,10 +260,11 @@ pa_status paged_kv_evict(const pa_plan *plan, const pa_plan *kept_plan, float *k
         const int32_t *w = plan->words.data(), *d = kept_plan->words.data();
         const int32_t ps = plan->page_size;
         // Rows are written into a page that nothing else reads or writes: a page no
-        // used entry of the source schedule names, named once, or the sequence's own
-        // page of the same index, held by nobody else.  Pages inside the sink keep
-        // every row where it is and may be shared.
-        const bool src_shared = (pa::plan_facts(plan) & pa::kFactSharedPages) != 0;
+        // entry of the source schedule holds (those that its device copy may have
+        // advanced onto among them), named once, or the sequence's own page of the same
+        // index, held by nobody else.  Pages inside the sink keep every row where it is
+        // and may be shared.
+        const bool src_shared = (pa::plan_facts(plan) & pa::kFactSharedReach) != 0;
         const bool dst_shared = (pa::plan_facts(kept_plan) & pa::kFactSharedPages) != 0;
         std::vector<int32_t> written, all;      // filled only when some page is shared
         for (int32_t s = 0; s < plan->sequences; ++s) {
@@ -274,17 +275,17 @@ pa_status paged_kv_evict(const pa_plan *plan, const pa_plan *kept_plan, float *k
             longest_src = std::max(longest_src, n);
             const int32_t *from = w + plan->off_table + (size_t)s * plan->width;
             const int32_t *to = d + kept_plan->off_table + (size_t)s * kept_plan->width;
-            const int64_t used = ((int64_t)n + ps - 1) / ps, kept_pages = ((int64_t)m + ps - 1) / ps;
+            const int64_t kept_pages = ((int64_t)m + ps - 1) / ps;
             for (int64_t g = 0; g < kept_pages; ++g) {
                 const bool fresh = to[g] != from[g];
                 if (fresh && (plan->held[(size_t)to[g] / 64] >> (to[g] % 64) & 1))
-                    BAD(PA_ERR_WRITE_CONFLICT, "the kept schedule writes a page that the source schedule reads");
+                    BAD(PA_ERR_WRITE_CONFLICT, "the kept schedule writes a page that the source schedule reads or reserves");
                 in_place |= !fresh;
                 // (rows may move even where the host copies' lengths agree: the source
                 // may have been advanced on the device)
                 if ((src_shared || dst_shared) && (fresh || (g + 1) * ps > sink)) written.push_back(to[g]);
             }
-            if (src_shared) all.insert(all.end(), from, from + used);
+            if (src_shared) all.insert(all.end(), from, from + plan->reach[(size_t)s]);
         }
         if (src_shared || dst_shared) {
             std::sort(written.begin(), written.end());

@@ -179,22 +179,38 @@ int32_t plan_facts(const pa_plan *plan) {
     if (facts) return facts;
     facts = kFactsKnown;
     const int32_t *w = plan->words.data();
-    plan->held.assign(((size_t)plan->pages + 63) / 64, 0);
+    std::vector<uint64_t> used(((size_t)plan->pages + 63) / 64, 0);
+    plan->reach.assign((size_t)plan->sequences, 0);
     for (int32_t s = 0; s < plan->sequences; ++s) {
-        const int64_t used = ((int64_t)w[plan->off_seqlen + s] + plan->page_size - 1) / plan->page_size;
+        const int64_t n = ((int64_t)w[plan->off_seqlen + s] + plan->page_size - 1) / plan->page_size;
         const int32_t *row = w + plan->off_table + (size_t)s * plan->width;
-        for (int64_t g = 0; g < used; ++g) {
-            uint64_t &word = plan->held[(size_t)row[g] / 64];
+        for (int64_t g = 0; g < n; ++g) {
+            uint64_t &word = used[(size_t)row[g] / 64];
             const uint64_t bit = 1ull << (row[g] % 64);
-            if (word & bit) facts |= kFactSharedPages;
+            if (word & bit) facts |= kFactSharedPages | kFactSharedReach;
             word |= bit;
         }
+        plan->reach[(size_t)s] = (int32_t)n;
     }
+    plan->held = used;
     std::vector<uint8_t> seen((size_t)plan->sequences, 0);
     for (int32_t i = 0; i < plan->n_decode; ++i) {
-        uint8_t &s = seen[(size_t)w[plan->off_qmeta + 4 * (size_t)w[plan->off_decode + i]]];
-        if (s) facts |= kFactRepeatedItems;
-        s = 1;
+        const int32_t s = w[plan->off_qmeta + 4 * (size_t)w[plan->off_decode + i]];
+        if (seen[(size_t)s]) {
+            facts |= kFactRepeatedItems;
+            continue;
+        }
+        seen[(size_t)s] = 1;
+        if (plan->n_tiles > 0) continue;          // cannot advance
+        const int32_t *row = w + plan->off_table + (size_t)s * plan->width;
+        int32_t &g = plan->reach[(size_t)s];
+        for (; g < plan->width && row[g] >= 0 && row[g] < plan->pages; ++g) {
+            const uint64_t bit = 1ull << (row[g] % 64);
+            if (used[(size_t)row[g] / 64] & bit) break;
+            uint64_t &word = plan->held[(size_t)row[g] / 64];
+            if (word & bit) facts |= kFactSharedReach;
+            word |= bit;
+        }
     }
     plan->facts.store(facts, std::memory_order_release);
     return facts;

@@ -20,11 +20,16 @@ struct pa_plan {
     // a window, non-causal [0] and causal [1] (the mixed call's SM share needs them)
     double keys_tiles[2] = {0, 0}, keys_decode[2] = {0, 0};
     // facts of the host copy that only some calls need, worked out on first use
-    // (plan_facts): 0 = not yet, else kFactsKnown | flags; `held` then has a bit
-    // for every page that a used block-table entry names
+    // (plan_facts): 0 = not yet, else kFactsKnown | flags.  `reach` then has the
+    // entries of each row that hold the sequence's keys or may come to hold some
+    // without the host's knowledge (graph replays of pa_plan_advance move the device
+    // copy alone): the used ones and, where the plan can advance, those after them up
+    // to the first that names no page or a page in use (padding).  `held` has a bit
+    // for every page that such an entry names.
     mutable std::atomic<int32_t> facts{0};
     mutable std::mutex facts_mutex;
     mutable std::vector<uint64_t> held;
+    mutable std::vector<int32_t> reach;
 };
 
 namespace pa {
@@ -32,6 +37,7 @@ namespace pa {
 constexpr int32_t kFactsKnown = 1;
 constexpr int32_t kFactSharedPages = 2;     // some page is held by two used block-table entries
 constexpr int32_t kFactRepeatedItems = 4;   // some sequence has more than one decode item
+constexpr int32_t kFactSharedReach = 8;     // some page is held by two entries within `reach`
 
 // Facts about the plan's host copy (kFact* flags); std::bad_alloc when the host
 // has no memory for them.
