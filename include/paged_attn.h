@@ -440,7 +440,10 @@ pa_status paged_attn_forward_mass(const pa_plan *plan, const void *q, const void
  * differ); otherwise its budget is at least sink + recent (PA_ERR_SHAPE).  Rows past
  * a kept length are left as they were.  Lengths are read from the plans' device
  * copies: a source advanced by graph replays is evicted at its true length
- * (kept_plan is used as it was built).  The
+ * (kept_plan is used as it was built).  The budget of a sequence that can have
+ * advanced may be anything up to what its held pages hold (PA_ERR_SHAPE above).  On the
+ * device a budget above the true length keeps every key, and one below sink + recent
+ * keeps the sink before the most recent keys; both set PA_DEVICE_RANGE.  The
  * next step's plan is built from the kept lengths; rotated positions no longer
  * equal cache rows then (see `positions` above).
  */

@@ -269,7 +269,9 @@ pa_status paged_kv_evict(const pa_plan *plan, const pa_plan *kept_plan, float *k
         std::vector<int32_t> written, all;      // filled only when some page is shared
         for (int32_t s = 0; s < plan->sequences; ++s) {
             const int32_t n = w[plan->off_seqlen + s], m = d[kept_plan->off_seqlen + s];
-            if (m > n) BAD(PA_ERR_SHAPE, "a sequence would keep more keys than it has");
+            // a source that can advance may be longer on the device, up to what its pages hold
+            const int64_t most = pa::can_advance(plan, s) ? (int64_t)plan->reach[(size_t)s] * ps : n;
+            if (m > most) BAD(PA_ERR_SHAPE, "a sequence would keep more keys than it has");
             if (m < n && m < (int64_t)sink + recent) BAD(PA_ERR_SHAPE, "a sequence's budget is below sink + recent");
             longest = std::max(longest, m);
             longest_src = std::max(longest_src, n);

@@ -120,6 +120,11 @@ __global__ void __launch_bounds__(kCluster ? 1024 : 512, kCluster ? 1 : 3) selec
         for (int i = me; i < b.n - b.last; i += all) kept[b.first + b.want + i] = b.last + i;
         for (int i = b.keep + me; i < a.kept_stride; i += all) kept[i] = -1;
     };
+    // what the host could not see of a source that advanced on the device: a budget
+    // above the length (every key stays), or one too small for the sink and the recent
+    // keys of a sequence that was to stay as it is
+    if (me == 0 && h == 0 && (a.dst.seq_lens[s] > b.n || (b.keep < b.n && b.keep < a.sink + a.recent)))
+        atomicCAS(a.status, 0, PA_DEVICE_RANGE);
     if (b.keep == b.n) {                      // the whole cluster leaves here together
         for (int i = me; i < a.kept_stride; i += all) kept[i] = i < b.n ? i : -1;
         return;

@@ -193,6 +193,7 @@ int32_t plan_facts(const pa_plan *plan) {
         plan->reach[(size_t)s] = (int32_t)n;
     }
     plan->held = used;
+    plan->moves.assign((size_t)plan->sequences, 0);
     std::vector<uint8_t> seen((size_t)plan->sequences, 0);
     for (int32_t i = 0; i < plan->n_decode; ++i) {
         const int32_t s = w[plan->off_qmeta + 4 * (size_t)w[plan->off_decode + i]];
@@ -202,6 +203,7 @@ int32_t plan_facts(const pa_plan *plan) {
         }
         seen[(size_t)s] = 1;
         if (plan->n_tiles > 0) continue;          // cannot advance
+        plan->moves[(size_t)s] = 1;
         const int32_t *row = w + plan->off_table + (size_t)s * plan->width;
         int32_t &g = plan->reach[(size_t)s];
         for (; g < plan->width && row[g] >= 0 && row[g] < plan->pages; ++g) {

@@ -30,6 +30,7 @@ struct pa_plan {
     mutable std::mutex facts_mutex;
     mutable std::vector<uint64_t> held;
     mutable std::vector<int32_t> reach;
+    mutable std::vector<uint8_t> moves;   // per sequence: pa_plan_advance moves it on
 };
 
 namespace pa {
@@ -42,6 +43,8 @@ constexpr int32_t kFactSharedReach = 8;     // some page is held by two entries 
 // Facts about the plan's host copy (kFact* flags); std::bad_alloc when the host
 // has no memory for them.
 int32_t plan_facts(const pa_plan *plan);
+// Whether sequence s of the plan may have advanced on the device (after plan_facts).
+inline bool can_advance(const pa_plan *plan, int32_t s) { return plan->moves[(size_t)s] != 0; }
 
 pa_status fail(pa_status st, const char *msg);
 pa_status fail_cuda(cudaError_t e, const char *what);

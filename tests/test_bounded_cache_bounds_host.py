@@ -3,7 +3,7 @@
 Plans are built on the host and bound to made-up device addresses, which nothing dereferences: each call ends with the
 status of the first check that fails, or with PA_ERR_STATE for a plan that no upload followed.
 """
-from test_cache_ops_host import CONFLICT, FAKE, STATE, plan
+from test_cache_ops_host import CONFLICT, FAKE, SHAPE, STATE, plan
 
 
 def evict(lib, a, b, stride=100, sink=0, recent=0, hkv=2, d=64, dv=64, dt=2):
@@ -31,3 +31,19 @@ def test_evict_leaves_reserved_pages_alone(built_lib):
     # padding that names a page in use reserves nothing
     zeros = plan([21, 30], [[1, 2, 0, 0], [0, 3, 0, 0]], [(0, 20), (1, 29)], pages=12)
     assert call([12, 17], [[1, 0], [0, 3]], zeros) == STATE
+
+
+def test_evict_budget_above_the_host_length(built_lib):
+    """A budget up to what the sequence's pages hold: the device's length may have reached it."""
+    src = plan([21, 30], [[0, 1, 2, 3], [4, 5, -1, -1]], [(0, 20), (1, 29)], pages=12)
+    call = lambda lens, table, a=src: evict(built_lib, a, plan(lens, table, pages=12))   # noqa: E731
+    rows = [[0, 1, 2, 3], [4, 5, -1, -1]]
+    assert call([30, 30], rows) == STATE and call([64, 32], rows) == STATE
+    assert call([30, 30], [[8, 9], [10, 11]]) == STATE
+    assert call([40, 30], [[0, 1, 8], [4, 5, -1]]) == STATE
+    assert call([64, 33], [[0, 1, 2, 3], [4, 5, 6, -1]]) == SHAPE       # its pages hold 32
+    still = plan([21, 30], [[0, 1, 2, 3], [4, 5, -1, -1]], pages=12)
+    assert call([22, 30], rows, still) == SHAPE                         # nothing can have advanced
+    # a reserved page is moved into in place, and another row reserves it too
+    both = plan([16, 16], [[0, 2], [1, 2]], [(0, 15), (1, 15)], pages=12)
+    assert call([20, 10], [[0, 2], [1, -1]], both) == CONFLICT
