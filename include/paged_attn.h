@@ -387,7 +387,8 @@ pa_status paged_qk_norm_rope_store(const pa_plan *plan, const void *q, int64_t q
  * plan's decode items, or max_keys when that is more, at most `window` + 3
  * when window > 0 (pass 0 for a call that is not causal).  A larger max_keys lets a
  * captured decode loop (pa_plan_advance, staged plans) grow past the histories
- * it was captured with.  0 for invalid arguments.
+ * it was captured with.  0 for invalid arguments, and for more rows than the call
+ * takes or more than 2^62 bytes.
  */
 size_t pa_mass_workspace_bytes(const pa_plan *plan, int32_t num_heads, int32_t num_kv_heads, int32_t value_dim,
                                int32_t splits, int32_t window, int64_t max_keys);
@@ -408,7 +409,8 @@ size_t pa_mass_workspace_bytes(const pa_plan *plan, int32_t num_heads, int32_t n
  * graph replays) still gets its output, but adds nothing to the totals and sets
  * PA_DEVICE_RANGE.  A captured call stays valid for plan images with the same
  * counts whose sequences have one decode item each (or several, when captured so)
- * and share no pages.  Histories hold at most 2^30 keys (PA_ERR_LIMIT).  splits in
+ * and share no pages.  Histories hold at most 2^30 keys, and queries x heads x splits
+ * are at most 2^31 - 1 (PA_ERR_LIMIT).  splits in
  * 1..PA_MAX_SPLITS; other arguments, shapes and checks as paged_attn_forward.
  */
 pa_status paged_attn_forward_mass(const pa_plan *plan, const void *q, const void *k_cache, const void *v_cache, void *out,

@@ -43,6 +43,10 @@ pa_status spans_disjoint(const Span *written, int n_written, const Span *read, i
     return PA_OK;
 }
 
+bool mass_rows_fit(const pa_plan *plan, int32_t hq, int32_t splits) {
+    return (int64_t)plan->queries * hq <= INT32_MAX / splits;
+}
+
 MassLayout mass_layout(const pa_plan *plan, int32_t hq, int32_t dv, int32_t splits, int32_t window, int64_t max_keys) {
     MassLayout l{};
     const size_t rows = (size_t)plan->queries * hq;
@@ -63,7 +67,9 @@ MassLayout mass_layout(const pa_plan *plan, int32_t hq, int32_t dv, int32_t spli
     int64_t keys = std::max<int64_t>(max_keys, plan->max_seq_len);
     if (window > 0 && keys > window) keys = (int64_t)window + 3;      // a row starts up to three keys early
     l.cap = plan->n_decode > 0 ? (keys + 31) / 32 * 32 : 0;
-    l.bytes = l.scores + align256((size_t)plan->n_decode * hq * (size_t)l.cap * sizeof(float));
+    // rows and keys are below 2^31 each, so their product fits; its bytes may not
+    const uint64_t scores = (uint64_t)plan->n_decode * (uint64_t)hq * (uint64_t)l.cap;
+    l.bytes = scores >> 60 ? SIZE_MAX : l.scores + align256((size_t)scores * sizeof(float));
     return l;
 }
 
@@ -128,9 +134,10 @@ size_t pa_mass_workspace_bytes(const pa_plan *plan, int32_t num_heads, int32_t n
                                int32_t splits, int32_t window, int64_t max_keys) {
     if (!plan || num_heads < 1 || num_heads > 65535 || num_kv_heads < 1 || num_heads % num_kv_heads || value_dim < 1 ||
         value_dim > PA_MAX_HEAD_DIM || splits < 1 || splits > PA_MAX_SPLITS || window < 0 || max_keys < 0 ||
-        max_keys > INT32_MAX)
+        max_keys > INT32_MAX || !pa::mass_rows_fit(plan, num_heads, splits))
         return 0;
-    return pa::mass_layout(plan, num_heads, value_dim, splits, window, max_keys).bytes;
+    const size_t bytes = pa::mass_layout(plan, num_heads, value_dim, splits, window, max_keys).bytes;
+    return bytes == SIZE_MAX ? 0 : bytes;
 }
 
 pa_status paged_attn_forward_mass(const pa_plan *plan, const void *q, const void *k_cache, const void *v_cache, void *out,
@@ -144,6 +151,8 @@ pa_status paged_attn_forward_mass(const pa_plan *plan, const void *q, const void
     if (!key_mass) return fail(PA_ERR_ARG, "paged_attn_forward_mass: key_mass is null");
     if (reinterpret_cast<uintptr_t>(key_mass) % sizeof(float))
         return fail(PA_ERR_ARG, "paged_attn_forward_mass: key_mass not 4-byte aligned");
+    if (splits >= 1 && splits <= PA_MAX_SPLITS && !pa::mass_rows_fit(plan, num_heads, splits))
+        return fail(PA_ERR_LIMIT, "paged_attn_forward_mass: more than 2^31 - 1 (query, head, split) rows");
     if (plan->max_seq_len > (1 << 30)) return fail(PA_ERR_LIMIT, "paged_attn_forward_mass: history above 2^30 keys");
     try {
         if (pa::plan_facts(plan) & pa::kFactSharedPages)

@@ -72,6 +72,9 @@ struct MassLayout {
     int32_t max_blocks;                                    // key blocks of sequences with tiles
     int64_t cap;                                           // keys of one score row
 };
+// Whether the (query, head, split) rows can be counted in 32 bits, as the kernels' grids do.
+bool mass_rows_fit(const pa_plan *plan, int32_t hq, int32_t splits);
+// For rows that fit; bytes: SIZE_MAX when the score rows pass 2^62 bytes.
 // max_keys: keys the score rows hold at least; 0: the longest history of the host copy.
 // window: the call's, 0 when it is not causal (a causal query sees at most `window` keys).
 MassLayout mass_layout(const pa_plan *plan, int32_t hq, int32_t dv, int32_t splits, int32_t window, int64_t max_keys);

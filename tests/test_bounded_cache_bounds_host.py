@@ -3,7 +3,8 @@
 Plans are built on the host and bound to made-up device addresses, which nothing dereferences: each call ends with the
 status of the first check that fails, or with PA_ERR_STATE for a plan that no upload followed.
 """
-from test_cache_ops_host import CONFLICT, FAKE, SHAPE, STATE, plan
+import paged_kv_attention_20_gb300 as pka
+from test_cache_ops_host import CONFLICT, FAKE, LIMIT, SHAPE, STATE, plan
 
 
 def evict(lib, a, b, stride=100, sink=0, recent=0, hkv=2, d=64, dv=64, dt=2):
@@ -47,3 +48,27 @@ def test_evict_budget_above_the_host_length(built_lib):
     # a reserved page is moved into in place, and another row reserves it too
     both = plan([16, 16], [[0, 2], [1, 2]], [(0, 15), (1, 15)], pages=12)
     assert call([20, 10], [[0, 2], [1, -1]], both) == CONFLICT
+
+
+def forward_mass(lib, p, hq=4, hkv=2, d=64, dv=64, window=0, dt=2, nbytes=2 ** 63, splits=1):
+    return lib.paged_attn_forward_mass(p.handle, FAKE, FAKE, FAKE, FAKE, FAKE, hq, hkv, d, dv, 0.1, 1, window, dt, FAKE, nbytes,
+                                       splits, None)
+
+
+def test_forward_mass_rows_past_32_bits(built_lib):
+    """(query, head, split) rows are counted in 32 bits: more of them are refused, and their score rows, whose bytes can
+    leave 64 bits, ask for no workspace."""
+    def ones(n):
+        return plan([1] * n, [[i] for i in range(n)], [(i, 0) for i in range(n)], ps=1, pages=n)
+    few, more, many = ones(512), ones(513), ones(1 << 17)
+    call = lambda p, **kw: forward_mass(built_lib, p, **{**dict(hq=65535, hkv=1, d=1, dv=1), **kw})   # noqa: E731
+    assert call(few, splits=64) == STATE               # 2147450880 rows
+    assert call(more, splits=64) == LIMIT
+    assert call(many) == LIMIT and call(many, hq=16383) == STATE
+    size = lambda p, heads, **kw: pka.mass_workspace_bytes(p, heads, 1, 1, **{**dict(splits=1), **kw})   # noqa: E731
+    assert size(more, 65535, splits=64) == 0 and size(few, 65535, splits=64) > 64 * 512 * 65535 * 8
+    assert size(many, 65535) == 0
+    far = 2 ** 31 - 1
+    assert size(many, 65535, max_keys=far) == 0        # 2^66 bytes of scores
+    assert size(many, 16383, max_keys=far) == 0        # just below 2^64
+    assert size(many, 16, max_keys=far) > 2 ** 17 * 16 * far * 4
