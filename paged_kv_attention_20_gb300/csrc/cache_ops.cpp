@@ -16,7 +16,7 @@ namespace {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Longest history (in keys) any query of the plan's host copy may see.
+// Longest history (in keys) any tile's query of the plan's host copy may see.
 int64_t longest_tile_seq(const pa_plan *plan) {
     const int32_t *w = plan->words.data();
     int32_t longest = 0;
@@ -153,7 +153,8 @@ pa_status paged_attn_forward_mass(const pa_plan *plan, const void *q, const void
         return fail(PA_ERR_ARG, "paged_attn_forward_mass: key_mass not 4-byte aligned");
     if (splits >= 1 && splits <= PA_MAX_SPLITS && !pa::mass_rows_fit(plan, num_heads, splits))
         return fail(PA_ERR_LIMIT, "paged_attn_forward_mass: more than 2^31 - 1 (query, head, split) rows");
-    if (plan->max_seq_len > (1 << 30)) return fail(PA_ERR_LIMIT, "paged_attn_forward_mass: history above 2^30 keys");
+    if (std::max<int64_t>(plan->max_seq_len, pa::longest_tile_seq(plan)) > pa::kMaxCountedKeys)
+        return fail(PA_ERR_LIMIT, "paged_attn_forward_mass: history above 2^30 keys");
     try {
         if (pa::plan_facts(plan) & pa::kFactSharedPages)
             return fail(PA_ERR_WRITE_CONFLICT, "paged_attn_forward_mass: two sequences hold one page, its totals would have two owners");

@@ -175,7 +175,12 @@ __global__ void __launch_bounds__(kIndexThreads) mass_tiles_prepare_kernel(MassA
         for (int base = 0; base < S; base += kIndexThreads) {
             const int s = base + tid;
             const int z = s < S ? a.group_start[s] : 0, w = s < S ? a.group_start[s + 1] : 0;
-            const int c = w > z ? (a.plan.seq_lens[s] + 127) / 128 : 0;
+            int c = w > z ? a.plan.seq_lens[s] : 0;
+            if (c > kMaxCountedKeys) {         // (only a device copy's length: the host refuses it)
+                atomicCAS(a.status, 0, PA_DEVICE_RANGE);
+                c = 0;
+            }
+            c = (c + 127) / 128;
             upto[tid] = block_prefix(c, sums);
             __syncthreads();
             const int total = upto[kIndexThreads - 1];
@@ -289,7 +294,7 @@ __device__ __forceinline__ void add_item(const MassArgs &a, int blocks, int ps_s
     visible_range(meta.y, a.causal ? 0 : a.plan.seq_lens[meta.x], a.causal, a.window, lo64, hi64);
     const int lo = (int)lo64, hi = (int)hi64;       // positions fit 32 bits
     const int origin = (int)score_origin(lo);
-    if (hi - origin > a.cap || hi > (1 << 30)) {
+    if (hi - origin > a.cap || hi > kMaxCountedKeys) {
         // the workspace holds no scores past cap: this item adds nothing (nor does
         // one whose steps could leave 32 bits)
         if (threadIdx.x == 0) atomicCAS(a.status, 0, PA_DEVICE_RANGE);
@@ -396,7 +401,7 @@ __device__ __forceinline__ void add_repeated(const MassArgs &a, int grouped, int
     auto stage = [&](int at, int item, int pos) {
         int64_t lo, hi;
         visible_range(pos, seq_len, a.causal, a.window, lo, hi);
-        if (hi - score_origin(lo) > a.cap || hi > (1 << 30)) {
+        if (hi - score_origin(lo) > a.cap || hi > kMaxCountedKeys) {
             atomicCAS(a.status, 0, PA_DEVICE_RANGE);    // no scores past cap: adds nothing
             lo = hi = 0;
         }
@@ -556,6 +561,10 @@ __global__ void __launch_bounds__(kReThreads) mass_recompute_kernel(MassArgs a, 
     const int first = a.group_start[s], last = a.group_start[s + 1];
     if (first == last) return;
     const int n = a.plan.seq_lens[s];
+    if (n > kMaxCountedKeys) {                          // (only a device copy's length: the host refuses it)
+        if (threadIdx.x == 0) atomicCAS(a.status, 0, PA_DEVICE_RANGE);
+        return;
+    }
     const int32_t *trow = a.plan.table + (int64_t)s * a.plan.width;
     const T *kc = static_cast<const T *>(a.k), *qc = static_cast<const T *>(a.q);
     const int key = threadIdx.x % kReKeys, slot = threadIdx.x / kReKeys;

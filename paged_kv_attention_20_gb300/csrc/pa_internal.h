@@ -144,6 +144,9 @@ struct NormRopeArgs {
 };
 cudaError_t launch_norm_rope_store(const NormRopeArgs &a, cudaStream_t st);
 
+// Keys of a history whose totals are counted or chosen from: steps through them stay in 32 bits.
+constexpr int kMaxCountedKeys = 1 << 30;
+
 // Per-key softmax weight totals (paged_attn_forward_mass).
 struct MassArgs {
     PlanView plan;

@@ -72,3 +72,13 @@ def test_forward_mass_rows_past_32_bits(built_lib):
     assert size(many, 65535, max_keys=far) == 0        # 2^66 bytes of scores
     assert size(many, 16383, max_keys=far) == 0        # just below 2^64
     assert size(many, 16, max_keys=far) > 2 ** 17 * 16 * far * 4
+
+
+def test_forward_mass_long_chunks(built_lib):
+    """Histories above 2^30 keys are refused for prompt chunks too: the kernels step through keys in 32 bits."""
+    def chunk(n, extra=()):
+        return plan([n], [list(range(1025))], [(0, n - 16 + i) for i in range(16)] + list(extra), ps=1 << 20, pages=1025)
+    at, above = chunk(1 << 30), chunk((1 << 30) + 1)
+    for kw in (dict(dt=2, d=128, dv=128), dict(dt=0, d=8, dv=8)):       # (neither has tensor-core tiles at this page size)
+        assert forward_mass(built_lib, at, **kw) == STATE
+        assert forward_mass(built_lib, above, **kw) == LIMIT
