@@ -428,7 +428,8 @@ pa_status paged_attn_forward_mass(const pa_plan *plan, const void *q, const void
  * kept schedule.
  *
  *   kept [sequences, num_kv_heads, kept_stride] int32: the kept keys' former
- *        indices, ascending, then -1 (kept_stride >= the longest kept history)
+ *        indices, ascending, then -1 (kept_stride >= the longest kept history;
+ *        PA_ERR_LIMIT above 2^30 columns or keys of a history)
  *
  * kept_plan's block table names, entry by entry, either the source's own page
  * (in place) or a page that no entry of the source schedule holds.  Held are the

@@ -314,6 +314,19 @@ pa_status paged_kv_evict(const pa_plan *plan, const pa_plan *kept_plan, float *k
     } catch (const std::bad_alloc &) {
         BAD(PA_ERR_LIMIT, "out of host memory");
     }
+    if (kept_stride > pa::kMaxCountedKeys || longest_src > pa::kMaxCountedKeys)
+        BAD(PA_ERR_LIMIT, "more than 2^30 keys or columns of kept");
+    pa::EvictArgs a{};
+    a.src.sequences = plan->sequences;
+    a.key_mass = key_mass;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.kept = kept;
+    a.kept_stride = kept_stride;
+    a.sink = sink; a.recent = recent;
+    a.hkv = num_kv_heads; a.d = head_dim; a.dv = value_dim;
+    a.elem = pa::elem_bytes(dtype);
+    if (!pa::evict_fits_grid(a, in_place)) BAD(PA_ERR_LIMIT, "more lists of keys than a launch can number");
     if (plan->sequences == 0 || kept_stride == 0) return PA_OK;
     if (!plan->dev || !kept_plan->dev) BAD(PA_ERR_STATE, "plan not uploaded");
     if (!key_mass || !k_cache || !v_cache || !kept) BAD(PA_ERR_ARG, "null tensor");
@@ -331,17 +344,8 @@ pa_status paged_kv_evict(const pa_plan *plan, const pa_plan *kept_plan, float *k
                                 {kept, (size_t)plan->sequences * num_kv_heads * kept_stride * sizeof(int32_t), "kept"}};
     const pa_status apart = pa::spans_disjoint(written, 4, nullptr, 0, "paged_kv_evict");
     if (apart != PA_OK) return apart;
-    pa::EvictArgs a{};
     a.src = pa::view_of(plan);
     a.dst = pa::view_of(kept_plan);
-    a.key_mass = key_mass;
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
-    a.kept = kept;
-    a.kept_stride = kept_stride;
-    a.sink = sink; a.recent = recent;
-    a.hkv = num_kv_heads; a.d = head_dim; a.dv = value_dim;
-    a.elem = pa::elem_bytes(dtype);
     a.status = pa::device_status_ptr();
     if (!a.status) BAD(PA_ERR_CUDA, "device status word unavailable");
     cudaError_t e = pa::launch_evict(a, longest_src, longest, in_place, (cudaStream_t)stream);

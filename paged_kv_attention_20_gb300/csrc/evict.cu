@@ -54,6 +54,7 @@ struct Budget {
 __device__ __forceinline__ Budget budget_of(const EvictArgs &a, int s) {
     Budget b;
     b.n = a.src.seq_lens[s];
+    if (b.n > kMaxCountedKeys) b.n = 0;       // (only a device copy's length: select_kernel reports it)
     b.keep = min(min(a.dst.seq_lens[s], b.n), a.kept_stride);
     b.first = min(a.sink, b.keep);
     const int r = min(a.recent, b.keep - b.first);
@@ -444,27 +445,43 @@ int ps_shift_of(int ps) {
     return s;
 }
 
+// Lanes of a column slice (log2) and, in place, the slices of K and of V, for rows moved
+// in units of `unit` bytes.
+struct Slices {
+    int uk, uv, w_shift, nk, parts;
+};
+Slices slices_of(const EvictArgs &a, int unit) {
+    Slices c{};
+    c.uk = (int)((int64_t)a.d * a.elem / unit);
+    c.uv = (int)((int64_t)a.dv * a.elem / unit);
+    while (c.w_shift < 4 && (1 << c.w_shift) < std::max(c.uk, c.uv)) ++c.w_shift;
+    const int w = 1 << c.w_shift;
+    c.nk = (c.uk + w - 1) / w;
+    c.parts = c.nk + (c.uv + w - 1) / w;
+    return c;
+}
+
+// Bytes of a row that move at a time.
+int move_unit(const EvictArgs &a) {
+    const int64_t kb = (int64_t)a.d * a.elem, vb = (int64_t)a.dv * a.elem;
+    const uintptr_t bases = reinterpret_cast<uintptr_t>(a.k_cache) | reinterpret_cast<uintptr_t>(a.v_cache);
+    return kb % 16 == 0 && vb % 16 == 0 && bases % 16 == 0 ? 16 : a.elem;
+}
+
 template <typename U> cudaError_t launch_move(const EvictArgs &a, bool in_place, int longest, cudaStream_t st) {
-    const int uk = (int)((int64_t)a.d * a.elem / sizeof(U)), uv = (int)((int64_t)a.dv * a.elem / sizeof(U));
+    const Slices c = slices_of(a, (int)sizeof(U));
     const int64_t pairs = (int64_t)a.src.sequences * a.hkv;
-    int w_shift = 0;
-    while (w_shift < 4 && (1 << w_shift) < (uk > uv ? uk : uv)) ++w_shift;
-    const int w = 1 << w_shift;
-    int64_t parts;
-    int nk = 0;
-    if (in_place) {
-        nk = (uk + w - 1) / w;
-        parts = nk + (uv + w - 1) / w;
-    } else {
+    int64_t parts = c.parts;
+    if (!in_place) {
         parts = (longest + kMoveRanks - 1) / kMoveRanks;
         if (parts < 1) parts = 1;
         if (parts * pairs > INT32_MAX) parts = INT32_MAX / pairs;
     }
-    if (pairs * parts > INT32_MAX) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)(pairs * parts)), block(kMoveThreads);
     const int sh = ps_shift_of(a.src.page_size);
-    return in_place ? launch_pdl(move_kernel<U, true>, grid, block, 0, st, a, sh, uk, uv, w_shift, nk, (int)parts)
-                    : launch_pdl(move_kernel<U, false>, grid, block, 0, st, a, sh, uk, uv, w_shift, nk, (int)parts);
+    return in_place
+               ? launch_pdl(move_kernel<U, true>, grid, block, 0, st, a, sh, c.uk, c.uv, c.w_shift, c.nk, (int)parts)
+               : launch_pdl(move_kernel<U, false>, grid, block, 0, st, a, sh, c.uk, c.uv, c.w_shift, 0, (int)parts);
 }
 
 // Fours of keys a CTA holds in shared memory at most (half of an SM's; the CTAs of
@@ -565,20 +582,20 @@ cudaError_t launch_select(const EvictArgs &a, int cluster, int room, cudaStream_
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictArgs &a, int longest, int longest_kept, bool in_place, cudaStream_t st) {
+bool evict_fits_grid(const EvictArgs &a, bool in_place) {
     const int64_t pairs = (int64_t)a.src.sequences * a.hkv;
-    if (pairs > INT32_MAX / 8) return cudaErrorInvalidValue;
-    const int cluster = select_ctas(pairs, longest);
+    return pairs <= INT32_MAX / (int)kMaxCluster && (!in_place || pairs * slices_of(a, move_unit(a)).parts <= INT32_MAX);
+}
+
+cudaError_t launch_evict(const EvictArgs &a, int longest, int longest_kept, bool in_place, cudaStream_t st) {
+    const int cluster = select_ctas((int64_t)a.src.sequences * a.hkv, longest);
     cudaError_t e = launch_select(a, cluster, staged_fours(cluster, longest), st);
     if (e != cudaSuccess) return e;
-    auto al = [](const void *p, int n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; };
-    const int64_t kb = (int64_t)a.d * a.elem, vb = (int64_t)a.dv * a.elem;
-    if (kb % 16 == 0 && vb % 16 == 0 && al(a.k_cache, 16) && al(a.v_cache, 16))
-        e = launch_move<uint4>(a, in_place, longest_kept, st);
-    else if (a.elem == 4)
-        e = launch_move<uint32_t>(a, in_place, longest_kept, st);
-    else
-        e = launch_move<uint16_t>(a, in_place, longest_kept, st);
+    switch (move_unit(a)) {
+        case 16: e = launch_move<uint4>(a, in_place, longest_kept, st); break;
+        case 4: e = launch_move<uint32_t>(a, in_place, longest_kept, st); break;
+        default: e = launch_move<uint16_t>(a, in_place, longest_kept, st); break;
+    }
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }

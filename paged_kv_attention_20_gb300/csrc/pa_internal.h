@@ -192,6 +192,8 @@ struct EvictArgs {
     int32_t kept_stride, sink, recent, hkv, d, dv, elem;
     int32_t *status;
 };
+// Whether the launches can number the lists and, in place, their column slices.
+bool evict_fits_grid(const EvictArgs &a, bool in_place);
 // longest, longest_kept: of the host copies; in_place: some kept page is the source's own
 cudaError_t launch_evict(const EvictArgs &a, int longest, int longest_kept, bool in_place, cudaStream_t st);
 

@@ -3,6 +3,8 @@
 Plans are built on the host and bound to made-up device addresses, which nothing dereferences: each call ends with the
 status of the first check that fails, or with PA_ERR_STATE for a plan that no upload followed.
 """
+import numpy as np
+
 import paged_kv_attention_20_gb300 as pka
 from test_cache_ops_host import CONFLICT, FAKE, LIMIT, SHAPE, STATE, plan
 
@@ -82,3 +84,28 @@ def test_forward_mass_long_chunks(built_lib):
     for kw in (dict(dt=2, d=128, dv=128), dict(dt=0, d=8, dv=8)):       # (neither has tensor-core tiles at this page size)
         assert forward_mass(built_lib, at, **kw) == STATE
         assert forward_mass(built_lib, above, **kw) == LIMIT
+
+
+def test_evict_sizes_past_32_bits(built_lib):
+    """kept rows and histories above 2^30 keys, which the kernels would step through past 32 bits."""
+    src, kept = plan([40, 30], [[0, 1, 2], [3, 4, -1]]), plan([20, 10], [[0, 1], [3, -1]])
+    assert evict(built_lib, src, kept, stride=1 << 30) == STATE
+    assert evict(built_lib, src, kept, stride=(1 << 30) + 1) == LIMIT
+    assert evict(built_lib, src, kept, stride=2 ** 31 - 1) == LIMIT
+    long = lambda n: plan([n], [list(range(1025))], ps=1 << 20, pages=1025)   # noqa: E731
+    short = plan([100], [[0]], ps=1 << 20, pages=1025)
+    assert evict(built_lib, long(1 << 30), short, hkv=1, d=8, dv=8) == STATE
+    assert evict(built_lib, long((1 << 30) + 1), short, hkv=1, d=8, dv=8) == LIMIT
+
+
+def test_evict_lists_past_the_grid(built_lib):
+    """So many (sequence, head) lists and column slices that a launch cannot number them: refused before any launch."""
+    n = 1 << 21
+    table = np.full((n, 1), -1, np.int32)
+    lens = np.zeros(n, np.int32)
+    table[0], lens[0] = 3, 9
+    src = plan(lens, table)
+    kept = plan(lens, table)
+    assert evict(built_lib, src, kept, hkv=8, d=1024, dv=1024, dt=0) == STATE
+    assert evict(built_lib, src, kept, hkv=64, d=1024, dv=1024, dt=0) == LIMIT      # 2^27 lists of 32 slices or more
+    assert evict(built_lib, src, kept, hkv=256, d=8, dv=8) == LIMIT                 # 2^29 lists
