@@ -29,6 +29,7 @@
 #include <cuda_fp16.h>
 
 #include "pa_internal.h"
+#include "per_device.h"
 
 namespace pa {
 namespace {
@@ -486,13 +487,9 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 template <typename T, int D, int GH>
 cudaError_t launch_fast_t(const AttnArgs &a, int items, int use_list, cudaStream_t st) {
     using C = FastCfg<T, D, GH>;
-    static bool configured = false;  // attribute set once per process (single device use)
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(decode_fast_kernel<T, D, GH>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
-        if (e != cudaSuccess) return e;
-        configured = true;
-    }
+    static PerDevice configured;
+    const cudaError_t e = allow_smem(configured, decode_fast_kernel<T, D, GH>, C::SMEM);
+    if (e != cudaSuccess) return e;
     const int groups = (a.hq / a.hkv) / GH;
     dim3 grid(items, a.hkv * groups, a.splits);
     decode_fast_kernel<T, D, GH><<<grid, C::NT, C::SMEM, st>>>(a, use_list, groups, ps_shift_of(a.plan.page_size));

@@ -45,6 +45,7 @@
 #include <cuda_fp16.h>
 
 #include "pa_internal.h"
+#include "per_device.h"
 #include "sm103_tc.cuh"
 #include "tma_host.h"
 
@@ -574,25 +575,15 @@ cudaError_t launch_cw(const AttnArgs &a, int items, int use_list, const CUtensor
                       const TcParams &tp, cudaStream_t st) {
     // Persistent grid: as many CTAs as fit on the GPU at once (one per SM), or
     // fewer when the caller keeps SMs for a concurrent kernel.
-    static int resident = 0;
-    if (resident == 0) {
-        cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<T, CW, kMass>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)kSmemBytes);
-        if (e != cudaSuccess) return e;
-        int per_sm = 0, dev = 0, sms = 0;
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_tc_kernel<T, CW, kMass>, kThreads, kSmemBytes);
-        if (e != cudaSuccess) return e;
-        e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return e;
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess) return e;
-        resident = per_sm * sms > 0 ? per_sm * sms : 1;
-    }
+    static PerDevice known;
+    int resident = 0;
+    cudaError_t e = resident_ctas(known, decode_tc_kernel<T, CW, kMass>, kThreads, kSmemBytes, resident);
+    if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)items * a.splits * a.hkv;
     int64_t ctas = units < resident ? units : resident;
     if (a.max_ctas > 0 && a.max_ctas < ctas) ctas = a.max_ctas;
     const dim3 grid((unsigned)ctas);
-    cudaError_t e = launch_pdl(decode_tc_kernel<T, CW, kMass>, grid, dim3(kThreads), kSmemBytes, st, tk, tv, a, use_list, tp);
+    e = launch_pdl(decode_tc_kernel<T, CW, kMass>, grid, dim3(kThreads), kSmemBytes, st, tk, tv, a, use_list, tp);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }

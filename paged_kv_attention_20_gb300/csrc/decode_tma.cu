@@ -24,6 +24,7 @@
 #include <cuda_fp16.h>
 
 #include "pa_internal.h"
+#include "per_device.h"
 #include "sm103_tc.cuh"
 #include "tma_host.h"
 
@@ -404,18 +405,13 @@ template <typename T, int D, int GH, bool kMass>
 cudaError_t launch_s(const AttnArgs &a, int items, int use_list, const CUtensorMap &tk, const CUtensorMap &tv,
                      const TmaParams &tp, cudaStream_t st) {
     using C = Cfg<D, GH>;
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(decode_tma_kernel<T, D, GH, kMass>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
-        if (e != cudaSuccess) return e;
-        configured = true;
-    }
+    static PerDevice configured;
+    cudaError_t e = allow_smem(configured, decode_tma_kernel<T, D, GH, kMass>, C::SMEM);
+    if (e != cudaSuccess) return e;
     TmaParams p = tp;
     p.groups = (a.hq / a.hkv) / GH;
     const dim3 grid((unsigned)((int64_t)items * a.splits * a.hkv * p.groups));
-    cudaError_t e =
-        launch_pdl(decode_tma_kernel<T, D, GH, kMass>, grid, dim3(128), C::SMEM, st, tk, tv, a, use_list, p);
+    e = launch_pdl(decode_tma_kernel<T, D, GH, kMass>, grid, dim3(128), C::SMEM, st, tk, tv, a, use_list, p);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }

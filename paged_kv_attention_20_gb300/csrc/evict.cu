@@ -16,10 +16,10 @@
 // barrier between the reads and the writes of a chunk is all it takes.
 
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
 #include "pa_internal.h"
+#include "per_device.h"
 #include "sm103_tc.cuh"
 
 namespace pa {
@@ -509,21 +509,18 @@ cudaLaunchConfig_t cluster_config(cudaLaunchAttribute (&attr)[2], unsigned grid,
 // its SMs over the size, since a cluster stays in one group of SMs and the groups'
 // sizes differ (of eight CTAs a GB300 holds 15, not 19).  0 when unknown.
 int clusters_at_once(int cluster) {
-    static std::atomic<int> known[64][kMaxCluster + 1];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    int n = known[dev][cluster].load(std::memory_order_relaxed);
-    if (n) return n;
-    cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = cluster_config(attr, (unsigned)cluster, cluster, kAlone);
-    if (cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(kClusterStagedFours * sizeof(uint4))) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, select_kernel<true>, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    known[dev][cluster].store(n, std::memory_order_relaxed);
-    return n;
+    static PerDevice known[kMaxCluster + 1];
+    int n = 0;
+    const cudaError_t e = known[cluster].get(n, [&](int, int &v) {
+        cudaLaunchAttribute attr[2];
+        const cudaLaunchConfig_t cfg = cluster_config(attr, (unsigned)cluster, cluster, kAlone);
+        const cudaError_t set = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     (int)(kClusterStagedFours * sizeof(uint4)));
+        return set == cudaSuccess ? cudaOccupancyMaxActiveClusters(&v, select_kernel<true>, &cfg) : set;
+    });
+    if (e == cudaSuccess) return n;
+    cudaGetLastError();
+    return 0;
 }
 
 // Fours of keys a CTA of `cluster` stages, whatever the sink's alignment; 0: more than

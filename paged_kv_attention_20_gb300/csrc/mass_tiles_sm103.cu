@@ -35,6 +35,7 @@
 #include <cuda_fp16.h>
 
 #include "pa_internal.h"
+#include "per_device.h"
 #include "sm103_tc.cuh"
 #include "tma_host.h"
 
@@ -422,15 +423,11 @@ cudaError_t launch_mass_tiles(const MassArgs &a, cudaStream_t st) {
     if (!make_map(&tq, a.q, a.hq, a.plan.queries, kQ, bf16) ||
         !make_map(&tk, a.k, a.hkv, (int64_t)a.plan.pages * a.plan.page_size, a.plan.page_size, bf16))
         return cudaErrorInvalidValue;
-    static int sms = 0;
-    if (sms == 0) {
-        int dev = 0, n = 0;
-        cudaError_t e = cudaFuncSetAttribute(mass_tiles_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
-        if (e == cudaSuccess) e = cudaGetDevice(&dev);
-        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess) return e;
-        sms = n;
-    }
+    static PerDevice configured;
+    cudaError_t e = allow_smem(configured, mass_tiles_kernel, sizeof(Smem));
+    int sms = 0;
+    if (e == cudaSuccess) e = device_sms(sms);
+    if (e != cudaSuccess) return e;
     TileParams prm{};
     prm.plan = a.plan;
     prm.key_mass = a.key_mass;
@@ -443,7 +440,7 @@ cudaError_t launch_mass_tiles(const MassArgs &a, cudaStream_t st) {
     prm.bf16 = bf16 ? 1 : 0;
     prm.scale_log2 = a.scale * kLog2e;
     prm.status = a.status;
-    cudaError_t e = launch_pdl(mass_tiles_kernel, dim3((unsigned)(2 * sms)), dim3(kThreads), sizeof(Smem), st, tq, tk, prm);
+    e = launch_pdl(mass_tiles_kernel, dim3((unsigned)(2 * sms)), dim3(kThreads), sizeof(Smem), st, tq, tk, prm);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }

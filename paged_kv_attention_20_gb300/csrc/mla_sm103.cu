@@ -44,6 +44,7 @@
 #include <cuda_fp16.h>
 
 #include "pa_internal.h"
+#include "per_device.h"
 #include "sm103_tc.cuh"
 #include "tma_host.h"
 
@@ -540,22 +541,15 @@ cudaError_t launch_mla(const AttnArgs &a, bool use_list, cudaStream_t st) {
     const dim3 grid((unsigned)(2 * items * prm.head_blocks * a.splits));
     cudaError_t e;
     if (bf16) {
-        static bool cfg = false;
-        if (!cfg) {
-            e = cudaFuncSetAttribute(mla_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)kSmemBytes);
-            if (e != cudaSuccess) return e;
-            cfg = true;
-        }
+        static PerDevice configured;
+        e = allow_smem(configured, mla_kernel<__nv_bfloat16>, kSmemBytes);
+        if (e != cudaSuccess) return e;
         e = launch_pdl(mla_kernel<__nv_bfloat16>, grid, dim3(kThreads), kSmemBytes, st, tq, tqp, tlat, tkp, prm);
         if (e != cudaSuccess) return e;
     } else {
-        static bool cfg = false;
-        if (!cfg) {
-            e = cudaFuncSetAttribute(mla_kernel<__half>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-            if (e != cudaSuccess) return e;
-            cfg = true;
-        }
+        static PerDevice configured;
+        e = allow_smem(configured, mla_kernel<__half>, kSmemBytes);
+        if (e != cudaSuccess) return e;
         e = launch_pdl(mla_kernel<__half>, grid, dim3(kThreads), kSmemBytes, st, tq, tqp, tlat, tkp, prm);
         if (e != cudaSuccess) return e;
     }

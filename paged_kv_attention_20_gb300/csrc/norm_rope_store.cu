@@ -20,6 +20,7 @@
 #include <cuda_fp16.h>
 
 #include "pa_internal.h"
+#include "per_device.h"
 #include "sm103_tc.cuh"
 
 namespace pa {
@@ -558,17 +559,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(NormRopeArgs a,
 
 template <typename T, int L, int kStages>
 cudaError_t launch_tokens(const NormRopeArgs &a, const StageLayout &lay, int tokens, cudaStream_t st) {
-    static int sms = 0;
-    if (sms == 0) {
-        int dev = 0, n = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(norm_rope_tokens_kernel<T, L, kStages>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)kTokenSmem);
-        if (e != cudaSuccess) return e;
-        sms = n;
-    }
+    static PerDevice configured;
+    cudaError_t e = allow_smem(configured, norm_rope_tokens_kernel<T, L, kStages>, kTokenSmem);
+    int sms = 0;
+    if (e == cudaSuccess) e = device_sms(sms);
+    if (e != cudaSuccess) return e;
     return launch_pdl(norm_rope_tokens_kernel<T, L, kStages>, dim3((unsigned)sms), dim3(32u * (unsigned)lay.warps),
                       kTokenSmem, st, a, lay, tokens);
 }

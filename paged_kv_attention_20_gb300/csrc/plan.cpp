@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "plan_host.h"
+#include "per_device.h"
 
 using pa::aligned16;
 using pa::elem_bytes;
@@ -74,15 +75,6 @@ SideStream *side_stream(cudaStream_t st) {
     ss.fork = fork;
     ss.join = join;
     return &ss;
-}
-
-int device_sms() {
-    static int sms[kMaxSideDevices] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxSideDevices) return 0;
-    if (sms[dev] == 0 && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return sms[dev];
 }
 
 int decode_sms_beside_prefill(const pa_plan *plan, int hq, int hkv, int d, int dv, int causal, int window,
@@ -701,9 +693,9 @@ pa_status attention(const pa_plan *plan, const void *q, const void *k, const voi
         bool tiles = plan->n_tiles > 0 && pa::prefill_supported(a);
         if (tiles) {
             // with splits > 1 both kernels write partials and one merge covers every query
-            const int sms = device_sms();
+            int sms = 0;
             const int beside =
-                sms > 0 ? decode_sms_beside_prefill(plan, hq, hkv, d, dv, causal, window, dtype, sms) : 0;
+                pa::device_sms(sms) == cudaSuccess ? decode_sms_beside_prefill(plan, hq, hkv, d, dv, causal, window, dtype, sms) : 0;
             SideStream *side = beside > 0 ? side_stream(st) : nullptr;
             if (side) {
                 // prefill on sms - beside persistent CTAs, launched first so that they

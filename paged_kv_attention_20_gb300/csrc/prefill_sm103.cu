@@ -45,6 +45,7 @@
 #include <cuda_fp16.h>
 
 #include "pa_internal.h"
+#include "per_device.h"
 #include "sm103_tc.cuh"
 #include "tma_host.h"
 
@@ -657,24 +658,14 @@ cudaError_t launch_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtenso
     // Persistent grid: no more CTAs than can be resident at once (one per SM;
     // each walks its share of the units), so none waits for another to finish;
     // fewer when the caller keeps SMs free for a concurrent kernel.
-    static int resident = 0;
-    if (resident == 0) {
-        cudaError_t e = cudaFuncSetAttribute(prefill_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)kSmemBytes);
-        if (e != cudaSuccess) return e;
-        int per_sm = 0, dev = 0, sms = 0;
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, prefill_kernel<T>, kThreads, kSmemBytes);
-        if (e != cudaSuccess) return e;
-        e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return e;
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess) return e;
-        resident = per_sm * sms > 0 ? per_sm * sms : 1;
-    }
+    static PerDevice known;
+    int resident = 0;
+    cudaError_t e = resident_ctas(known, prefill_kernel<T>, kThreads, kSmemBytes, resident);
+    if (e != cudaSuccess) return e;
     int ctas = units < resident ? units : resident;
     if (max_ctas > 0 && max_ctas < ctas) ctas = max_ctas;
     const dim3 grid((unsigned)ctas);
-    cudaError_t e = launch_pdl(prefill_kernel<T>, grid, dim3(kThreads), kSmemBytes, st, tq, tk, tv, prm);
+    e = launch_pdl(prefill_kernel<T>, grid, dim3(kThreads), kSmemBytes, st, tq, tk, tv, prm);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }

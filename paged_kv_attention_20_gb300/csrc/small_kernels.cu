@@ -10,6 +10,8 @@
 // and `attention_into_split` (FP32 statistics): out = sum_s w_s o_s / sum_s w_s
 // with w_s = exp(lse_s - max_s lse_s); empty splits (lse = -inf) weigh 0.
 
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -152,15 +154,17 @@ cudaError_t launch_plan_advance(const PlanView &plan, int32_t *status, cudaStrea
 }
 
 int32_t *device_status_ptr() {
-    static int32_t *cached[64] = {nullptr};
+    static std::atomic<int32_t *> cached[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
-    if (!cached[dev]) {
+    int32_t *at = cached[dev].load(std::memory_order_acquire);
+    if (!at) {
         void *p = nullptr;
         if (cudaGetSymbolAddress(&p, g_device_status) != cudaSuccess) return nullptr;
-        cached[dev] = static_cast<int32_t *>(p);
+        at = static_cast<int32_t *>(p);
+        cached[dev].store(at, std::memory_order_release);
     }
-    return cached[dev];
+    return at;
 }
 
 cudaError_t read_device_status(int32_t *code, bool clear) {
