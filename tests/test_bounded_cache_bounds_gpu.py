@@ -4,7 +4,10 @@ import pytest
 import torch
 
 import paged_kv_attention_20_gb300 as pka
-from cache_ops_reference import kept_keys, slots
+from cache_ops_reference import kept_keys, key_mass, slots, weight_tolerance
+from test_evict_gpu import verify as verify_eviction
+from test_key_mass_gpu import decode_case as mass_case, run_case, verify as verify_mass
+from workloads import build_case
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +69,55 @@ def test_evict_budget_above_the_device_length(cuda_device):
 def test_evict_device_length_makes_a_budget_too_small(cuda_device):
     """The host sees 21 of 21 keys stay; of the device's 45, 21 are fewer than the sink and the recent keys."""
     evict_and_check([21, 16], TABLE, 18, 6, 4)
+
+
+def test_page_facts_follow_an_eager_advance(cuda_device):
+    """What a plan has found out about its pages is found again once it has advanced: totals of a page that two used
+    entries name by then, and an eviction onto a page that another sequence has reached, are refused."""
+    k, v = (torch.zeros(4, PS, HKV, 64, device="cuda") for _ in range(2))
+    mass, q = torch.zeros(4, HKV, PS, device="cuda"), torch.zeros(1, 2 * HKV, 64, device="cuda")
+    plan = pka.paged_attn_plan([16], [[0, 0]], [0], [15], PS, 4, device="cuda")
+    call = lambda: pka.paged_attn_forward_mass(plan, q, k, v, mass, 0.125, splits=1)   # noqa: E731
+    call()
+    pka.paged_attn_plan_advance(plan)
+    with pytest.raises(pka.PagedAttentionError) as e:
+        call()
+    assert e.value.status == 5
+    # the first row's second entry names the second's page: padding, until the first row has come to it
+    plan = pka.paged_attn_plan([16, 14], [[0, 3], [3, 1]], [0, 1], [15, 13], PS, 4, device="cuda")
+    kept_plan = pka.paged_attn_plan([8, 8], [[0], [3]], [], [], PS, 4, device="cuda")
+    pka.paged_kv_evict(plan, kept_plan, mass, k, v)
+    pka.paged_attn_plan_advance(plan)
+    with pytest.raises(pka.PagedAttentionError) as e:
+        pka.paged_kv_evict(plan, kept_plan, mass, k, v)
+    assert e.value.status == 5
+    assert pka.device_status() == 0
+
+
+def test_large_scores_key_by_key(cuda_device):
+    """Scores in the hundreds: weights near 1 and near 0, each key against its float64 sum.  Beside the relative tolerance a
+    weight below the smallest normal number may be lost, one a head."""
+    case = mass_case(8, 2, 128, 128, 16, torch.bfloat16)
+    case.scale = 4.0
+    _, mass, before, dc, _ = run_case(case)
+    added, seen = key_mass(case, dc.k_cache)
+    b, got = before.double().cpu().numpy(), mass.double().cpu().numpy()
+    tol = weight_tolerance(case, dc.k_cache) * added + 2.0 ** -24 * (b + added) + 4 * 2.0 ** -126
+    assert (np.abs(got - b - added)[seen] <= tol[seen]).all() and np.array_equal(got[~seen], b[~seen])
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_long_lists_of_full_width(cuda_device, dt, in_place):
+    """Several long histories with eight heads of 128: every column slice walks its ranks to the end."""
+    verify_eviction([30000, 41111, 777, 20000], [7001, 40000, 777, 513], hkv=8, d=128, dv=128, dt=dt, in_place=in_place,
+                    sink=4, recent=100)
+
+
+@pytest.mark.parametrize("splits", [1, 2])
+@pytest.mark.parametrize("d,ps,dt", [(256, 16, torch.bfloat16), (256, 32, torch.float32), (128, 16, torch.float32)])
+def test_prompt_chunks_of_wide_heads(cuda_device, d, ps, dt, splits):
+    """Chunks with totals where the tiles have no tensor-core kernel: wide heads and fp32, beside decode items."""
+    lens = [200, 90, 300]
+    queries = [(0, 150 + i) for i in range(40)] + [(1, i) for i in range(90)] + [(2, 299)]
+    verify_mass(build_case("mass", 31, lens, queries, 4, 2, d, d, ps, dt, d ** -0.5), splits)
