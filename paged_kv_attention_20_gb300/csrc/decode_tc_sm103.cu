@@ -426,6 +426,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < CW; c += 32) {
+                    // The weights are rounded to the operand type for the P.V product alone:
+                    // kind::f16 takes both factors in one 16-bit type, and P as a sum of two
+                    // such terms would double the product's MMAs.  Each is off by at most half
+                    // a step (bf16: 2^-8), about as much as the output's own rounding, so the
+                    // error of a bf16 output against 64 bits is sqrt(2) of that rounding's
+                    // (2.3e-3 to 1.7e-3); the row sums and the key totals take them unrounded.
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {

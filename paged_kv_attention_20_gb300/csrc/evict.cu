@@ -7,9 +7,9 @@
 // rows 0 .. keep-1 of the destination schedule: its pages are the sequence's own
 // ones or fresh ones.
 //
-// Two kernels.  `select_kernel` finds the keep-th largest total by radix
-// selection over order-preserving 32-bit keys and writes the kept indices in
-// ascending order.  `move_kernel` moves the rows; in place that is safe without
+// Two kernels.  `select_kernel` finds the keep-th largest total by narrowing an
+// interval of order-preserving 32-bit keys, up to 11 bits a round, and writes the
+// kept indices in ascending order.  `move_kernel` moves the rows; in place that is safe without
 // any ordering between CTAs: a CTA owns a column slice of one (sequence, head)
 // and walks the ranks upwards, rank i reads row src(i) >= i and writes row i, so
 // what a chunk of ranks writes has been read by this or an earlier chunk, and a
@@ -378,6 +378,9 @@ __device__ __forceinline__ void move_column(U *at, uint32_t moves, int per, int6
 // kOrdered (some page is written in place): part p of a (sequence, head) owns
 // column slice p of all its ranks and walks them upwards.  Otherwise nothing
 // written is read, and part p takes every parts-th chunk of ranks, all columns.
+// The ordered walk is bound by its own length, a barrier every 64 ranks: 64 histories
+// of 0.5-8K to half (1024 CTAs) take 271 us a call in place and 185 into fresh pages, two
+// of 100-131K to a quarter (two slices a list, 32 CTAs) 753 against 115.
 template <typename U, bool kOrdered>
 __global__ void __launch_bounds__(kMoveThreads, kOrdered ? 4 : 5)
     move_kernel(EvictArgs a, int ps_shift, int uk, int uv, int w_shift, int nk, int parts) {

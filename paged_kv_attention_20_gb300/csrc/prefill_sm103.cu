@@ -527,6 +527,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float2 ls2 = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int c = 0; c < 64; c += 32) {
+                    // P is rounded to the operand type for P.V alone (kind::f16 takes both
+                    // factors in one 16-bit type; two such terms for P would double the MMAs):
+                    // half a step each (bf16: 2^-8), as much again as the output's rounding, so
+                    // a bf16 output is 2.3e-3 off in 64 bits where that rounding alone gives
+                    // 1.7e-3.  The row sums take P unrounded.
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
