@@ -111,7 +111,7 @@ __device__ __forceinline__ void merge_rows(const AttnArgs &a, int use_list, int 
 // Rows spread over every SM and all splits of a row are in flight at once,
 // where one warp per row would walk its splits one after another.
 template <typename T, int VEC>
-__device__ __forceinline__ void merge_row_wide(const AttnArgs &a, int use_list, int block, float *part) {
+__device__ __forceinline__ void merge_row_wide(const AttnArgs &a, int use_list, unsigned block, float *part) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;   // part: [8][dv]
     const int item = block / a.hq, h = block - item * a.hq;
     const int qi = use_list ? a.plan.decode[item] : item;
