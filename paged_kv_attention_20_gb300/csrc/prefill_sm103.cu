@@ -124,7 +124,8 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) 
     return *reinterpret_cast<uint32_t *>(&h);
 }
 
-template <typename T>
+// kLse: an unsplit call leaves every row's log-sum-exp too (paged_attn_forward_mass).
+template <typename T, bool kLse>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, PrefillParams prm) {
@@ -631,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 // the per-key totals need the row's log-sum-exp of an unsplit call too
-                if (prm.ws_lse && r < u.nq && h2 == 0) prm.ws_lse[orow] = (m_ref + log2f(lsum)) * 0.6931471805599453f;
+                if (kLse && r < u.nq && h2 == 0) prm.ws_lse[orow] = (m_ref + log2f(lsum)) * 0.6931471805599453f;
                 }
                 // O of this unit has been read: the next unit's first P.V may overwrite it
                 tc_fence_before();
@@ -657,7 +658,7 @@ bool make_map(CUtensorMap *m, const void *base, int heads, int64_t rows, int box
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <typename T>
+template <typename T, bool kLse>
 cudaError_t launch_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const PrefillParams &prm,
                      int units, int max_ctas, cudaStream_t st) {
     // Persistent grid: no more CTAs than can be resident at once (one per SM;
@@ -665,12 +666,12 @@ cudaError_t launch_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtenso
     // fewer when the caller keeps SMs free for a concurrent kernel.
     static PerDevice known;
     int resident = 0;
-    cudaError_t e = resident_ctas(known, prefill_kernel<T>, kThreads, kSmemBytes, resident);
+    cudaError_t e = resident_ctas(known, prefill_kernel<T, kLse>, kThreads, kSmemBytes, resident);
     if (e != cudaSuccess) return e;
     int ctas = units < resident ? units : resident;
     if (max_ctas > 0 && max_ctas < ctas) ctas = max_ctas;
     const dim3 grid((unsigned)ctas);
-    e = launch_pdl(prefill_kernel<T>, grid, dim3(kThreads), kSmemBytes, st, tq, tk, tv, prm);
+    e = launch_pdl(prefill_kernel<T, kLse>, grid, dim3(kThreads), kSmemBytes, st, tq, tk, tv, prm);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
@@ -707,8 +708,12 @@ cudaError_t launch_prefill(const AttnArgs &a, cudaStream_t st) {
     prm.bf16 = bf16 ? 1 : 0;
     const int64_t units = (int64_t)a.plan.n_tiles * a.splits * a.hq;
     if (units > INT32_MAX) return cudaErrorInvalidValue;
-    return bf16 ? launch_t<__nv_bfloat16>(tq, tk, tv, prm, (int)units, a.max_ctas, st)
-                : launch_t<__half>(tq, tk, tv, prm, (int)units, a.max_ctas, st);
+    const int n = (int)units;
+    if (a.splits == 1 && a.ws_lse)
+        return bf16 ? launch_t<__nv_bfloat16, true>(tq, tk, tv, prm, n, a.max_ctas, st)
+                    : launch_t<__half, true>(tq, tk, tv, prm, n, a.max_ctas, st);
+    return bf16 ? launch_t<__nv_bfloat16, false>(tq, tk, tv, prm, n, a.max_ctas, st)
+                : launch_t<__half, false>(tq, tk, tv, prm, n, a.max_ctas, st);
 }
 
 }  // namespace pa
