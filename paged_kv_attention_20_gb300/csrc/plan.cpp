@@ -618,7 +618,7 @@ pa_status attention(const pa_plan *plan, const void *q, const void *k, const voi
         if (splits < 1 || splits > PA_MAX_SPLITS) return bad(PA_ERR_SPLITS, "splits must be in 1..64");
         lay = pa::mass_layout(plan, hq, dv, splits, causal ? window : 0, 0);
         if (!ws && plan->queries > 0) return bad(PA_ERR_WORKSPACE, "workspace is null");
-        if (ws_bytes < lay.bytes) return bad(PA_ERR_WORKSPACE, "workspace too small");
+        if (lay.bytes == SIZE_MAX || ws_bytes < lay.bytes) return bad(PA_ERR_WORKSPACE, "workspace too small");
         if (ws && !aligned16(ws)) return bad(PA_ERR_WORKSPACE, "workspace not 16-byte aligned");
     } else if (split_call) {
         if (splits < 1 || splits > PA_MAX_SPLITS) return bad(PA_ERR_SPLITS, "splits must be in 1..64");

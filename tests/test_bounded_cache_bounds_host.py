@@ -6,7 +6,7 @@ status of the first check that fails, or with PA_ERR_STATE for a plan that no up
 import numpy as np
 
 import paged_kv_attention_20_gb300 as pka
-from test_cache_ops_host import CONFLICT, FAKE, LIMIT, SHAPE, STATE, plan
+from test_cache_ops_host import CONFLICT, FAKE, LIMIT, SHAPE, STATE, WORKSPACE, plan
 
 
 def evict(lib, a, b, stride=100, sink=0, recent=0, hkv=2, d=64, dv=64, dt=2):
@@ -74,6 +74,16 @@ def test_forward_mass_rows_past_32_bits(built_lib):
     assert size(many, 65535, max_keys=far) == 0        # 2^66 bytes of scores
     assert size(many, 16383, max_keys=far) == 0        # just below 2^64
     assert size(many, 16, max_keys=far) > 2 ** 17 * 16 * far * 4
+
+
+def test_forward_mass_scores_past_any_workspace(built_lib):
+    """32768 items of one history of 2^30 keys with 65535 heads: 2^63 bytes of scores, and no workspace is that large."""
+    n = 1 << 15
+    queries = [(0, (1 << 30) - 1 - 2 * i) for i in range(n)]
+    p = plan([1 << 30], [list(range(1024))], queries, ps=1 << 20, pages=1024)
+    assert pka.mass_workspace_bytes(p, 65535, 1, 1, 1) == 0
+    for nbytes in (2 ** 62, 2 ** 63, 2 ** 64 - 1):
+        assert forward_mass(built_lib, p, hq=65535, hkv=1, d=1, dv=1, nbytes=nbytes) == WORKSPACE
 
 
 def test_forward_mass_long_chunks(built_lib):
