@@ -104,7 +104,7 @@ template <int GH, int QP, int RH> struct Shared {
     float sum[2][4][GC];                             // and row sums of a unit (a warp may be here while another still reads red)
     struct Out {
         int64_t at;                                  // row of a column's output, -1: none
-        float factor;
+        float inv, up;                               // what its sum is multiplied by, one after the other
         int real;
         uint32_t nan[4];
     } out[2][GC];
@@ -848,9 +848,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float L = (s.sum[grp][0][row] + s.sum[grp][1][row]) + (s.sum[grp][2][row] + s.sum[grp][3][row]);
                     const bool there = held(x, c);
                     const int64_t at = there ? row_of(x, c) + (a.ws_o ? (int64_t)x.split * rows : 0) : -1;
-                    // L is 0 only where no key was seen; NaN stays NaN
+                    // L is 0 only where no key was seen; NaN stays NaN.  Two factors: the power goes down to
+                    // 2^-126 with the values' scales, and divided by L (2^16 for as many equal scores) it
+                    // would leave fp32's range where the output does not.
                     s.out[grp][row].at = at;
-                    s.out[grp][row].factor = L == 0.f ? 0.f : exp2f(ref.x - kTop - ref.y) / L;
+                    s.out[grp][row].inv = L == 0.f ? 0.f : exp2f(-kTop) / L;
+                    s.out[grp][row].up = exp2f(ref.x - ref.y);
                     s.out[grp][row].real = c.real;
                     for (int w = 0; w < 4; ++w) s.out[grp][row].nan[w] = x.nq > 1 ? s.nan[grp][row][w] : 0u;
                     if (there && a.ws_o) a.ws_lse[at] = L == 0.f ? -INFINITY : (ref.y + log2f(L)) * kLn2;
@@ -864,10 +867,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int g = 0; g < GC; ++g) {
                     const int64_t at = s.out[grp][g].at;
-                    const float f = s.out[grp][g].factor;
+                    const float inv = s.out[grp][g].inv;
                     const float v = fmaf(fmaf(__uint_as_float(o[2 * GC + g]), 0.0625f, __uint_as_float(o[GC + g])), 0.125f, __uint_as_float(o[g]));
                     const bool is_nan = s.out[grp][g].nan[w4] >> lane & 1u;
-                    const float y = is_nan ? __uint_as_float(0x7fffffffu) : f == 0.f ? 0.f : v * f;
+                    const float y = is_nan ? __uint_as_float(0x7fffffffu) : inv == 0.f ? 0.f : v * inv * s.out[grp][g].up;
                     if (at >= 0 && (RH == 1 || part == s.out[grp][g].real)) {
                         if (a.ws_o)
                             a.ws_o[at * D + col] = y;
