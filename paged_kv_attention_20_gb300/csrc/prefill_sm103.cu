@@ -34,7 +34,9 @@
 // Key tiles past the last query's position are never loaded; the diagonal
 // tiles are masked per row.  Keys at or past the sequence length never reach
 // P.V: their scores are masked and their V rows are zeroed in shared memory
-// (tail slots may hold anything, NaN included).  The online softmax keeps a
+// (tail slots may hold anything, NaN included); NaN or infinity in a key that
+// only some of a tile's queries see reaches those alone (second pass, below).
+// The online softmax keeps a
 // per-row reference maximum that only moves when a tile's maximum exceeds it
 // by more than 8 (log2 units), so O in TMEM is rarely rescaled.
 // Every wait is bounded; a timeout sets the library's device status word and
@@ -43,6 +45,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "pa_internal.h"
 #include "per_device.h"
@@ -84,6 +88,8 @@ struct Smem {
     float xred[2][2 * kM];         // row-max / row-sum exchange between the two warps of a row,
                                    // slot n % 2 for exchange n
     uint64_t xa[2][4];             // per slot and lane quarter: both warps' values written
+    int32_t again;                 // a unit's O is not finite: bit 0; a wait timed out: bit 1
+    int32_t bad[8];                // unit i has V rows that are not finite: i + 1 in slot i % 8 (second pass)
     int32_t up[4][12];             // parameters of unit i in slot i % 4, written by the K producer
     uint64_t up_full[4];           // slot written
     uint64_t up_empty[4];          // slot read by every other role (11 arrivals)
@@ -100,6 +106,7 @@ static_assert(kSmemBytes <= 232448, "prefill shared memory above the per-block l
 struct PrefillParams {
     PlanView plan;
     void *out;
+    const void *v;          // value cache
     float *ws_o, *ws_lse;   // split partials [S, Q, Hq, 128] (null: the output is written) and [S, Q, Hq]
     int32_t *status;
     int hq, hkv;
@@ -114,6 +121,7 @@ struct PrefillParams {
 
 __device__ __forceinline__ void set_timeout(Smem &s, int32_t *status, int code) {
     atomicCAS(status, 0, code);
+    atomicOr(&s.again, 2);
 }
 
 template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
@@ -125,6 +133,9 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) 
     __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<uint32_t *>(&h);
 }
+
+// Exponent bits, all set where a 16-bit element is not finite.
+template <typename T> constexpr uint32_t exp_bits = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
 
 // kLse: an unsplit call leaves every row's log-sum-exp too (paged_attn_forward_mass).
 // kPacked: the shared prefix of a batch.  A tile's rows are (query, head of one KV head's
@@ -238,6 +249,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         return u;
     };
 
+    // Keys that every query of a tile sees (every row of a packed one sees the prefix).
+    auto seen_by_all = [&](const Unit &u) -> int2 {
+        return make_int2(!kPacked && prm.window > 0 ? max(u.pos0 + u.nq - prm.window, 0) : 0,
+                         !kPacked && prm.causal ? u.pos0 + 1 : u.seq_len);
+    };
+
     // The CTA's i-th unit: round i of n_ctas-sized rounds, taken in serpentine
     // order (odd rounds from the last CTA down), so with units sorted by
     // decreasing size the CTAs' totals even out.  A CTA whose slot in the
@@ -247,6 +264,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ui = i * n_ctas + slot;
         return ui < units ? ui : units;
     };
+    const int rounds = (units + n_ctas - 1) / n_ctas, n_units = rounds > 0 && unit_of(rounds - 1) == units ? rounds - 1 : rounds;
+    // NaN or infinity in a value row that only some of a tile's queries see (the tiles of the diagonal
+    // and of the window's edge) reaches the others, for whom its weight is 0, through P V.  To look at
+    // such rows of every tile takes a window of 1000 keys 8 % longer (94 us for 8 x 512 queries, 87
+    // without); so O is looked at (1 %), and where it is not finite the CTA goes through its units once
+    // more with care: those rows' elements become 0 before P V, and the epilogue gives them to the
+    // queries that see them.  Unit n_units + i of the second pass is unit i of the first for every
+    // role; rings and phases run on.
+    auto place_of = [&](int i) -> int { return unit_of(i < n_units ? i : i - n_units); };
 
     // Unit parameters come from dependent loads of plan metadata (~700 cycles).
     // The K producer, which runs furthest ahead, computes them and leaves them
@@ -302,6 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_mbar_init();
     }
+    if (tid < 8) s.bad[tid] = 0;
+    if (tid == 0) s.again = 0;
     if (warp == 0) {
         tmem_alloc(&s.tmem_base, 512);
         tmem_relinquish();
@@ -313,6 +341,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto tmem_s = [tmem](int b) -> uint32_t { return tmem + 128u * (uint32_t)b; };   // S / P buffers 0..2
     const uint32_t tmem_o = tmem + 384;
 
+    int gt = 0;                                            // the role's tiles so far (all units)
+    int xphase = 0;                                        // exchanges of the softmax warps so far
+    int first = 0;                                         // unit of the pass
+    for (;;) {                                             // passes
     if (warp == 8 || warp == 10) {
         // ------------------------------------------------- TMA producers --
         // Warp 8 streams K (and Q of each unit), warp 10 streams V, each through
@@ -331,12 +363,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (is_k) tma_prefetch_desc(&tm_q);
         }
         const int oob_row = prm.plan.pages * ps;          // rows >= this read as zeros
-        int gt = 0;                                        // tiles streamed so far (all units)
         bool go = true;
-        for (int i = 0; go && unit_of(i) < units; ++i) {
+        for (int i = first; go && i < first + n_units; ++i) {
             Unit u;
             if (is_k) {
-                u = unit_at(unit_of(i));
+                u = unit_at(place_of(i));
                 if (lane == 0 && !publish_unit(i, u)) {
                     set_timeout(s, prm.status, PA_DEVICE_TIMEOUT_TMA);
                     go = false;
@@ -410,11 +441,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // waits until the softmax warps have read O of the previous unit.
         if (lane == 0) {
             bool ok = true;
-            int gt = 0;
             if (warp == 9) {
                 const uint32_t idesc_s = idesc_f16(kM, kN, prm.bf16 != 0, false, false);
                 const uint64_t q_desc = smem_desc(smem_u32(s.q), 16, 1024, kLayoutSwizzle128B);
-                for (int i = 0; ok && unit_of(i) < units; ++i) {
+                for (int i = first; ok && i < first + n_units; ++i) {
                     Unit u;
                     if (!read_unit(i, u, false)) { ok = false; break; }
                     if (!mbar_wait(&s.q_full, i & 1)) { ok = false; break; }
@@ -443,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else {
                 const uint32_t idesc_o = idesc_f16(kM, kD, prm.bf16 != 0, false, true);
-                for (int i = 0; ok && unit_of(i) < units; ++i) {
+                for (int i = first; ok && i < first + n_units; ++i) {
                     Unit u;
                     if (!read_unit(i, u, false)) { ok = false; break; }
                     if (i > 0 && !mbar_wait(&s.o_free, (i - 1) & 1)) { ok = false; break; }
@@ -474,8 +504,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int col0 = 64 * h2;
         const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
         bool ok = true;
-        int xphase = 0;
-        int gt = 0;                                // tiles consumed so far (all units)
         // value of the other warp of this row (bounded waits; false on timeout)
         // One barrier round per exchange: slot n % 2 is written again at exchange
         // n + 2 only after the partner arrived for exchange n + 1, which it does
@@ -492,19 +520,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         // a unit's parameters come from the K producer through shared memory; the
         // next unit's are read before this unit's epilogue
         Unit u{};
-        if (unit_of(0) < units) ok = read_unit(0, u, true);
+        if (n_units > 0) ok = read_unit(first, u, true);
         if (!ok) set_timeout(s, prm.status, PA_DEVICE_TIMEOUT_SOFTMAX);
-        for (int i = 0; ok && unit_of(i) < units; ++i) {
+        for (int i = first; ok && i < first + n_units; ++i) {
             int64_t row_j0 = 0, row_j1 = 0;           // this row's keys in this split: [vis_lo, vis_end)
             if (r < u.nq) row_keys(u, u.pos0 + r, row_j0, row_j1);   // rows past the tile's queries see nothing
             const int vis_lo = (int)row_j0, vis_end = (int)row_j1;
+            // keys whose value rows go to the MMA as they are: the sequence's, with care those that every
+            // query sees
+            const int good_lo = i < n_units ? 0 : seen_by_all(u).x, good_hi = i < n_units ? u.seq_len : seen_by_all(u).y;
             float m_ref = -INFINITY, l = 0.f;
             for (int kt = 0; kt < u.n_kt && ok; ++kt, ++gt) {
                 const int sb = gt % 3;
                 ok = __all_sync(0xffffffffu, mbar_wait(&s.s_full[sb], (gt / 3) & 1));
                 if (!ok) break;
                 tc_fence_after();
-                const int kbase = (u.kt0 + kt) * kN + col0;
+                const int kb = (u.kt0 + kt) * kN, kbase = kb + col0;
                 // my 64 scores of the row into registers (two loads, one wait)
                 uint32_t sv[64];
                 tmem_ld32(tmem_s(sb) + lane_off + col0, sv);
@@ -577,23 +608,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tmem_wait_st();
                 l = l * alpha + (ls2.x + ls2.y);
-                // V rows at or past the sequence end (tail slots) must not reach the MMA
-                if ((u.kt0 + kt) * kN + kN > u.seq_len) {
+                // V rows at or past the sequence end (tail slots) must not reach the MMA, nor (second
+                // pass) what is not finite in rows that only some of the queries see
+                if (kb < good_lo || kb + kN > good_hi) {
                     const int st = gt % kStages;
                     ok = __all_sync(0xffffffffu, mbar_wait(&s.v_full[st], (gt / kStages) & 1));
                     if (!ok) break;
-                    if ((u.kt0 + kt) * kN + r >= u.seq_len) {
+                    uint8_t *const row = s.v[st] + (r >> 3) * 2048 + h2 * 1024 + (r & 7) * 128;
+                    if (kb + r >= u.seq_len) {
                         const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            *reinterpret_cast<uint4 *>(s.v[st] + (r >> 3) * 2048 + h2 * 1024 + (r & 7) * 128 + i * 16) = z;
+                        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(row + c * 16) = z;
+                    } else if (kb + r < good_lo || kb + r >= good_hi) {
+#pragma unroll 1
+                        for (int e = 0; e < 64; ++e) {
+                            uint16_t *x = reinterpret_cast<uint16_t *>(row) + e;
+                            if ((*x & exp_bits<T>) != exp_bits<T>) continue;
+                            *x = 0;
+                            s.bad[i & 7] = i + 1;
+                        }
                     }
-                    fence_proxy_async_smem();  // the zeroed V rows before the tensor core reads them
+                    fence_proxy_async_smem();  // the changed V rows before the tensor core reads them
                 }
                 tc_fence_before();
                 mbar_arrive(&s.p_ready[gt % 3]);
             }
-            const bool more = unit_of(i + 1) < units;
+            const bool more = i + 1 < first + n_units;
             Unit nu = u;
             if (more && ok) ok = read_unit(i + 1, nu, true);
             if (ok && u.n_kt > 0)
@@ -610,6 +650,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float lsum = l + l_other;
                 const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
                 const int64_t orow = row_at(u, r);
+                // Second pass: elements of value rows that this row sees and other rows of the tile do not,
+                // taken out before P V as they were not finite: bit e for column col0 + e, to which +inf
+                // (-inf) is added; NaN has both.  Every warp's notes are there once the last P V is done,
+                // and a slot's next unit is eight on (a warp is at most five units ahead of another).
+                uint64_t plus = 0, minus = 0;
+                if (!kPacked && i >= n_units && u.n_kt > 0 && s.bad[i & 7] == i + 1) {
+                    for (int j = vis_lo; j < vis_end; ++j) {
+                        if (j >= good_lo && j < good_hi) {
+                            j = good_hi - 1;
+                            continue;
+                        }
+                        const int g = j / ps;
+                        const uint4 *v = reinterpret_cast<const uint4 *>(
+                            static_cast<const T *>(prm.v) + (((int64_t)u.trow[g] * ps + (j - g * ps)) * prm.hkv + u.kvh) * kD + col0);
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) {
+                            const uint4 four = v[c];
+                            const uint32_t w[4] = {four.x, four.y, four.z, four.w};
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const uint32_t x = w[e / 2] >> (16 * (e & 1)) & 0xffffu;
+                                if ((x & exp_bits<T>) != exp_bits<T>) continue;
+                                const bool is_nan = (x & 0x7fffu) != exp_bits<T>;
+                                if (is_nan || !(x & 0x8000u)) plus |= 1ull << (8 * c + e);
+                                if (is_nan || (x & 0x8000u)) minus |= 1ull << (8 * c + e);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+                // O of the first and last query tells: each key that not all see is hidden from one of them
+                const bool ends = !kPacked && i < n_units && (r == 0 || r == u.nq - 1);
+                auto look_at = [&](uint32_t (&vv)[64]) {
+                    if (__any_sync(0xffffffffu, ends)) {
+                        float sum[2] = {0.f, 0.f};
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) sum[e & 1] = fmaf(__uint_as_float(vv[e]), 0.f, sum[e & 1]);
+                        if (ends && isnan(sum[0] + sum[1])) atomicOr(&s.again, 1);
+                    }
+                    if (kPacked || !__any_sync(0xffffffffu, (plus | minus) != 0)) return;
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) {
+                        if (plus >> e & 1u) vv[e] = __float_as_uint(__uint_as_float(vv[e]) + INFINITY);
+                        if (minus >> e & 1u) vv[e] = __float_as_uint(__uint_as_float(vv[e]) - INFINITY);
+                    }
+                };
                 const int jj = lane & 7, g = lane & ~7;   // lane in its group of 8, the group's first row
                 if (kPacked || prm.ws_o) {
                     const int64_t rows = (int64_t)prm.plan.queries * prm.hq;
@@ -622,6 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 64; ++e) vv[e] = 0u;
                     }
+                    look_at(vv);
                     // fp32 partials: each half of the row's 64 columns is eight 16-byte chunks
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
@@ -648,6 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(tmem_o + lane_off + col0, vv);          // all 64 columns, one wait
                 tmem_ld32(tmem_o + lane_off + col0 + 32, vv + 32);
                 tmem_wait_ld();
+                look_at(vv);
                 // the row's 64 output columns as eight 16-byte chunks of 16-bit pairs
                 uint32_t ch[32];
 #pragma unroll
@@ -671,6 +759,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             u = nu;
         }
+    }
+    if (kPacked || first > 0) break;
+    __syncthreads();
+    if (s.again != 1) break;
+    first = n_units;
     }
     griddep_launch();
     tc_fence_before();
@@ -750,6 +843,7 @@ cudaError_t launch_prefix(const AttnArgs &a, int32_t shared, cudaStream_t st) {
         return cudaErrorInvalidValue;
     PrefillParams prm{};
     prm.plan = a.plan;
+    prm.v = a.v;
     prm.ws_o = a.ws_o;
     prm.ws_lse = a.ws_lse;
     prm.splits = a.splits;
@@ -776,6 +870,7 @@ cudaError_t launch_prefill(const AttnArgs &a, cudaStream_t st) {
         return cudaErrorInvalidValue;
     PrefillParams prm{};
     prm.plan = a.plan;
+    prm.v = a.v;
     prm.out = a.out;
     prm.ws_o = a.ws_o;
     prm.ws_lse = a.ws_lse;
