@@ -100,6 +100,17 @@ SideStream *side_stream(cudaStream_t st) {
     return &ss;
 }
 
+cudaError_t fork_side(SideStream &side, cudaStream_t st) {
+    const cudaError_t e = cudaEventRecord(side.fork, st);
+    return e == cudaSuccess ? cudaStreamWaitEvent(side.stream, side.fork, 0) : e;
+}
+
+cudaError_t join_side(SideStream &side, cudaStream_t st, cudaError_t e) {
+    cudaError_t joined = cudaEventRecord(side.join, side.stream);
+    if (joined == cudaSuccess) joined = cudaStreamWaitEvent(st, side.join, 0);
+    return e != cudaSuccess ? e : joined;
+}
+
 pa_status fail(pa_status st, const char *msg) {
     g_error = msg;
     return st;
@@ -737,8 +748,8 @@ pa_status attention(const pa_plan *plan, const void *q, const void *k, const voi
             if (side) {
                 // prefill on sms - beside persistent CTAs, launched first so that they
                 // hold their SMs; the decode items fill the rest from the side stream
-                e = cudaEventRecord(side->fork, st);
-                if (e == cudaSuccess) e = cudaStreamWaitEvent(side->stream, side->fork, 0);
+                e = pa::fork_side(*side, st);
+                const bool forked = e == cudaSuccess;
                 pa::AttnArgs ap = a;
                 ap.max_ctas = sms - beside;
                 mark(t0);
@@ -747,8 +758,7 @@ pa_status attention(const pa_plan *plan, const void *q, const void *k, const voi
                 pa::AttnArgs ad = a;
                 ad.max_ctas = beside;
                 if (e == cudaSuccess) e = pa::launch_decode(ad, true, side->stream);
-                if (e == cudaSuccess) e = cudaEventRecord(side->join, side->stream);
-                if (e == cudaSuccess) e = cudaStreamWaitEvent(st, side->join, 0);
+                if (forked) e = pa::join_side(*side, st, e);
             } else {
                 mark(t0);
                 e = pa::launch_prefill(a, st);

@@ -72,6 +72,11 @@ struct SideStream {
 };
 // The calling thread's on the current device; null where there is none yet and `st` is being captured.
 SideStream *side_stream(cudaStream_t st);
+// What is put on the side stream from here on comes after what `st` holds.
+cudaError_t fork_side(SideStream &side, cudaStream_t st);
+// And what `st` gets from here on after that; also where a launch in between failed with `e`, as
+// the work beside still writes the caller's tensors.  The first error.
+cudaError_t join_side(SideStream &side, cudaStream_t st, cudaError_t e);
 
 // The events of pa_time_next_kernel, for the one call that takes them.
 void take_timing(cudaEvent_t &start, cudaEvent_t &stop);

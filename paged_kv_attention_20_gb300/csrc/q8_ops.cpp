@@ -355,13 +355,13 @@ pa_status paged_attn_forward_q8(const pa_plan *plan, const void *q, const uint8_
         // the decode items beside the copy and the tiles, on SMs of their own
         const int beside = pa::q8_sms_beside_prefill(plan, a, sms);
         pa::SideStream *side = beside > 0 ? pa::side_stream(st) : nullptr;
+        bool forked = false;
         if (side) {
             x.a.max_ctas = beside;
             wide.max_ctas = sms - beside;
-            e = cudaEventRecord(side->fork, st);
-            if (e == cudaSuccess) e = cudaStreamWaitEvent(side->stream, side->fork, 0);
+            e = pa::fork_side(*side, st);
+            forked = e == cudaSuccess;
             if (e == cudaSuccess) e = pa::launch_q8_decode(x, true, plan->longest_run, side->stream);
-            if (e == cudaSuccess) e = cudaEventRecord(side->join, side->stream);
         }
         if (e == cudaSuccess) e = pa::launch_q8_first_pages(a.plan, first, pa::kCopyPage, wide.plan.pages, a.status, st);
         pa::Q8LoadArgs c{};
@@ -379,11 +379,10 @@ pa_status paged_attn_forward_q8(const pa_plan *plan, const void *q, const uint8_
         mark(t0);
         if (e == cudaSuccess) e = pa::launch_prefill(wide, st);
         mark(t1);
-        if (side) {
-            if (e == cudaSuccess) e = cudaStreamWaitEvent(st, side->join, 0);
-        } else if (e == cudaSuccess && plan->n_decode > 0) {
+        if (forked)
+            e = pa::join_side(*side, st, e);
+        else if (e == cudaSuccess && plan->n_decode > 0)
             e = pa::launch_q8_decode(x, true, plan->longest_run, st);
-        }
         if (e == cudaSuccess && splits > 1) e = pa::launch_merge(a, false, st);
     } else {
         const bool all_decode = plan->n_tiles == 0;

@@ -153,6 +153,7 @@ pa_status paged_attn_forward_shared(const pa_plan *plan, const void *q, const vo
         if (ev && e == cudaSuccess) e = cudaEventRecord(ev, st);
     };
     pa::SideStream *side = nullptr;
+    bool forked = false;
     pa::AttnArgs own = a, merged = a;
     own.splits = merged.splits = all;
     if (shared > 0 && prefix_splits > 0 && pa::prefix_supported(a)) {
@@ -170,8 +171,8 @@ pa_status paged_attn_forward_shared(const pa_plan *plan, const void *q, const vo
             // the prefix first, so that its CTAs hold their SMs; the own keys from the side stream
             prefix.max_ctas = share;
             own.max_ctas = sms - share;
-            e = cudaEventRecord(side->fork, st);
-            if (e == cudaSuccess) e = cudaStreamWaitEvent(side->stream, side->fork, 0);
+            e = pa::fork_side(*side, st);
+            forked = e == cudaSuccess;
         }
         mark(t0);
         if (e == cudaSuccess) e = pa::launch_prefix(prefix, shared, st);
@@ -185,10 +186,7 @@ pa_status paged_attn_forward_shared(const pa_plan *plan, const void *q, const vo
     if (e == cudaSuccess && tiles) e = pa::launch_prefill(own, to);
     if (e == cudaSuccess && (!tiles || plan->n_decode > 0)) e = pa::launch_decode(own, tiles || plan->n_tiles == 0, to);
     mark(t1);
-    if (side) {
-        if (e == cudaSuccess) e = cudaEventRecord(side->join, side->stream);
-        if (e == cudaSuccess) e = cudaStreamWaitEvent(st, side->join, 0);
-    }
+    if (forked) e = pa::join_side(*side, st, e);
     if (e == cudaSuccess) e = pa::launch_merge(merged, false, st);
     if (e != cudaSuccess) return pa::fail_cuda(e, kName);
     return PA_OK;
