@@ -10,49 +10,71 @@ using pa::fail;
 
 namespace {
 
-// How the work is laid out: splits of the prefix and of the sequences' own keys, and the SMs the
-// prefix's kernel takes while the own keys are attended on the others (0: one after the other).
-struct Layout {
-    int32_t prefix_splits, splits, sms;
+// SMs that the prefix's kernel takes while the own keys are attended on the others (0: one after
+// the other), and how long the call is thought to take with them, in seconds.
+struct Beside {
+    int32_t sms;
+    double time;
 };
 
-// The prefix's units, (128 rows of queries and heads, KV head, split), take 9 us to start and
-// end and 1 us a tile of 128 keys; the decode kernel reads 34 GB/s of short histories on each SM,
-// 4.4 TB/s in all; a split's partials are written and read again.  The layout is taken that ends
-// soonest (64 sequences with 512 keys of their own: behind 4096 keys 57 us side by side, 74 one
-// after the other; behind 16384 with 3, 4, 5 and 8 splits 66, 59, 80 and 72).  The own keys'
-// splits are the split heuristic's for what is left of the sequences.
-Layout layout_of(const pa_plan *plan, int32_t hq, int32_t hkv, int32_t shared, int32_t sms) {
-    Layout best{1, 1, 0};
-    if (plan->queries == 0) return best;
+// For the splits that a call is given.  The prefix's units, (128 rows of queries and heads, KV head,
+// split), take 9 us to start and end and 1 us a tile of 128 keys, in rounds on the SMs that they
+// have; a split's partials are written and read again.  The own keys of groups of up to seven heads
+// are read by many blocks at 34 GB/s an SM, 3.3 TB/s in all beside the prefix, and at 4.4 TB/s on the
+// whole GPU where the prefix has ended.  Those of larger groups have a persistent kernel that keeps
+// to its SMs: 3.2 us a unit and 1.35 us a tile of it.  The SMs are those that make 1 to 8 rounds.
+// Against sweeps of the share (16 to 256 queries, 7 or 8 split counts each, groups of 4 and 8) the one
+// taken is the best or within 5 % of it, 12 % where a call has far more splits than it should.  64
+// queries behind 16384 keys, 9 splits: with 1, 512 and 2048 own keys 44, 81 and 168 us; on the SMs of
+// the best split count, which the call does not run with, 45, 86 and 200 (groups of 8: 83, 105 and
+// 160; 123, 120 and 191).
+Beside beside_of(const pa_plan *plan, int32_t hq, int32_t hkv, int32_t shared, int32_t prefix_splits, int32_t splits, int32_t sms) {
     const int64_t group = hq / hkv, per_tile = std::max<int64_t>(1, 128 / group);
+    const int64_t units = (plan->queries + per_tile - 1) / per_tile * hkv * prefix_splits;
+    const double tiles = shared / 128.0 / prefix_splits;
+    const double own_keys = std::max(0.0, plan->keys_decode[1] + plan->keys_tiles[1] - (double)plan->queries * shared);
+    const double own_bytes = own_keys * hkv * 512.0;
+    const double partials = (double)plan->queries * hq * 128 * 4 * 2 / 4e12 * prefix_splits;
+    auto prefix = [&](int64_t n) { return 9e-6 + (double)((units + n - 1) / n) * (1e-6 + 1e-6 * tiles); };
+    const bool persistent = group >= 8 && group <= 128;
+    const int64_t own_units = std::max<int64_t>(1, (int64_t)plan->n_decode * hkv * splits);
+    const double unit = 3.2e-6 + 1.35e-6 * std::max(1.0, own_keys * hkv / (double)own_units / 128);
+    auto rounds = [&](int64_t n) { return std::max((double)((own_units + n - 1) / n) * unit, own_bytes / 4.4e12); };
+    Beside best{0, prefix(sms) + (persistent ? rounds(sms) : 5e-6 + own_bytes / 4.4e12) + partials};
+    if (plan->n_tiles > 0) return best;
+    for (int64_t r = 1; r <= 8; ++r) {
+        const int64_t n = (units + r - 1) / r;
+        if (n > sms - 8) continue;
+        const double t = prefix(n), rate = std::min(3.4e10 * (double)(sms - n), 3.3e12);
+        const double own = persistent ? rounds(sms - n) : 5e-6 + std::min(own_bytes / rate, t + std::max(0.0, own_bytes - rate * t) / 4.4e12);
+        const double time = std::max(t, own) + partials + 3e-6;          // a fork and a join more
+        if (time < best.time) best = Beside{(int32_t)n, time};
+    }
+    return best;
+}
+
+// Splits of the prefix, those that end soonest, and of the sequences' own keys, the split heuristic's
+// for what is left of the sequences.
+struct Layout {
+    int32_t prefix_splits, splits;
+};
+
+Layout layout_of(const pa_plan *plan, int32_t hq, int32_t hkv, int32_t shared, int32_t sms) {
+    Layout best{1, 1};
+    if (plan->queries == 0) return best;
+    const int64_t group = hq / hkv;
     const int64_t longest = std::max<int64_t>(0, std::max(plan->max_seq_len, plan->tile_longest) - shared);
     const int64_t blocks = std::max<int64_t>(1, (int64_t)plan->n_decode * hkv * ((group + 3) / 4) + (int64_t)plan->n_tiles * hq);
     int64_t own = (blocks >= sms ? 4 : 8) * (int64_t)sms / blocks;
     own = std::min<int64_t>(own, std::max<int64_t>(1, longest / (4 * (int64_t)plan->page_size)));
     best.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>(own, PA_MAX_SPLITS / 2));
-    const int64_t units = (plan->queries + per_tile - 1) / per_tile * hkv;
-    const double tiles = shared / 128.0;
-    const double own_bytes = (plan->keys_decode[1] + plan->keys_tiles[1] - (double)plan->queries * shared) * hkv * 512.0;
-    const double partials = (double)plan->queries * hq * 128 * 4 * 2 / 4e12;
-    const double t_own = 5e-6 + own_bytes / std::min(3.4e10 * sms, 4.4e12);
-    double best_t = -1;
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>(PA_MAX_SPLITS / 2, shared / 128));
+    double best_t = -1;
     for (int32_t s = 1; s <= most; ++s) {
-        auto prefix = [&](int64_t n) {
-            return (double)((units * s + n - 1) / n) * (9e-6 + 1e-6 * tiles / s) + s * partials;
-        };
-        auto take = [&](double t, int32_t n) {
-            if (best_t >= 0 && t >= best_t) return;
-            best_t = t;
-            best.prefix_splits = s;
-            best.sms = n;
-        };
-        take(prefix(sms) + t_own, 0);
-        // side by side, a fork and a join more
-        const int64_t n = units * s;
-        if (plan->n_tiles == 0 && n <= sms - 8)
-            take(std::max(prefix(n), 5e-6 + own_bytes / std::min(3.4e10 * (sms - n), 4.4e12) + s * partials) + 3e-6, (int32_t)n);
+        const double t = beside_of(plan, hq, hkv, shared, s, best.splits, sms).time;
+        if (best_t >= 0 && t >= 0.97 * best_t) continue;           // (more splits have to be worth it)
+        best_t = t;
+        best.prefix_splits = s;
     }
     return best;
 }
@@ -165,7 +187,9 @@ pa_status paged_attn_forward_shared(const pa_plan *plan, const void *q, const vo
         own.ws_o = a.ws_o + (size_t)prefix_splits * rows * value_dim;
         own.ws_lse = a.ws_lse + (size_t)prefix_splits * rows;
         int sms = 0;
-        const int share = pa::device_sms(sms) == cudaSuccess ? layout_of(plan, num_heads, num_kv_heads, shared, sms).sms : 0;
+        const int share = pa::device_sms(sms) == cudaSuccess
+                              ? beside_of(plan, num_heads, num_kv_heads, shared, prefix_splits, splits, sms).sms
+                              : 0;
         side = share > 0 ? pa::side_stream(st) : nullptr;
         if (side) {
             // the prefix first, so that its CTAs hold their SMs; the own keys from the side stream
