@@ -861,6 +861,7 @@ pa_status pa_plan_advance(pa_plan *plan, pa_stream_t stream) {
         if (sl < np + 1) sl = (int32_t)(np + 1);
         plan->max_seq_len = std::max<int64_t>(plan->max_seq_len, sl);
     }
+    for (int c = 0; c < 2; ++c) pa::visible_key_sums(plan, c, 0, plan->keys_tiles[c], plan->keys_decode[c]);
     return PA_OK;
 }
 
