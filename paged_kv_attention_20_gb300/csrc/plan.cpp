@@ -72,6 +72,18 @@ void visible_key_sums(const pa_plan *plan, int causal, int window, double &keys_
     for (int i = 0; i < plan->n_decode; ++i) keys_decode += visible(w[plan->off_decode + i]);
 }
 
+int64_t most_visible_keys(const pa_plan *plan, int causal, int window) {
+    const int32_t *w = plan->words.data();
+    int64_t most = 0;
+    for (int i = 0; i < plan->n_decode; ++i) {
+        const int32_t *m = w + plan->off_qmeta + 4 * (size_t)w[plan->off_decode + i];
+        int64_t lo, hi;
+        pa::visible_range(m[1], w[plan->off_seqlen + m[0]], causal, window, lo, hi);
+        most = std::max(most, hi - lo);
+    }
+    return most;
+}
+
 SideStream *side_stream(cudaStream_t st) {
     thread_local SideStream side[kMaxSideDevices];
     int dev = 0;

@@ -57,6 +57,8 @@ inline bool can_advance(const pa_plan *plan, int32_t s) { return plan->moves[(si
 
 // Visible keys summed over the prefill tiles' queries and over the decode items.
 void visible_key_sums(const pa_plan *plan, int causal, int window, double &keys_tiles, double &keys_decode);
+// Most keys that a decode item sees.
+int64_t most_visible_keys(const pa_plan *plan, int causal, int window);
 
 // A mixed call's decode items can run beside its prefill tiles: the tiles are
 // bound by the tensor core and the softmax, the decode items by HBM, and one

@@ -113,21 +113,18 @@ int q8_sms_beside_prefill(const pa_plan *plan, const AttnArgs &a, int sms) {
 // launch less).
 int32_t q8_splits(const pa_plan *plan, const Q8AttnArgs &x, int sms) {
     const AttnArgs &a = x.a;
-    if (!q8_decode_tc_supported(x)) {
-        const int64_t keys = a.window > 0 ? std::min<int64_t>(plan->max_seq_len, a.window) : plan->max_seq_len;
-        return keys <= 256 ? 1 : a.splits;
-    }
+    const int64_t visible = most_visible_keys(plan, a.causal, a.window);
+    if (!q8_decode_tc_supported(x)) return visible <= 256 ? 1 : a.splits;
     const int32_t pair = a.d == 64 ? 2 : 1, group = a.hq / a.hkv;
     const int64_t columns = (int64_t)pair * group * plan->longest_run;
     const int64_t per = std::min<int64_t>(group, 16 / pair);
     const double items = columns <= 16 ? plan->decode_runs : plan->n_decode;
     const double units = items * ((a.hkv + pair - 1) / pair) * (double)((group + per - 1) / per);
     const double tile = columns <= 4 ? 0.56e-6 : columns <= 8 ? 0.68e-6 : 0.9e-6;
-    double longest = (double)plan->max_seq_len, keys = plan->keys_decode[a.causal], none = 0;
-    if (a.window > 0) {
-        longest = std::min(longest, (double)a.window + plan->longest_run);
-        visible_key_sums(plan, a.causal, a.window, none, keys);
-    }
+    // (under a window a unit of several queries reads a few keys more than one of them sees)
+    const double longest = (double)visible + (a.window > 0 ? plan->longest_run - 1 : 0);
+    double keys = plan->keys_decode[a.causal], none = 0;
+    if (a.window > 0) visible_key_sums(plan, a.causal, a.window, none, keys);
     const double most = longest / 128, mean = keys / plan->n_decode / 128;
     const double merge = (double)plan->queries * a.hq * a.dv * 8 / 4e12;
     int32_t best = 1;

@@ -1,0 +1,47 @@
+"""How many of the splits that a caller allows the 8-bit attention takes."""
+import pytest
+
+from launch_fakes import consecutive, fakes  # noqa: F401
+
+F32, BF16 = 0, 2
+
+
+def taken(fakes, lens, queries, hq=32, hkv=8, splits=16, tensor_cores=True, capturing=False, width=None, **kw):  # noqa: F811
+    """The splits of the decode launch and of the merge (None: no merge)."""
+    table, pool = consecutive(lens, 16)
+    if width:
+        table = [row[:width] + [-1] * (width - len(row)) for row in table]
+    plan = fakes.plan(lens, table, queries, 16, pool)
+    fakes.reset(capturing=capturing, tensor_cores=tensor_cores)
+    assert fakes.forward_q8(plan, hq, hkv, splits=splits, **kw) == 0
+    events = {e.name: e for e in fakes.events()}
+    decode = events.get("q8_decode_tc") or events["q8_decode_any"]
+    return decode.splits, events["merge"].splits if "merge" in events else None
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_window_without_a_causal_end(fakes, dtype):  # noqa: F811
+    """A query at a low position of a long history sees from its window's start to the history's end."""
+    kw = dict(splits=16, dtype=dtype, tensor_cores=dtype == BF16)
+    whole = taken(fakes, [100000], [(0, 99999)], **kw)
+    assert whole[0] > 8 and whole[1] == whole[0]
+    assert taken(fakes, [100000], [(0, 50)], causal=0, window=100, **kw) == whole
+    # at the history's end the window is all there is, and with a causal end always
+    for pos, causal in ((99999, 0), (99999, 1), (50, 1), (5000, 1)):
+        assert taken(fakes, [100000], [(0, pos)], causal=causal, window=100, **kw) == (1, None)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_keys_behind_the_query_do_not_count(fakes, dtype):  # noqa: F811
+    """Early positions of long histories (a prompt checked again, say) are short."""
+    kw = dict(splits=16, dtype=dtype, tensor_cores=dtype == BF16)
+    assert taken(fakes, [100000], [(0, 120)], **kw) == taken(fakes, [121], [(0, 120)], **kw) == (1, None)
+    assert taken(fakes, [100000, 300], [(0, 4000), (1, 20)], **kw) == taken(fakes, [4001, 21], [(0, 4000), (1, 20)], **kw)
+
+
+def test_no_more_than_allowed(fakes):  # noqa: F811
+    for lens in ([131072], [300, 9000, 40000], [200] * 4, [8000] * 64):
+        queries = [(s, n - 1) for s, n in enumerate(lens)]
+        for splits in (1, 2, 5, 64):
+            s, merged = taken(fakes, lens, queries, splits=splits)
+            assert 1 <= s <= splits and merged == (s if s > 1 else None)
