@@ -515,7 +515,8 @@ size_t pa_q8_workspace_bytes(const pa_plan *plan, int32_t num_heads, int32_t num
  * NaN in a key of one KV head reaches its neighbour's outputs for the queries that see the
  * key.  Histories hold at most 2^30 keys (PA_ERR_LIMIT).  splits in 1..PA_MAX_SPLITS: a
  * query's keys are attended in at most that many parts (a plan without prefill tiles in as
- * many of them as end soonest); workspace: at least
+ * many of them as end soonest for the host copy's lengths, and a captured call, whose replays
+ * may see others, for histories that fill their block-table rows); workspace: at least
  * pa_q8_workspace_bytes, 16-byte aligned, not shared by calls that may overlap; what it has
  * beyond the need makes more room for the tiles' histories.  Tiles whose histories do not
  * fit on a replay leave their outputs undefined and set PA_DEVICE_RANGE.  A captured call

@@ -111,9 +111,20 @@ int q8_sms_beside_prefill(const pa_plan *plan, const AttnArgs &a, int sms) {
 // The kernel for other shapes takes the caller's count, but for one or two tiles of 128 keys a query:
 // a second tile takes as long as a merge (4 histories to 200 keys, fp32: 14-18 us either way, and a
 // launch less).
-int32_t q8_splits(const pa_plan *plan, const Q8AttnArgs &x, int sms) {
+// A captured call is replayed for lengths that are not known here; it takes its histories to grow,
+// all by one factor, until the longest fills its row of the block table (one history captured at 200
+// keys with 16 splits and replayed at 32768: 32 us, 161 in the one split that 200 keys need; fp32
+// 128, 1650).
+int32_t q8_splits(const pa_plan *plan, const Q8AttnArgs &x, int sms, bool captured) {
     const AttnArgs &a = x.a;
-    const int64_t visible = most_visible_keys(plan, a.causal, a.window);
+    int64_t visible = most_visible_keys(plan, a.causal, a.window);
+    double grown = 1;
+    if (captured) {
+        const int64_t reach = std::min<int64_t>((int64_t)plan->width * plan->page_size, kMaxCountedKeys);
+        const int64_t most = a.window > 0 && a.causal ? std::min<int64_t>(reach, a.window) : reach;
+        grown = (double)most / (double)std::max<int64_t>(visible, 1);
+        visible = most;
+    }
     if (!q8_decode_tc_supported(x)) return visible <= 256 ? 1 : a.splits;
     const int32_t pair = a.d == 64 ? 2 : 1, group = a.hq / a.hkv;
     const int64_t columns = (int64_t)pair * group * plan->longest_run;
@@ -125,7 +136,7 @@ int32_t q8_splits(const pa_plan *plan, const Q8AttnArgs &x, int sms) {
     const double longest = (double)visible + (a.window > 0 ? plan->longest_run - 1 : 0);
     double keys = plan->keys_decode[a.causal], none = 0;
     if (a.window > 0) visible_key_sums(plan, a.causal, a.window, none, keys);
-    const double most = longest / 128, mean = keys / plan->n_decode / 128;
+    const double most = longest / 128, mean = grown * keys / plan->n_decode / 128;
     const double merge = (double)plan->queries * a.hq * a.dv * 8 / 4e12;
     int32_t best = 1;
     double best_t = 0;
@@ -321,7 +332,11 @@ pa_status paged_attn_forward_q8(const pa_plan *plan, const void *q, const uint8_
     char *const base = static_cast<char *>(ws);
     int sms = 0;
     if (pa::device_sms(sms) != cudaSuccess) sms = 0;
-    if (plan->n_tiles == 0 && splits > 1 && sms > 0) a.splits = pa::q8_splits(plan, x, sms);
+    if (plan->n_tiles == 0 && splits > 1 && sms > 0) {
+        cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+        const bool captured = cudaStreamIsCapturing((cudaStream_t)stream, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone;
+        a.splits = pa::q8_splits(plan, x, sms, captured);
+    }
     if (a.splits > 1) {
         a.ws_o = reinterpret_cast<float *>(base);
         a.ws_lse = reinterpret_cast<float *>(base + (splits * rows * value_dim * sizeof(float) + 255) / 256 * 256);

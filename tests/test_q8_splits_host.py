@@ -39,6 +39,35 @@ def test_keys_behind_the_query_do_not_count(fakes, dtype):  # noqa: F811
     assert taken(fakes, [100000, 300], [(0, 4000), (1, 20)], **kw) == taken(fakes, [4001, 21], [(0, 4000), (1, 20)], **kw)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_captured_calls_may_see_longer_histories(fakes, dtype):  # noqa: F811
+    """As many splits as for histories that fill the block table, whatever the lengths at the capture."""
+    kw = dict(splits=16, dtype=dtype, tensor_cores=dtype == BF16)
+    long = taken(fakes, [32768], [(0, 32767)], **kw)
+    assert long[0] > 8
+    for now in (1, 200, 5000, 32768):
+        assert taken(fakes, [32768], [(0, now - 1)], capturing=True, **kw) == long
+    # one table row grown from 200 keys to what it can hold
+    table = [list(range(2048))]
+    plan = fakes.plan([200], table, [(0, 199)], 16, 2048)
+    fakes.reset(capturing=True, tensor_cores=dtype == BF16)
+    assert fakes.forward_q8(plan, 32, 8, splits=16, dtype=dtype) == 0
+    assert fakes.events()[0].splits == long[0]
+    fakes.reset(tensor_cores=dtype == BF16)
+    assert fakes.forward_q8(plan, 32, 8, splits=16, dtype=dtype) == 0
+    assert fakes.events()[0].splits == 1                      # not captured: by the lengths it has
+    # a window is all that a causal query ever sees
+    assert taken(fakes, [32768], [(0, 199)], capturing=True, window=100, **kw) == (1, None)
+    assert taken(fakes, [32768], [(0, 199)], capturing=True, window=100, causal=0, **kw) == long
+
+
+def test_captured_at_full_length_is_as_not_captured(fakes):  # noqa: F811
+    for lens in ([131072], [8000] * 64, [2000] * 4, [500] * 16, [32768, 50000, 90000, 131072]):
+        queries = [(s, n - 1) for s, n in enumerate(lens)]
+        for hq in (32, 64):
+            assert taken(fakes, lens, queries, hq=hq, splits=64) == taken(fakes, lens, queries, hq=hq, splits=64, capturing=True)
+
+
 def test_no_more_than_allowed(fakes):  # noqa: F811
     for lens in ([131072], [300, 9000, 40000], [200] * 4, [8000] * 64):
         queries = [(s, n - 1) for s, n in enumerate(lens)]
