@@ -502,9 +502,13 @@ pa_status paged_kv_load_q8(const pa_plan *plan, const pa_plan *to_plan, const ui
  * of the tiles' histories in pages of 128 rows.  max_keys: keys that the
  * copy holds at least, all sequences with tiles together, for plans staged later into a
  * captured call (0: the plan's own).  0: no workspace is needed, or invalid arguments.
+ * Enough for every window; a call with a window copies each history from the first block of
+ * 128 keys that a tile's query sees, for which pa_q8_window_workspace_bytes is enough.
  */
 size_t pa_q8_workspace_bytes(const pa_plan *plan, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t value_dim,
                              pa_dtype dtype, int32_t splits, int64_t max_keys);
+size_t pa_q8_window_workspace_bytes(const pa_plan *plan, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                    int32_t value_dim, pa_dtype dtype, int32_t splits, int32_t window, int64_t max_keys);
 
 /*
  * paged_attn_forward_split over the 8-bit cache:
@@ -517,7 +521,7 @@ size_t pa_q8_workspace_bytes(const pa_plan *plan, int32_t num_heads, int32_t num
  * query's keys are attended in at most that many parts (a plan without prefill tiles in as
  * many of them as end soonest for the host copy's lengths, and a captured call, whose replays
  * may see others, for histories that fill their block-table rows); workspace: at least
- * pa_q8_workspace_bytes, 16-byte aligned, not shared by calls that may overlap; what it has
+ * pa_q8_workspace_bytes (under a window pa_q8_window_workspace_bytes), 16-byte aligned, not shared by calls that may overlap; what it has
  * beyond the need makes more room for the tiles' histories.  Tiles whose histories do not
  * fit on a replay leave their outputs undefined and set PA_DEVICE_RANGE.  A captured call
  * stays valid for plan images with the same counts.  Other arguments, shapes and checks as

@@ -33,7 +33,8 @@ EXPORTED = ["pa_last_error", "pa_status_string", "pa_abi_version", "paged_attn_p
             "paged_attn_decode_sms_beside_prefill", "paged_kv_store", "paged_attn_forward",
             "paged_attn_forward_split", "paged_mla_forward", "pa_plan_advance", "pa_time_next_kernel",
             "pa_device_status", "paged_qk_norm_rope_store", "pa_mass_workspace_bytes", "paged_attn_forward_mass",
-            "paged_kv_evict", "paged_kv_store_q8", "paged_kv_load_q8", "pa_q8_workspace_bytes", "paged_attn_forward_q8",
+            "paged_kv_evict", "paged_kv_store_q8", "paged_kv_load_q8", "pa_q8_workspace_bytes", "pa_q8_window_workspace_bytes",
+            "paged_attn_forward_q8",
             "paged_attn_forward_shared", "paged_attn_shared_splits"]
 
 
@@ -113,6 +114,8 @@ def load() -> ctypes.CDLL:
     lib.paged_kv_load_q8.restype = ctypes.c_int
     lib.pa_q8_workspace_bytes.argtypes = [vp, i32, i32, i32, i32, ctypes.c_int, i32, i64]
     lib.pa_q8_workspace_bytes.restype = sz
+    lib.pa_q8_window_workspace_bytes.argtypes = [vp, i32, i32, i32, i32, ctypes.c_int, i32, i32, i64]
+    lib.pa_q8_window_workspace_bytes.restype = sz
     lib.paged_attn_forward_q8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, ctypes.c_float, i32, i32,
                                           ctypes.c_int, vp, sz, i32, vp]
     lib.paged_attn_forward_q8.restype = ctypes.c_int
@@ -647,16 +650,17 @@ def paged_kv_load_q8(plan: Plan, to_plan: Plan, k_cache, v_cache, k_scale, v_sca
 
 
 def q8_workspace_bytes(plan: Plan, heads: int, kv_heads: int, head_dim: int, value_dim: int, splits: int,
-                       dtype=torch.bfloat16, max_keys: int = 0) -> int:
-    return int(load().pa_q8_workspace_bytes(plan.handle, int(heads), int(kv_heads), int(head_dim), int(value_dim),
-                                            _DTYPES[dtype], int(splits), int(max_keys)))
+                       dtype=torch.bfloat16, max_keys: int = 0, window: int = 0) -> int:
+    """Bytes for paged_attn_forward_q8; window: the call's (0: enough for any)."""
+    return int(load().pa_q8_window_workspace_bytes(plan.handle, int(heads), int(kv_heads), int(head_dim), int(value_dim),
+                                                   _DTYPES[dtype], int(splits), int(window), int(max_keys)))
 
 
 def make_q8_workspace(plan: Plan, heads: int, kv_heads: int, head_dim: int, value_dim: int, splits: int,
-                      dtype=torch.bfloat16, max_keys: int = 0, device=None) -> torch.Tensor:
+                      dtype=torch.bfloat16, max_keys: int = 0, device=None, window: int = 0) -> torch.Tensor:
     """Caller-owned workspace of paged_attn_forward_q8 (max_keys: room for the prompt chunks' histories, all together,
-    of plans staged later into a captured call)."""
-    n = q8_workspace_bytes(plan, heads, kv_heads, head_dim, value_dim, splits, dtype, max_keys)
+    of plans staged later into a captured call; window: the call's, 0: enough for any)."""
+    n = q8_workspace_bytes(plan, heads, kv_heads, head_dim, value_dim, splits, dtype, max_keys, window)
     return torch.empty((n + 3) // 4, dtype=torch.float32, device=device or plan.device)
 
 
@@ -681,7 +685,7 @@ def paged_attn_forward_q8(plan: Plan, q, k_cache, v_cache, k_scale, v_scale, sca
     if splits is None:
         splits = paged_attn_split_heuristic(plan, hq, hkv, window=window)
     if workspace is None:
-        workspace = make_q8_workspace(plan, hq, hkv, d, dv, splits, dt, device=k_cache.device)
+        workspace = make_q8_workspace(plan, hq, hkv, d, dv, splits, dt, device=k_cache.device, window=window)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     status = (_LIB or load()).paged_attn_forward_q8(

@@ -215,8 +215,8 @@ struct Q8StoreArgs {
 cudaError_t launch_q8_store(const Q8StoreArgs &a, cudaStream_t st);
 
 // Rows of the 8-bit cache into a paged cache of `dtype`: to the pages of another plan, or
-// (first_page) the sequences with prefill tiles to pages of to_page_size rows one behind the
-// other, whose block table to_table_out is written too.
+// (places) the sequences with prefill tiles, from the first page that a tile's query sees, to
+// pages of to_page_size rows one behind the other, whose block table to_table_out is written too.
 constexpr int32_t kQ8NoTiles = -1, kQ8NoRoom = -2;
 struct Q8LoadArgs {
     PlanView plan;
@@ -224,17 +224,17 @@ struct Q8LoadArgs {
     void *k_to, *v_to;
     const int32_t *to_table, *to_lens;
     int32_t to_width, to_page_size;
-    const int32_t *first_page;              // [sequences]: first page, kQ8NoTiles or kQ8NoRoom; or null
-    int32_t *to_table_out;                  // [sequences, to_width]
+    const int2 *places;                     // [sequences]: {page of the first one seen, kQ8NoTiles or kQ8NoRoom, which it is}; or null
+    int32_t *to_table_out;                  // [sequences, to_width], entries before the first one seen are not written
     int32_t hkv, d, dv;
     pa_dtype dtype;
     int32_t *status;
 };
-// longest: of the host copies (grid sizing only)
+// longest: keys read, of the host copies (grid sizing only)
 cudaError_t launch_q8_load(const Q8LoadArgs &a, int longest, cudaStream_t st);
-// first_page of every sequence for `room` pages of page_size rows; PA_DEVICE_RANGE where they do not suffice.
-cudaError_t launch_q8_first_pages(const PlanView &plan, int32_t *first_page, int32_t page_size, int32_t room, int32_t *status,
-                                  cudaStream_t st);
+// places of every sequence in `room` pages of page_size rows; PA_DEVICE_RANGE where they do not suffice.
+cudaError_t launch_q8_places(const PlanView &plan, int2 *places, int32_t window, int32_t page_size, int32_t room, int32_t *status,
+                             cudaStream_t st);
 
 // Attention over the 8-bit cache: a.k and a.v are the e4m3 caches, q and out of a.dtype.
 struct Q8AttnArgs {

@@ -384,15 +384,14 @@ pa_status paged_attn_plan(const int32_t *seq_lens, int32_t num_seqs, const int32
     }
 
     {
-        std::vector<uint8_t> seen((size_t)num_seqs, 0);
+        std::vector<int32_t> lowest((size_t)num_seqs, INT32_MAX);
         for (int t = 0; t < p->n_tiles; ++t) {
             const int32_t s = tiles[4 * (size_t)t];
-            if (seen[(size_t)s]) continue;
-            seen[(size_t)s] = 1;
-            ++p->tile_sequences;
-            p->tile_blocks += ((int64_t)seq_lens[s] + 127) / 128;
+            lowest[(size_t)s] = std::min(lowest[(size_t)s], tiles[4 * (size_t)t + 3]);
             p->tile_longest = std::max<int64_t>(p->tile_longest, seq_lens[s]);
         }
+        for (int32_t s = 0; s < num_seqs; ++s)
+            if (lowest[(size_t)s] != INT32_MAX) p->tile_starts.emplace_back(s, lowest[(size_t)s]);
     }
 
     // Word layout (int32 words; 16-byte aligned sections):

@@ -13,8 +13,8 @@ struct pa_plan {
     int32_t queries = 0, sequences = 0, width = 0, page_size = 0, pages = 0;
     int32_t n_decode = 0, n_tiles = 0, n_tile_queries = 0;
     int64_t max_seq_len = 0;          // longest sequence any decode item reads
-    int64_t tile_blocks = 0, tile_longest = 0;   // of the sequences with prefill tiles: blocks of 128 keys, the longest's keys
-    int32_t tile_sequences = 0;
+    int64_t tile_longest = 0;         // keys of the longest sequence with prefill tiles
+    std::vector<std::pair<int32_t, int32_t>> tile_starts;   // sequences with prefill tiles, the lowest position of their queries
     int32_t longest_run = 1, decode_runs = 0;    // of decode items at consecutive positions of a sequence
     std::vector<int32_t> words;       // host copy of the device metadata
     size_t off_qmeta = 0, off_seqlen = 0, off_table = 0, off_decode = 0, off_tiles = 0, off_order = 0;

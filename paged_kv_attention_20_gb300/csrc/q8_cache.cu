@@ -6,6 +6,7 @@
 // row's maximum before its first element can be written; a group of lanes holds the
 // row in registers meanwhile, 16 elements a lane, so that a lane writes 16 bytes.
 
+#include <climits>
 #include <type_traits>
 
 #include "per_device.h"
@@ -219,17 +220,18 @@ __global__ void __launch_bounds__(kThreads, 8) load_kernel(Q8LoadArgs a, int blo
     griddep_launch();
     const int ps = a.plan.page_size;
     for (int s = blockIdx.y; s < a.plan.sequences; s += gridDim.y) {
-        int n = a.plan.seq_lens[s], first = 0;
-        if (a.first_page) {
-            first = a.first_page[s];
-            if (first == kQ8NoTiles) continue;
+        int n = a.plan.seq_lens[s];
+        int2 place = make_int2(0, 0);
+        if (a.places) {
+            place = a.places[s];
+            if (place.x == kQ8NoTiles) continue;
         } else {
             const int m = a.to_lens[s];
             if (m > n && blockIdx.x == 0 && threadIdx.x == 0) atomicCAS(a.status, 0, PA_DEVICE_RANGE);
             n = m < n ? m : n;
         }
         const int32_t *row = a.plan.table + (int64_t)s * a.plan.width;
-        for (int64_t j0 = (int64_t)blockIdx.x * block_keys; j0 < n; j0 += (int64_t)gridDim.x * block_keys) {
+        for (int64_t j0 = (int64_t)place.y * a.to_page_size + (int64_t)blockIdx.x * block_keys; j0 < n; j0 += (int64_t)gridDim.x * block_keys) {
             const int keys = n - j0 < block_keys ? (int)(n - j0) : block_keys;
             __syncthreads();               // the rows of the round before are read
             if ((int)threadIdx.x < keys) {
@@ -240,9 +242,9 @@ __global__ void __launch_bounds__(kThreads, 8) load_kernel(Q8LoadArgs a, int blo
                 scale_at[threadIdx.x] = page * a.hkv * ps + r;
                 const int tg = j / a.to_page_size, tr = j - tg * a.to_page_size;
                 int32_t to;
-                if (a.first_page) {
+                if (a.places) {
                     // without room for the sequence nothing is written and its table names the first page
-                    to = first == kQ8NoRoom ? 0 : first + tg;
+                    to = place.x == kQ8NoRoom ? 0 : place.x + (tg - place.y);
                     if (tr == 0 || j == (int)j0) a.to_table_out[(int64_t)s * a.to_width + tg] = to;
                 } else {
                     to = a.to_table[(int64_t)s * a.to_width + tg];
@@ -250,30 +252,32 @@ __global__ void __launch_bounds__(kThreads, 8) load_kernel(Q8LoadArgs a, int blo
                 to_row[threadIdx.x] = (int64_t)to * a.to_page_size + tr;
             }
             __syncthreads();
-            if (first == kQ8NoRoom) continue;
+            if (place.x == kQ8NoRoom) continue;
             read_rows<T, E>(a.k, a.k_scale, static_cast<T *>(a.k_to), a.hkv, a.d, ps, from_row, scale_at, to_row, keys);
             read_rows<T, E>(a.v, a.v_scale, static_cast<T *>(a.v_to), a.hkv, a.dv, ps, from_row, scale_at, to_row, keys);
         }
     }
 }
 
-// First page of every sequence with prefill tiles in a run of pages that holds them all:
-// one block, sequences in their order.
-__global__ void __launch_bounds__(1024) first_pages_kernel(PlanView plan, int32_t *first_page, int32_t page_size, int32_t room,
-                                                           int32_t *status) {
+// Place of every sequence with prefill tiles in a run of pages that holds what their queries see:
+// one block, sequences in their order.  (The places are read around L1, which the atomics pass.)
+__global__ void __launch_bounds__(1024) places_kernel(PlanView plan, int2 *places, int32_t window, int32_t page_size, int32_t room,
+                                                      int32_t *status) {
     __shared__ int32_t warp_sum[32];
     griddep_wait();
     griddep_launch();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int s = tid; s < plan.sequences; s += 1024) first_page[s] = 0;
+    for (int s = tid; s < plan.sequences; s += 1024) places[s].y = INT_MAX;
     __syncthreads();
-    for (int t = tid; t < plan.n_tiles; t += 1024) first_page[plan.tiles[t].x] = 1;
+    for (int t = tid; t < plan.n_tiles; t += 1024) atomicMin(&places[plan.tiles[t].x].y, plan.tiles[t].w);
     __syncthreads();
     int64_t before = 0;
     for (int s0 = 0; s0 < plan.sequences; s0 += 1024) {
         const int s = s0 + tid;
-        const bool tiles = s < plan.sequences && first_page[s] != 0;
-        const int pages = tiles ? (int)(((int64_t)plan.seq_lens[s] + page_size - 1) / page_size) : 0;
+        const int lowest = s < plan.sequences ? __ldcg(&places[s].y) : INT_MAX;
+        const bool tiles = lowest != INT_MAX;
+        const int first = tiles && window > 0 && lowest >= window ? (lowest - window + 1) / page_size : 0;
+        const int pages = tiles ? (int)(((int64_t)plan.seq_lens[s] + page_size - 1) / page_size) - first : 0;
         int sum = pages;
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, sum, o);
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(1024) first_pages_kernel(PlanView plan, int32_
         at += sum - pages;
         if (s < plan.sequences) {
             const bool fits = at + pages <= room;
-            first_page[s] = !tiles ? kQ8NoTiles : fits ? (int32_t)at : kQ8NoRoom;
+            places[s] = make_int2(!tiles ? kQ8NoTiles : fits ? (int32_t)at : kQ8NoRoom, first);
             if (tiles && !fits) atomicCAS(status, 0, PA_DEVICE_RANGE);
         }
         before += all;
@@ -333,9 +337,9 @@ cudaError_t launch_q8_load(const Q8LoadArgs &a, int longest, cudaStream_t st) {
     }
 }
 
-cudaError_t launch_q8_first_pages(const PlanView &plan, int32_t *first_page, int32_t page_size, int32_t room, int32_t *status,
-                                  cudaStream_t st) {
-    return launch_pdl(first_pages_kernel, dim3(1), dim3(1024), 0, st, plan, first_page, page_size, room, status);
+cudaError_t launch_q8_places(const PlanView &plan, int2 *places, int32_t window, int32_t page_size, int32_t room, int32_t *status,
+                             cudaStream_t st) {
+    return launch_pdl(places_kernel, dim3(1), dim3(1024), 0, st, plan, places, window, page_size, room, status);
 }
 
 }  // namespace pa

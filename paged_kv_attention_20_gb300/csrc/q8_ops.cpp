@@ -21,12 +21,30 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 // boxes then (1149 TFLOP/s on the mixed step's chunks, 1030 with pages of 16).
 constexpr int32_t kCopyPage = 128;
 
+// Of the histories of sequences with tiles, from the first block of 128 keys that a tile's query
+// sees: their blocks, and the keys of the longest.
+struct CopiedKeys {
+    int64_t blocks = 0, longest = 0;
+};
+
+CopiedKeys copied_keys(const pa_plan *plan, int32_t window) {
+    CopiedKeys c;
+    for (const auto &[seq, pos] : plan->tile_starts) {
+        const int64_t len = plan->words[plan->off_seqlen + seq];
+        const int64_t first = window > 0 ? std::max<int64_t>(0, (int64_t)pos - window + 1) / kCopyPage : 0;
+        c.blocks += (len + kCopyPage - 1) / kCopyPage - first;
+        c.longest = std::max(c.longest, len - first * kCopyPage);
+    }
+    return c;
+}
+
 struct Q8Layout {
     bool tiles;
     int32_t width;                        // of the copy's block table
-    size_t first_page, table, k, bytes;   // the values follow the keys
+    size_t places, table, k, bytes;       // the values follow the keys
     size_t page_bytes;                    // of one page of one tensor
     int64_t room;                         // pages
+    CopiedKeys copied;
 };
 
 bool tiles_on_tensor_cores(const pa_plan *plan, int32_t d, int32_t dv, pa_dtype dtype) {
@@ -35,17 +53,18 @@ bool tiles_on_tensor_cores(const pa_plan *plan, int32_t d, int32_t dv, pa_dtype 
 
 // max_keys: keys the copy holds at least, over all sequences with tiles; 0: the host copy's.
 Q8Layout q8_layout(const pa_plan *plan, int32_t hq, int32_t hkv, int32_t d, int32_t dv, pa_dtype dtype, int32_t splits,
-                   int64_t max_keys) {
+                   int32_t window, int64_t max_keys) {
     Q8Layout l{};
     l.tiles = tiles_on_tensor_cores(plan, d, dv, dtype);
     l.bytes = splits > 1 ? align256(pa_workspace_bytes(plan->queries, hq, dv, splits)) : 0;
     if (!l.tiles) return l;
-    l.first_page = l.bytes;
-    l.table = l.first_page + align256((size_t)plan->sequences * sizeof(int32_t));
+    l.copied = copied_keys(plan, window);
+    l.places = l.bytes;
+    l.table = l.places + align256((size_t)plan->sequences * sizeof(int2));
     l.width = (int32_t)((std::min<int64_t>((int64_t)plan->width * plan->page_size, INT32_MAX) + kCopyPage - 1) / kCopyPage);
     l.k = l.table + align256((size_t)plan->sequences * l.width * sizeof(int32_t));
     l.page_bytes = (size_t)kCopyPage * hkv * 128 * 2;
-    l.room = std::max<int64_t>(plan->tile_blocks, (max_keys + kCopyPage - 1) / kCopyPage + plan->tile_sequences);
+    l.room = std::max<int64_t>(l.copied.blocks, (max_keys + kCopyPage - 1) / kCopyPage + (int64_t)plan->tile_starts.size());
     l.bytes = l.k + 2 * (size_t)l.room * l.page_bytes;
     return l;
 }
@@ -77,14 +96,14 @@ namespace {
 // share is taken that ends both soonest, when it saves at least 5 % and both are long enough
 // for the fork and join to be noise (the mixed step: 282 us with 52 SMs, 311 one after the
 // other).
-int q8_sms_beside_prefill(const pa_plan *plan, const AttnArgs &a, int sms) {
+int q8_sms_beside_prefill(const pa_plan *plan, const AttnArgs &a, int64_t copied_blocks, int sms) {
     constexpr double kFlopsPerSm = 6.5e12, kBytesPerSm = 4.8e10, kHbmBytes = 6.0e12, kCopyBytes = 4.0e12;
     if (plan->n_decode == 0 || plan->n_tiles == 0 || sms < 8) return 0;
     double keys_p = plan->keys_tiles[a.causal], keys_d = plan->keys_decode[a.causal];
     if (a.window > 0) visible_key_sums(plan, a.causal, a.window, keys_p, keys_d);
     const double flops = keys_p * a.hq * 4.0 * 128, bytes = keys_d * a.hkv * 258.0;
     // the copy comes before the tiles, beside the decode items: a byte read and two written
-    const double t_copy = (double)plan->tile_blocks * kCopyPage * a.hkv * 256.0 * 3 / kCopyBytes;
+    const double t_copy = (double)copied_blocks * kCopyPage * a.hkv * 256.0 * 3 / kCopyBytes;
     const double t_prefill = flops / (kFlopsPerSm * sms), t_decode = bytes / kHbmBytes;
     if (t_prefill < 20e-6 || t_decode < 20e-6) return 0;
     double best = t_copy + t_prefill + t_decode;
@@ -270,12 +289,17 @@ pa_status paged_kv_load_q8(const pa_plan *plan, const pa_plan *to_plan, const ui
 
 size_t pa_q8_workspace_bytes(const pa_plan *plan, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t value_dim,
                              pa_dtype dtype, int32_t splits, int64_t max_keys) {
+    return pa_q8_window_workspace_bytes(plan, num_heads, num_kv_heads, head_dim, value_dim, dtype, splits, 0, max_keys);
+}
+
+size_t pa_q8_window_workspace_bytes(const pa_plan *plan, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                    int32_t value_dim, pa_dtype dtype, int32_t splits, int32_t window, int64_t max_keys) {
     if (!plan || !pa::valid_dtype(dtype) || num_heads < 1 || num_heads > 65535 || num_kv_heads < 1 ||
         num_heads % num_kv_heads || head_dim < 1 || head_dim > PA_MAX_HEAD_DIM || value_dim < 1 ||
-        value_dim > PA_MAX_HEAD_DIM || splits < 1 || splits > PA_MAX_SPLITS || max_keys < 0 || max_keys > INT32_MAX ||
+        value_dim > PA_MAX_HEAD_DIM || splits < 1 || splits > PA_MAX_SPLITS || window < 0 || max_keys < 0 || max_keys > INT32_MAX ||
         !pa::mass_rows_fit(plan, num_heads, splits))
         return 0;
-    return pa::q8_layout(plan, num_heads, num_kv_heads, head_dim, value_dim, dtype, splits, max_keys).bytes;
+    return pa::q8_layout(plan, num_heads, num_kv_heads, head_dim, value_dim, dtype, splits, window, max_keys).bytes;
 }
 
 pa_status paged_attn_forward_q8(const pa_plan *plan, const void *q, const uint8_t *k_cache, const uint8_t *v_cache,
@@ -293,7 +317,7 @@ pa_status paged_attn_forward_q8(const pa_plan *plan, const void *q, const uint8_
     if (splits < 1 || splits > PA_MAX_SPLITS) BAD(PA_ERR_SPLITS, "splits must be in 1..64");
     if (!pa::mass_rows_fit(plan, num_heads, splits)) BAD(PA_ERR_LIMIT, "more than 2^31 - 1 (query, head, split) rows");
     const pa::Q8Layout lay =
-        pa::q8_layout(plan, num_heads, num_kv_heads, head_dim, value_dim, dtype, splits, 0);
+        pa::q8_layout(plan, num_heads, num_kv_heads, head_dim, value_dim, dtype, splits, window, 0);
     if (std::max(plan->max_seq_len, plan->tile_longest) > pa::kMaxCountedKeys) BAD(PA_ERR_LIMIT, "history above 2^30 keys");
     if (splits > 1 && pa_workspace_bytes(plan->queries, num_heads, value_dim, splits) > PA_WORKSPACE_LIMIT_BYTES)
         BAD(PA_ERR_WORKSPACE, "split partials above the 1 GiB limit");
@@ -363,9 +387,9 @@ pa_status paged_attn_forward_q8(const pa_plan *plan, const void *q, const uint8_
         wide.plan.pages = (int32_t)room;
     }
     if (lay.tiles && pa::prefill_supported(wide)) {
-        int32_t *first = reinterpret_cast<int32_t *>(base + lay.first_page);
+        int2 *const places = reinterpret_cast<int2 *>(base + lay.places);
         // the decode items beside the copy and the tiles, on SMs of their own
-        const int beside = pa::q8_sms_beside_prefill(plan, a, sms);
+        const int beside = pa::q8_sms_beside_prefill(plan, a, lay.copied.blocks, sms);
         pa::SideStream *side = beside > 0 ? pa::side_stream(st) : nullptr;
         bool forked = false;
         if (side) {
@@ -375,19 +399,19 @@ pa_status paged_attn_forward_q8(const pa_plan *plan, const void *q, const uint8_
             forked = e == cudaSuccess;
             if (e == cudaSuccess) e = pa::launch_q8_decode(x, true, plan->longest_run, side->stream);
         }
-        if (e == cudaSuccess) e = pa::launch_q8_first_pages(a.plan, first, pa::kCopyPage, wide.plan.pages, a.status, st);
+        if (e == cudaSuccess) e = pa::launch_q8_places(a.plan, places, window, pa::kCopyPage, wide.plan.pages, a.status, st);
         pa::Q8LoadArgs c{};
         c.plan = a.plan;
         c.k = k_cache; c.v = v_cache; c.k_scale = k_scale; c.v_scale = v_scale;
         c.k_to = const_cast<void *>(wide.k); c.v_to = const_cast<void *>(wide.v);
-        c.first_page = first;
+        c.places = places;
         c.to_table_out = reinterpret_cast<int32_t *>(base + lay.table);
         c.to_width = lay.width;
         c.to_page_size = pa::kCopyPage;
         c.hkv = num_kv_heads; c.d = head_dim; c.dv = value_dim;
         c.dtype = dtype;
         c.status = a.status;
-        if (e == cudaSuccess) e = pa::launch_q8_load(c, (int)plan->tile_longest, st);
+        if (e == cudaSuccess) e = pa::launch_q8_load(c, (int)lay.copied.longest, st);
         mark(t0);
         if (e == cudaSuccess) e = pa::launch_prefill(wide, st);
         mark(t1);

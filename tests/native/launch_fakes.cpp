@@ -106,8 +106,8 @@ cudaError_t launch_mass_recompute(const MassArgs &, cudaStream_t st) { return no
 cudaError_t launch_evict(const EvictArgs &, int, int, bool, cudaStream_t st) { return note("evict", st); }
 cudaError_t launch_q8_store(const Q8StoreArgs &, cudaStream_t st) { return note("q8_store", st); }
 cudaError_t launch_q8_load(const Q8LoadArgs &, int longest, cudaStream_t st) { return note("q8_load", st, 0, 0, longest); }
-cudaError_t launch_q8_first_pages(const PlanView &, int32_t *, int32_t page_size, int32_t room, int32_t *, cudaStream_t st) {
-    return note("q8_first_pages", st, 0, 0, room, page_size);
+cudaError_t launch_q8_places(const PlanView &, int2 *, int32_t window, int32_t, int32_t room, int32_t *, cudaStream_t st) {
+    return note("q8_places", st, 0, 0, room, window);
 }
 cudaError_t launch_q8_decode_any(const Q8AttnArgs &q, bool, cudaStream_t st) { return note("q8_decode_any", st, q.a.splits, q.a.max_ctas); }
 cudaError_t launch_q8_decode_tc(const Q8AttnArgs &q, bool, int, cudaStream_t st) { return note("q8_decode_tc", st, q.a.splits, q.a.max_ctas); }

@@ -20,7 +20,7 @@ def behind_a_prefix(fakes):
 
 
 CALLS = {
-    "8-bit": (mixed, lambda f, p: f.forward_q8(p, 32, 8, splits=2), ["q8_first_pages", "q8_load", "prefill", "q8_decode_tc", "merge"]),
+    "8-bit": (mixed, lambda f, p: f.forward_q8(p, 32, 8, splits=2), ["q8_places", "q8_load", "prefill", "q8_decode_tc", "merge"]),
     "16-bit": (mixed, lambda f, p: f.forward(p, 32, 8, splits=2), ["prefill", "decode", "merge"]),
     "shared": (behind_a_prefix, lambda f, p: f.forward_shared(p, 32, 8, 16384, (4, 1)), ["prefix", "decode", "merge"]),
 }
