@@ -89,7 +89,16 @@ SideStream *side_stream(cudaStream_t st) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxSideDevices) return nullptr;
     SideStream &ss = side[dev];
-    if (ss.stream) return &ss;
+    if (ss.stream) {
+        // A capture keeps the streams that joined it until it ends: a call on another stream
+        // meanwhile, waited for by one of them, would invalidate it.
+        cudaStreamCaptureStatus its = cudaStreamCaptureStatusNone, the_calls = cudaStreamCaptureStatusNone;
+        unsigned long long a = 0, b = 0;
+        if (cudaStreamGetCaptureInfo(ss.stream, &its, &a, nullptr, nullptr, nullptr, nullptr) != cudaSuccess) return nullptr;
+        if (its == cudaStreamCaptureStatusNone) return &ss;
+        if (cudaStreamGetCaptureInfo(st, &the_calls, &b, nullptr, nullptr, nullptr, nullptr) != cudaSuccess) return nullptr;
+        return its == cudaStreamCaptureStatusActive && the_calls == its && a == b ? &ss : nullptr;
+    }
     if (ss.failed) return nullptr;
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(st, &cap) != cudaSuccess || cap != cudaStreamCaptureStatusNone) return nullptr;

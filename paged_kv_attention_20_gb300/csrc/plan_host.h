@@ -72,7 +72,8 @@ struct SideStream {
     cudaEvent_t fork = nullptr, join = nullptr;
     bool failed = false;
 };
-// The calling thread's on the current device; null where there is none yet and `st` is being captured.
+// The calling thread's on the current device; null where there is none yet and `st` is being captured,
+// and where it belongs to a capture that is not `st`'s.
 SideStream *side_stream(cudaStream_t st);
 // What is put on the side stream from here on comes after what `st` holds.
 cudaError_t fork_side(SideStream &side, cudaStream_t st);

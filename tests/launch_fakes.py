@@ -30,9 +30,13 @@ class Fakes:
         i64 = ctypes.c_int64
         self.lib.fake_event.argtypes = [ctypes.c_int, ctypes.POINTER(i64), ctypes.POINTER(i64), ctypes.POINTER(i64)]
         self.lib.fake_event.restype = ctypes.c_char_p
+        self.lib.fake_capture.argtypes = [i64, i64]
+        self.stream = STREAM
 
     def reset(self, fails: str = "", capturing: bool = False, tensor_cores: bool = True) -> None:
-        self.lib.fake_reset(fails.encode(), int(capturing), int(tensor_cores))
+        self.lib.fake_reset(fails.encode(), int(tensor_cores))
+        self.lib.fake_capture(STREAM, int(capturing))
+        self.stream = STREAM
 
     def events(self) -> list[Event]:
         found = []
@@ -58,17 +62,17 @@ class Fakes:
     def forward_q8(self, plan, hq, hkv, d=128, splits=1, causal=1, window=0, dtype=2, ws_bytes=SIZE):
         q, k, v, ks, vs, out, ws = self.operands(7)
         return self.lib.paged_attn_forward_q8(plan, q, k, v, ks, vs, out, hq, hkv, d, d, 0.1, causal, window, dtype, ws, ws_bytes,
-                                              splits, STREAM)
+                                              splits, self.stream)
 
     def forward_shared(self, plan, hq, hkv, shared, splits, d=128, causal=1, dtype=2):
         q, k, v, out, ws = self.operands(5)
         return self.lib.paged_attn_forward_shared(plan, q, k, v, out, hq, hkv, d, d, 0.1, causal, shared, dtype, ws, SIZE,
-                                                  splits[0], splits[1], STREAM)
+                                                  splits[0], splits[1], self.stream)
 
     def forward(self, plan, hq, hkv, d=128, splits=1, causal=1, window=0, dtype=2):
         q, k, v, out, ws = self.operands(5)
         return self.lib.paged_attn_forward_split(plan, q, k, v, out, hq, hkv, d, d, 0.1, causal, window, dtype, ws, SIZE, splits,
-                                                 STREAM)
+                                                 self.stream)
 
 
 @pytest.fixture(scope="session")

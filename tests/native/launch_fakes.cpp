@@ -3,6 +3,7 @@
 // kernels a call launches, on which stream, with how many splits and CTAs, and what it does when a
 // launch fails.  Test infrastructure only: nothing in the library uses it.
 #include <cstring>
+#include <map>
 #include <vector>
 
 #include "pa_internal.h"
@@ -17,7 +18,8 @@ struct Event {
 
 std::vector<Event> g_events;
 char g_fails[64] = "";
-int g_capturing = 0, g_tensor_cores = 1;
+int g_tensor_cores = 1;
+std::map<int64_t, int64_t> g_capture, g_event_capture;      // of a stream, of the last record of an event (0: none)
 int64_t g_handles = 0;
 
 int64_t id(const void *p) { return (int64_t)reinterpret_cast<uintptr_t>(p); }
@@ -33,12 +35,14 @@ cudaError_t note(const char *name, cudaStream_t st, int64_t a = 0, int64_t b = 0
 
 extern "C" {
 
-void fake_reset(const char *fails, int capturing, int tensor_cores) {
+void fake_reset(const char *fails, int tensor_cores) {
     g_events.clear();
+    g_capture.clear();
+    g_event_capture.clear();
     std::strncpy(g_fails, fails, sizeof g_fails - 1);
-    g_capturing = capturing;
     g_tensor_cores = tensor_cores;
 }
+void fake_capture(int64_t stream, int64_t capture) { g_capture[stream] = capture; }
 int fake_events() { return (int)g_events.size(); }
 const char *fake_event(int i, int64_t *stream, int64_t *event, int64_t *value) {
     const Event &e = g_events[(size_t)i];
@@ -66,11 +70,25 @@ cudaError_t cudaEventCreateWithFlags(cudaEvent_t *ev, unsigned) {
 }
 cudaError_t cudaEventDestroy(cudaEvent_t) { return cudaSuccess; }
 cudaError_t cudaStreamDestroy(cudaStream_t) { return cudaSuccess; }
-cudaError_t cudaStreamIsCapturing(cudaStream_t, cudaStreamCaptureStatus *s) {
-    return *s = g_capturing ? cudaStreamCaptureStatusActive : cudaStreamCaptureStatusNone, cudaSuccess;
+cudaError_t cudaStreamIsCapturing(cudaStream_t st, cudaStreamCaptureStatus *s) {
+    return *s = g_capture[id(st)] ? cudaStreamCaptureStatusActive : cudaStreamCaptureStatusNone, cudaSuccess;
 }
-cudaError_t cudaEventRecord(cudaEvent_t ev, cudaStream_t st) { return note("record", st, 0, 0, 0, 0, ev); }
-cudaError_t cudaStreamWaitEvent(cudaStream_t st, cudaEvent_t ev, unsigned) { return note("wait", st, 0, 0, 0, 0, ev); }
+cudaError_t cudaStreamGetCaptureInfo(cudaStream_t st, cudaStreamCaptureStatus *s, unsigned long long *capture, cudaGraph_t *,
+                                     const cudaGraphNode_t **, const cudaGraphEdgeData **, size_t *) {
+    *capture = (unsigned long long)g_capture[id(st)];
+    return cudaStreamIsCapturing(st, s);
+}
+cudaError_t cudaEventRecord(cudaEvent_t ev, cudaStream_t st) {
+    g_event_capture[id(ev)] = g_capture[id(st)];
+    return note("record", st, 0, 0, 0, 0, ev);
+}
+// A stream joins the capture of what it waits for; one that is in another capture may not.
+cudaError_t cudaStreamWaitEvent(cudaStream_t st, cudaEvent_t ev, unsigned) {
+    const int64_t capture = g_event_capture[id(ev)];
+    if (g_capture[id(st)] && g_capture[id(st)] != capture) return cudaErrorStreamCaptureIsolation;
+    g_capture[id(st)] = capture;
+    return note("wait", st, 0, 0, 0, 0, ev);
+}
 
 }  // extern "C"
 

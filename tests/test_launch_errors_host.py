@@ -59,3 +59,26 @@ def test_side_stream_is_joined(fakes, name, capturing):  # noqa: F811
         assert call(fakes, plan) == CUDA
         assert not beside(fakes.events()), fails
         assert b"a fake's error" in fakes.lib.pa_last_error()
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_calls_during_a_capture_of_another_stream(fakes, name):  # noqa: F811
+    """The second stream stays with the capture that it joined until that ends; other calls of the thread do without it."""
+    build, call, launches = CALLS[name]
+    plan = build(fakes)
+    fakes.reset()
+    assert call(fakes, plan) == 0                     # (it is there)
+    fakes.reset(capturing=True)
+    assert call(fakes, plan) == 0
+    for stream, capture in ((78, 0), (79, 2), (STREAM, 1), (78, 0)):
+        seen = len(fakes.events())
+        fakes.lib.fake_capture(stream, capture)
+        fakes.stream = stream
+        assert call(fakes, plan) == 0
+        events = fakes.events()[seen:]
+        assert sorted(e.name for e in events if e.name not in ("record", "wait")) == sorted(launches)
+        beside_it = {e.stream for e in events} - {stream}
+        assert bool(beside_it) == (stream == STREAM)
+    fakes.reset()                                     # the captures have ended
+    fakes.stream = 78
+    assert call(fakes, plan) == 0 and {e.stream for e in fakes.events()} != {78}
