@@ -548,9 +548,11 @@ pa_status paged_attn_forward_q8(const pa_plan *plan, const void *q, const uint8_
  * workspace: >= pa_workspace_bytes(queries, num_heads, value_dim, prefix_splits + splits),
  * 16-byte aligned, not shared by calls that may overlap; prefix_splits + splits <=
  * PA_MAX_SPLITS.  The prefix has a kernel of its own for 16-bit operands, head dims of 128,
- * pages of 16, 32, 64 or 128 rows and groups of up to 128 heads; other shapes, and all with
- * prefix_splits 0, attend to all keys of every sequence in prefix_splits + splits splits.  A captured call stays valid for plan images
- * with the same counts whose sequences share the prefix.
+ * pages of 16, 32, 64 or 128 rows and groups of up to 128 heads, which rounds the prefix's
+ * weights to the operand type for their product with the values; other shapes, and all with
+ * prefix_splits 0, attend to all keys of every sequence in prefix_splits + splits splits (for
+ * which paged_attn_split_heuristic's count is the better one).  A captured call stays valid
+ * for plan images with the same counts whose sequences share the prefix.
  */
 pa_status paged_attn_forward_shared(const pa_plan *plan, const void *q, const void *k_cache, const void *v_cache, void *out,
                                     int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t value_dim, float scale,
@@ -558,9 +560,9 @@ pa_status paged_attn_forward_shared(const pa_plan *plan, const void *q, const vo
                                     int32_t prefix_splits, int32_t splits, pa_stream_t stream);
 
 /*
- * Split counts for paged_attn_forward_shared on a GPU of num_sms SMs: out[0] for the
- * prefix (0: so short that each sequence better reads it itself), out[1] for the
- * sequences' own keys.
+ * Split counts for paged_attn_forward_shared on a GPU of num_sms SMs, for shapes with a
+ * kernel for the prefix: out[0] for the prefix (0: so short that each sequence better reads
+ * it itself), out[1] for the sequences' own keys.
  */
 pa_status paged_attn_shared_splits(const pa_plan *plan, int32_t num_heads, int32_t num_kv_heads, int32_t shared,
                                    int32_t num_sms, int32_t out[2]);

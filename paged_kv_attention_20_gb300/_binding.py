@@ -711,8 +711,9 @@ def paged_attn_shared_splits(plan: Plan, num_heads: int, num_kv_heads: int, shar
 def paged_attn_forward_shared(plan: Plan, q, k_cache, v_cache, scale: float, shared: int, splits=None, workspace=None,
                               causal: bool = True, out=None):
     """Paged attention of a batch whose sequences hold the same pages for their first `shared` keys (a multiple of the
-    page size): those are read once for all queries.  splits is the pair of paged_attn_shared_splits (the default); the
-    workspace (make_workspace for their sum) is allocated here when not given."""
+    page size): those are read once for all queries.  splits defaults to the pair of paged_attn_shared_splits, and for
+    shapes without a kernel for the prefix to (0, the split heuristic's); the workspace (make_workspace for their sum) is
+    allocated here when not given."""
     dt, code, index, (pages, ps, hkv, d), dv = _caches(plan, k_cache, v_cache)
     n, hq, dq = _dense(q, "q", dt, index, 3)
     if n != plan.queries or dq != d:
@@ -722,7 +723,9 @@ def paged_attn_forward_shared(plan: Plan, q, k_cache, v_cache, scale: float, sha
     elif _dense(out, "out", dt, index, 3) != (n, hq, dv):
         raise ValueError(f"out must have shape {(n, hq, dv)}")
     if splits is None:
-        splits = paged_attn_shared_splits(plan, hq, hkv, shared)
+        with_kernel = dt != torch.float32 and d == dv == 128 and ps in (16, 32, 64, 128) and hq // hkv <= 128
+        splits = paged_attn_shared_splits(plan, hq, hkv, shared) if with_kernel else \
+            (0, paged_attn_split_heuristic(plan, hq, hkv))
     prefix_splits, own_splits = splits
     if workspace is None:
         workspace = make_workspace(plan, hq, dv, prefix_splits + own_splits, k_cache.device)
