@@ -358,8 +358,9 @@ pa_status paged_attn_forward_q8(const pa_plan *plan, const void *q, const uint8_
     if (pa::device_sms(sms) != cudaSuccess) sms = 0;
     if (plan->n_tiles == 0 && splits > 1 && sms > 0) {
         cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-        const bool captured = cudaStreamIsCapturing((cudaStream_t)stream, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone;
-        a.splits = pa::q8_splits(plan, x, sms, captured);
+        const bool asked = cudaStreamIsCapturing((cudaStream_t)stream, &capture) == cudaSuccess;
+        if (!asked) (void)cudaGetLastError();        // (the launch says what is wrong with the stream)
+        a.splits = pa::q8_splits(plan, x, sms, !asked || capture != cudaStreamCaptureStatusNone);
     }
     if (a.splits > 1) {
         a.ws_o = reinterpret_cast<float *>(base);

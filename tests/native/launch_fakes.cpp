@@ -18,6 +18,7 @@ struct Event {
 
 std::vector<Event> g_events;
 char g_fails[64] = "";
+cudaError_t g_last = cudaSuccess;
 int g_tensor_cores = 1;
 std::map<int64_t, int64_t> g_capture, g_event_capture;      // of a stream, of the last record of an event (0: none)
 int64_t g_handles = 0;
@@ -28,6 +29,7 @@ int64_t id(const void *p) { return (int64_t)reinterpret_cast<uintptr_t>(p); }
 cudaError_t note(const char *name, cudaStream_t st, int64_t a = 0, int64_t b = 0, int64_t c = 0, int64_t d = 0, const void *event = nullptr) {
     const bool fails = !std::strcmp(name, g_fails);
     if (!fails) g_events.push_back({name, id(st), id(event), {a, b, c, d}});
+    if (fails) g_last = cudaErrorInvalidValue;
     return fails ? cudaErrorInvalidValue : cudaSuccess;
 }
 
@@ -41,6 +43,7 @@ void fake_reset(const char *fails, int tensor_cores) {
     g_event_capture.clear();
     std::strncpy(g_fails, fails, sizeof g_fails - 1);
     g_tensor_cores = tensor_cores;
+    g_last = cudaSuccess;
 }
 void fake_capture(int64_t stream, int64_t capture) { g_capture[stream] = capture; }
 int fake_events() { return (int)g_events.size(); }
@@ -55,7 +58,10 @@ const char *fake_event(int i, int64_t *stream, int64_t *event, int64_t *value) {
 cudaError_t cudaGetDevice(int *dev) { return *dev = 0, cudaSuccess; }
 cudaError_t cudaDeviceGetAttribute(int *value, cudaDeviceAttr, int) { return *value = 152, cudaSuccess; }
 const char *cudaGetErrorString(cudaError_t) { return "a fake's error"; }
-cudaError_t cudaGetLastError() { return cudaSuccess; }
+cudaError_t cudaGetLastError() {
+    const cudaError_t e = g_last;
+    return g_last = cudaSuccess, e;
+}
 cudaError_t cudaMemcpyAsync(void *, const void *, size_t, cudaMemcpyKind, cudaStream_t st) { return note("copy", st); }
 cudaError_t cudaPointerGetAttributes(cudaPointerAttributes *at, const void *) {
     std::memset(at, 0, sizeof *at);
@@ -71,6 +77,7 @@ cudaError_t cudaEventCreateWithFlags(cudaEvent_t *ev, unsigned) {
 cudaError_t cudaEventDestroy(cudaEvent_t) { return cudaSuccess; }
 cudaError_t cudaStreamDestroy(cudaStream_t) { return cudaSuccess; }
 cudaError_t cudaStreamIsCapturing(cudaStream_t st, cudaStreamCaptureStatus *s) {
+    if (!std::strcmp("is_capturing", g_fails)) return g_last = cudaErrorStreamCaptureImplicit;
     return *s = g_capture[id(st)] ? cudaStreamCaptureStatusActive : cudaStreamCaptureStatusNone, cudaSuccess;
 }
 cudaError_t cudaStreamGetCaptureInfo(cudaStream_t st, cudaStreamCaptureStatus *s, unsigned long long *capture, cudaGraph_t *,

@@ -74,3 +74,11 @@ def test_no_more_than_allowed(fakes):  # noqa: F811
         for splits in (1, 2, 5, 64):
             s, merged = taken(fakes, lens, queries, splits=splits)
             assert 1 <= s <= splits and merged == (s if s > 1 else None)
+
+
+def test_a_stream_that_cannot_be_asked(fakes):  # noqa: F811
+    """The legacy stream while another thread captures, say: taken for a captured one, and no error is left behind."""
+    plan = fakes.plan([200], [list(range(2048))], [(0, 199)], 16, 2048)
+    fakes.reset("is_capturing")
+    assert fakes.forward_q8(plan, 32, 8, splits=16) == 0
+    assert fakes.events()[0].splits > 8 and fakes.lib.cudaGetLastError() == 0
