@@ -514,8 +514,9 @@ size_t pa_q8_window_workspace_bytes(const pa_plan *plan, int32_t num_heads, int3
  * paged_attn_forward_split over the 8-bit cache:
  *   out[q, h, :] = sum_j softmax_j(scale * q[q,h,:] . K_j) V_j
  * with K_j and V_j what the stored rows stand for; q and out are of `dtype`.  Scores and
- * sums of decode items are fp32 sums of exact products; prefill tiles of 16-bit operands
- * see the rows as paged_kv_load_q8 gives them in `dtype`.  Heads of 64 are scored in pairs:
+ * sums of decode items are fp32 sums of exact products, their weights exact to 2^-10; prefill
+ * tiles of 16-bit operands see the rows as paged_kv_load_q8 gives them in `dtype` and round
+ * their weights to it, as paged_attn_forward's do.  Heads of 64 are scored in pairs:
  * NaN in a key of one KV head reaches its neighbour's outputs for the queries that see the
  * key.  Histories hold at most 2^30 keys (PA_ERR_LIMIT).  splits in 1..PA_MAX_SPLITS: a
  * query's keys are attended in at most that many parts (a plan without prefill tiles in as
