@@ -397,9 +397,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
                 const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * tp.scale_log2;
                 float alpha = 1.f;
-                if (mt > m_ref + kSlack) {
-                    alpha = exp2f(m_ref - mt);          // 0 while this copy had seen no key
-                    m_ref = mt;
+                if (mt > m_ref + (kTop<T> + kSlack)) {
+                    alpha = exp2f(m_ref - (mt - kTop<T>));          // 0 while this copy had seen no key
+                    m_ref = mt - kTop<T>;
                 }
                 // rescaling O needs the previous P.V finished (rare: the row max moved by > 2^8)
                 if (kt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {

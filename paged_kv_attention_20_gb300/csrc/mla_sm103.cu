@@ -352,9 +352,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             const float mt = fmaxf(ma, mb) * prm.scale_log2;   // the scale is positive
             float alpha = 1.f;
-            if (mt > m_ref + kSlack) {
-                alpha = exp2f(m_ref - mt);
-                m_ref = mt;
+            if (mt > m_ref + (kTop<T> + kSlack)) {
+                alpha = exp2f(m_ref - (mt - kTop<T>));
+                m_ref = mt - kTop<T>;
             }
             // rescaling O needs the previous P.V finished (rare: the row max moved by > 2^8)
             if (kt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {

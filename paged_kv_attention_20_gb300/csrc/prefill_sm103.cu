@@ -38,7 +38,7 @@
 // only some of a tile's queries see reaches those alone (second pass, below).
 // The online softmax keeps a
 // per-row reference maximum that only moves when a tile's maximum exceeds it
-// by more than 8 (log2 units), so O in TMEM is rarely rescaled.
+// by more than 8 (log2 units; fp16 weights reach 2^15), so O in TMEM is rarely rescaled.
 // Every wait is bounded; a timeout sets the library's device status word and
 // the CTA stops issuing work.
 
@@ -561,9 +561,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 const float mt = fmaxf(mine, other);
                 float alpha = 1.f;
-                if (mt > m_ref + kSlack) {
-                    alpha = exp2f(m_ref - mt);
-                    m_ref = mt;
+                if (mt > m_ref + (kTop<T> + kSlack)) {
+                    alpha = exp2f(m_ref - (mt - kTop<T>));
+                    m_ref = mt - kTop<T>;
                 }
                 // rescaling O needs the previous P.V finished (rare: the row max moved by > 2^8)
                 if (kt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {

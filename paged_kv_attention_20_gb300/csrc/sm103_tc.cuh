@@ -5,10 +5,20 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cstdint>
 
 namespace pa {
 namespace tc {
+
+// Softmax weights go to the tensor core as 16-bit numbers 2^(s - ref), and a row's reference moves
+// only when a score passes it by so much that a weight would exceed 2^(kTop + 8).  A fresh reference
+// gives the largest score a weight of 2^kTop: in fp16, whose numbers lose bits below 2^-14 and end at
+// 2^-24 and 2^16, weights down to 2^-21 of the largest are exact to 2^-11 then, and a long tail of
+// smaller ones does not vanish (with kTop 0, 2^-14: 3000 weights of 2^-20.6 came out 3 % off).  bf16
+// has fp32's range.
+template <typename T> constexpr float kTop = 0.f;
+template <> constexpr float kTop<__half> = 7.f;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
