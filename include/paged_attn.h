@@ -522,11 +522,11 @@ size_t pa_q8_window_workspace_bytes(const pa_plan *plan, int32_t num_heads, int3
  * query's keys are attended in at most that many parts (a plan without prefill tiles in as
  * many of them as end soonest for the host copy's lengths, and a captured call, whose replays
  * may see others, for histories that fill their block-table rows); workspace: at least
- * pa_q8_workspace_bytes (under a window pa_q8_window_workspace_bytes), 16-byte aligned, not shared by calls that may overlap; what it has
- * beyond the need makes more room for the tiles' histories.  Tiles whose histories do not
- * fit on a replay leave their outputs undefined and set PA_DEVICE_RANGE.  A captured call
- * stays valid for plan images with the same counts.  Other arguments, shapes and checks as
- * paged_attn_forward.
+ * pa_q8_workspace_bytes (under a window pa_q8_window_workspace_bytes), 16-byte aligned, not
+ * shared by calls that may overlap; what it has beyond the need makes more room for the
+ * tiles' histories.  Tiles whose histories do not fit on a replay leave their outputs
+ * undefined and set PA_DEVICE_RANGE.  A captured call stays valid for plan images with the
+ * same counts.  Other arguments, shapes and checks as paged_attn_forward.
  */
 pa_status paged_attn_forward_q8(const pa_plan *plan, const void *q, const uint8_t *k_cache, const uint8_t *v_cache,
                                 const uint8_t *k_scale, const uint8_t *v_scale, void *out, int32_t num_heads,
